@@ -331,6 +331,63 @@ PKV_API pkv_status pkv_paged_attention_verify(void* out, const void* q, const vo
                                       int partition_tokens, void* stream);
 
 /*
+ * paged_attention_prefill -- the attention of a step's new tokens over the
+ * paged cache: prompts, chunks of a prompt over what is already cached, and
+ * running sequences that add one token, in one ragged batch.
+ *
+ * P3 §四 (chunked prefill beside decode); P1 §4.2.2 (a prompt's K/V fill its
+ * blocks).  Sequence s has n_s = query_starts[s+1] - query_starts[s] new
+ * tokens, whose K and V are already in its blocks as its last n_s positions
+ * (pkv_paged_kv_append first).  New token i attends over positions
+ * t < seq_lens[s] - n_s + i + 1:
+ *     z_t = scale * <q[r][h], K_t>,  out[r][h] = sum_t softmax(z)_t * V_t,
+ * r = query_starts[s] + i, K and V those of KV head h / (num_heads /
+ * num_kv_heads).  A token that sees no position gets zeros.  Accumulation and
+ * softmax statistics are fp32; the weights are rounded to `dt` for the product
+ * with V, `out` is rounded to nearest even.  What the cache holds at positions
+ * that a token does not see (infinities and NaN too) does not reach its
+ * output.
+ *
+ *   out, q        [num_tokens][num_heads][head_dim], dtype `dt`; rows that no
+ *                 sequence owns are neither read nor written
+ *   seq_lens      int32 [num_seqs]: positions cached, the new tokens among
+ *                 them, each in [0, max_seq_len] (a larger length is treated as
+ *                 max_seq_len and raises the error word's bounds bit)
+ *   query_starts  int32 [num_seqs + 1], not decreasing, in [0, num_tokens] (a
+ *                 sequence whose pair is not is skipped and raises the bounds
+ *                 bit); equal neighbours are a sequence with no new token
+ *   workspace     device scratch of pkv_prefill_workspace_bytes(...) bytes,
+ *                 16-byte aligned, contents on entry ignored; calls that share
+ *                 one must be ordered on one stream
+ *   planned       0: plan and run; PKV_PLANNED: run over the plan that
+ *                 pkv_prefill_plan wrote into `workspace` (once per step, for
+ *                 every layer): the same seq_lens and query_starts contents
+ *                 and the same num_seqs, num_tokens, max_seq_len, num_heads,
+ *                 num_kv_heads and head_dim (not checked on the host; a plan
+ *                 that does not fit the arguments gives undefined outputs and
+ *                 raises the bounds bit, but never leaves the buffers)
+ *   block_tables, max_blocks_per_seq, max_seq_len, block_size, num_blocks and
+ *   the pools as for pkv_paged_attention_decode
+ * head_dim in {64, 128}; block_size in {8, 16, 32}; num_heads a multiple of
+ * num_kv_heads; num_tokens * (num_heads / num_kv_heads) below 2^30.
+ * num_seqs == 0 or num_tokens == 0 is a no-op.
+ */
+PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads,
+                                   int head_dim);
+
+PKV_API pkv_status pkv_prefill_plan(const int32_t* seq_lens, const int32_t* query_starts, int num_seqs,
+                            int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+PKV_API pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* key_cache,
+                                       const void* value_cache, const int32_t* block_tables,
+                                       int max_blocks_per_seq, const int32_t* seq_lens,
+                                       const int32_t* query_starts, int num_seqs, int64_t num_tokens,
+                                       int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                                       int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
+                                       void* workspace, size_t workspace_bytes, int planned, void* stream);
+
+/*
  * 8-bit KV cache (E4M3) -- P3 §6.2 (KV cache quantization: attention reads
  * low-precision K/V, saving memory and bandwidth with little accuracy loss).
  * The page names no format; these calls use OCP FP8 E4M3 codes (1 sign, 4

@@ -37,7 +37,8 @@ ABI_SYMBOLS = ("pkv_version", "pkv_last_error", "pkv_paged_kv_append", "pkv_deco
                "pkv_bm_free", "pkv_bm_append_slots", "pkv_bm_block_tables", "pkv_paged_kv_append_fp8",
                "pkv_paged_attention_decode_fp8", "pkv_decode_plan", "pkv_paged_attention_decode_planned",
                "pkv_paged_attention_decode_fp8_planned", "pkv_paged_kv_append_decode",
-               "pkv_paged_attention_verify_fp8")
+               "pkv_paged_attention_verify_fp8", "pkv_prefill_workspace_bytes", "pkv_prefill_plan",
+               "pkv_paged_attention_prefill")
 
 _lib = None
 
@@ -95,6 +96,13 @@ def load() -> ctypes.CDLL:
                                                c_i, c_i, c_i, c_i64, c_f, c_i, c_i, c_p, c_p, c_p, c_sz, c_i, c_i, c_p]
     lib.pkv_decode_plan.restype = c_i
     lib.pkv_decode_plan.argtypes = [c_p, c_i, c_p, c_i, c_i, c_i64, c_i, c_i, c_i, c_i, c_i, c_p, c_sz, c_i, c_p]
+    lib.pkv_prefill_workspace_bytes.restype = c_sz
+    lib.pkv_prefill_workspace_bytes.argtypes = [c_i, c_i64, c_i, c_i, c_i]
+    lib.pkv_prefill_plan.restype = c_i
+    lib.pkv_prefill_plan.argtypes = [c_p, c_p, c_i, c_i64, c_i, c_i, c_i, c_i, c_p, c_sz, c_p]
+    lib.pkv_paged_attention_prefill.restype = c_i
+    lib.pkv_paged_attention_prefill.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i, c_p, c_p, c_i, c_i64, c_i, c_i, c_i, c_i,
+                                                c_i, c_i64, c_f, c_i, c_p, c_sz, c_i, c_p]
     lib.pkv_copy_blocks.restype = c_i
     lib.pkv_copy_blocks.argtypes = [ctypes.POINTER(c_p), ctypes.POINTER(c_p), c_i, c_p, c_i64, c_i64, c_i, c_i,
                                     c_i, c_i, c_p]
@@ -425,6 +433,69 @@ def paged_attention_verify(out, q, key_cache, value_cache, block_tables, seq_len
         _check(load().pkv_paged_attention_verify(
             *ptrs, block_tables.shape[1], *lens_arg, Hq, Hkv, d, bs, NB, float(scale), _DT[key_cache.dtype], nq,
             ws_ptr, ws_bytes, int(partition_tokens), _stream(q)))
+
+
+def prefill_workspace_bytes(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim) -> int:
+    n = load().pkv_prefill_workspace_bytes(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid prefill shape")
+    return int(n)
+
+
+def alloc_prefill_workspace(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, device="cuda"):
+    """A device buffer of the size the prefill call needs (for this many new tokens in all)."""
+    n = prefill_workspace_bytes(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+@_one_device
+def prefill_plan(workspace, seq_lens, query_starts, num_tokens, num_heads, num_kv_heads, head_dim,
+                 max_seq_len) -> None:
+    """The work list of a prefill batch, once per step (``pkv_prefill_plan``): the layers that pass
+    ``planned=True`` with the same batch and workspace then skip the plan kernel."""
+    B = seq_lens.shape[0]
+    args = [_cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("query_starts", query_starts, torch.int32, 1)]
+    if query_starts.shape[0] != B + 1:
+        raise ValueError("query_starts must have num_seqs + 1 entries")
+    _check(load().pkv_prefill_plan(*args, B, int(num_tokens), int(max_seq_len), num_heads, num_kv_heads, head_dim,
+                                   _cuda("workspace", workspace), workspace.numel() * workspace.element_size(),
+                                   _stream(workspace)))
+
+
+@_one_device
+def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, scale=None,
+                            max_seq_len=None, workspace=None, planned=False) -> None:
+    """Attention of a ragged batch of new tokens over the paged cache.  q, out: [T, Hq, d]; sequence s owns rows
+    query_starts[s] .. query_starts[s + 1] - 1 (int32 [B + 1]), whose K/V are its last positions in the pools; row i
+    of n attends over positions [0, seq_lens[s] - n + i].  Rows of no sequence are left as they are.  ``workspace``:
+    see ``alloc_prefill_workspace`` (allocated here when omitted); ``planned``: run over the list ``prefill_plan``
+    put there for this batch.  ``max_seq_len`` is read from the device if omitted, which synchronises."""
+    NB, bs, Hkv, d = _pool("key_cache", key_cache)
+    if value_cache.shape != key_cache.shape or value_cache.dtype != key_cache.dtype:
+        raise ValueError("value_cache must match key_cache")
+    if q.dim() != 3:
+        raise ValueError("q must be [num_tokens, num_heads, head_dim]")
+    T, Hq, dq = q.shape
+    if dq != d or tuple(out.shape) != (T, Hq, d):
+        raise ValueError("q and out must be [num_tokens, num_heads, head_dim]")
+    B = seq_lens.shape[0]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    ptrs = [_cuda("out", out, key_cache.dtype), _cuda("q", q, key_cache.dtype), _cuda("key_cache", key_cache),
+            _cuda("value_cache", value_cache), _cuda("block_tables", block_tables, torch.int32, 2)]
+    lens = [_cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("query_starts", query_starts, torch.int32, 1)]
+    if block_tables.shape[0] != B or query_starts.shape[0] != B + 1:
+        raise ValueError("block_tables must have num_seqs rows and query_starts num_seqs + 1 entries")
+    if planned and workspace is None:
+        raise ValueError("planned=True needs the workspace that prefill_plan wrote")
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    if workspace is None:
+        workspace = alloc_prefill_workspace(B, T, Hq, Hkv, d, q.device)
+    _check(load().pkv_paged_attention_prefill(
+        *ptrs, block_tables.shape[1], *lens, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB, float(scale),
+        _DT[key_cache.dtype], _cuda("workspace", workspace), workspace.numel() * workspace.element_size(),
+        PLANNED if planned else 0, _stream(q)))
 
 
 @_one_device

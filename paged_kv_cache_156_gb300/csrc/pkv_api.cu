@@ -610,6 +610,135 @@ pkv_status pkv_paged_kv_append_fp8(const void* k, const void* v, void* key_cache
 
 namespace {
 
+// Prefill: what the plan and the run check alike.  Fills the layout and the plan's arguments.
+pkv_status prefill_args(pkv::PrefillArgs& a, pkv::PrefillWorkspace& lay, const int32_t* seq_lens,
+                        const int32_t* query_starts, int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads,
+                        int num_kv_heads, int head_dim, void* workspace, size_t workspace_bytes) {
+    pkv_status st = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len);
+    if (st != PKV_OK) return st;
+    const int group = num_heads / num_kv_heads;
+    if (num_tokens < 0 || num_tokens * group >= (int64_t(1) << 30))
+        return fail(PKV_ERR_INVALID, "num_tokens %lld: at least 0, num_tokens * (num_heads / num_kv_heads) below 2^30",
+                    static_cast<long long>(num_tokens));
+    if (num_seqs == 0 || num_tokens == 0) return ok();
+    if (!seq_lens || !query_starts) return fail(PKV_ERR_INVALID, "null pointer");
+    if ((reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(query_starts) & 3u))
+        return fail(PKV_ERR_INVALID, "lengths and query starts must be 4-byte aligned");
+    const int dev = current_device();
+    const int sms = sm_count_of(dev) > 0 ? sm_count_of(dev) : 152;
+    lay = pkv::prefill_workspace_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, sms);
+    if (static_cast<int64_t>(lay.capacity) * num_kv_heads >= (int64_t(1) << 31))
+        return fail(PKV_ERR_UNSUPPORTED, "too many work items");
+    if (!workspace || workspace_bytes < lay.total || !aligned16(workspace))
+        return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned), got %zu", lay.total,
+                    workspace ? workspace_bytes : size_t(0));
+    a = pkv::PrefillArgs{};
+    char* ws = static_cast<char*>(workspace);
+    a.seq_lens = seq_lens;
+    a.query_starts = query_starts;
+    a.header = reinterpret_cast<int*>(ws);
+    a.items = reinterpret_cast<int4*>(ws + lay.items);
+    a.tickets = reinterpret_cast<unsigned*>(ws + lay.tickets);
+    a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+    a.part_o = reinterpret_cast<float*>(ws + lay.o);
+    a.num_tokens = num_tokens;
+    a.num_seqs = num_seqs;
+    a.max_seq_len = max_seq_len;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = group;
+    a.capacity = lay.capacity;
+    a.part_cap = lay.part_cap;
+    a.part_rows = lay.part_rows;
+    a.slots = sms;
+    return ok();
+}
+
+pkv_status prefill_call(void* out, const void* q, const void* key_cache, const void* value_cache,
+                        const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* query_starts, int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads,
+                        int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
+                        void* workspace, size_t workspace_bytes, int planned, void* stream) {
+    if (planned != 0 && planned != PKV_PLANNED) return fail(PKV_ERR_INVALID, "planned %d: 0 or PKV_PLANNED", planned);
+    if (!valid_dtype(dt)) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", static_cast<int>(dt));
+    if (!valid_block_size(block_size)) return fail(PKV_ERR_UNSUPPORTED, "block_size %d not built (8, 16, 32)", block_size);
+    if (num_blocks <= 0 || num_blocks > (int64_t(1) << 31))
+        return fail(PKV_ERR_INVALID, "num_blocks %lld outside [1, 2^31]", static_cast<long long>(num_blocks));
+    if (max_blocks_per_seq < 0 || static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
+        return fail(PKV_ERR_INVALID, "max_seq_len %d exceeds max_blocks_per_seq %d * block_size %d", max_seq_len,
+                    max_blocks_per_seq, block_size);
+    if (!isfinite(scale)) return fail(PKV_ERR_INVALID, "scale is not finite");
+    pkv::PrefillArgs a{};
+    pkv::PrefillWorkspace lay{};
+    pkv_status st = prefill_args(a, lay, seq_lens, query_starts, num_seqs, num_tokens, max_seq_len, num_heads,
+                                 num_kv_heads, head_dim, workspace, workspace_bytes);
+    if (st != PKV_OK || num_seqs == 0 || num_tokens == 0) return st;
+    if (!out || !q || !key_cache || !value_cache || !block_tables) return fail(PKV_ERR_INVALID, "null pointer");
+    if (reinterpret_cast<uintptr_t>(block_tables) & 3u) return fail(PKV_ERR_INVALID, "tables must be 4-byte aligned");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache))
+        return fail(PKV_ERR_INVALID, "out, q and caches must be 16-byte aligned");
+    a.out = out;
+    a.q = q;
+    a.block_tables = block_tables;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.err = error_word(current_device());
+    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    a.negate_q = scale < 0.0f;
+    CUtensorMap tmk{}, tmv{};
+    if ((st = encode_pool(&tmk, key_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return st;
+    if ((st = encode_pool(&tmv, value_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = planned ? cudaSuccess : pkv::launch_prefill_plan(a, s);
+    if (e == cudaSuccess) e = pkv::launch_prefill(a, tmk, tmv, dt == PKV_F16 ? 0 : 1, head_dim, s);
+    if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_prefill_workspace_bytes(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads, int head_dim) {
+    if (check_decode_shape(num_seqs, num_heads, num_kv_heads, head_dim, 0) != PKV_OK || num_tokens < 0 ||
+        num_tokens * (num_heads / num_kv_heads) >= (int64_t(1) << 30))
+        return (size_t)-1;
+    const int sms = sm_count_of(current_device());
+    return pkv::prefill_workspace_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, sms > 0 ? sms : 152).total;
+}
+
+pkv_status pkv_prefill_plan(const int32_t* seq_lens, const int32_t* query_starts, int num_seqs, int64_t num_tokens,
+                            int max_seq_len, int num_heads, int num_kv_heads, int head_dim, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    CallRange range_("pkv_prefill_plan");
+    pkv::PrefillArgs a{};
+    pkv::PrefillWorkspace lay{};
+    pkv_status st = prefill_args(a, lay, seq_lens, query_starts, num_seqs, num_tokens, max_seq_len, num_heads,
+                                 num_kv_heads, head_dim, workspace, workspace_bytes);
+    if (st != PKV_OK || num_seqs == 0 || num_tokens == 0) return st;
+    a.err = error_word(current_device());
+    cudaError_t e = pkv::launch_prefill_plan(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "prefill plan launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* key_cache, const void* value_cache,
+                                       const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                       const int32_t* query_starts, int num_seqs, int64_t num_tokens, int max_seq_len,
+                                       int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                       int64_t num_blocks, float scale, pkv_dtype dt, void* workspace,
+                                       size_t workspace_bytes, int planned, void* stream) {
+    CallRange range_("pkv_paged_attention_prefill");
+    return prefill_call(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, query_starts,
+                        num_seqs, num_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                        scale, dt, workspace, workspace_bytes, planned, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
 // Shared by copy_blocks (one pool) and swap_blocks (two pools).
 pkv_status block_copies(void* const* src_key, void* const* src_value, void* const* dst_key, void* const* dst_value,
                         int num_layers, const int64_t* src_dst_pairs, int64_t num_pairs, int64_t src_num_blocks,

@@ -201,6 +201,61 @@ int verify_tc_ctas_per_sm(int head_dim);
 // configuration; kv8: the E4M3-pool kernel), or 0 if it cannot be queried.
 int decode_ctas_per_sm(int head_dim, bool kv8 = false);
 
+// ---------------------------------------------------------------- prefill (csrc/pkv_prefill.cu, pkv_prefill_plan.cu)
+// A work item is kPrefillRows query rows of one KV head of one sequence over a run of
+// kPrefillStep-position steps.  Row r of sequence s, KV head g is token r / group, query
+// head g * group + r % group.
+constexpr int kPrefillRows = 256;
+constexpr int kPrefillSub = 128;                // rows of one of an item's two tiles (the MMA's M)
+constexpr int kPrefillStep = 128;
+constexpr int kPrefillMaxParts = 152;           // parts one tile's positions are split into at most
+
+struct PrefillArgs {
+    void* out;                       // [num_tokens][num_heads][D]
+    const void* q;
+    const int32_t* block_tables;     // [B][max_blocks_per_seq]
+    const int32_t* seq_lens;         // [B]
+    const int32_t* query_starts;     // [B + 1]
+    int* header;                     // [0] number of work items
+    int4* items;                     // [capacity][2]: (sequence, tile, first step, end step),
+                                     // (first query row of q, tokens, length, split: 0, or see prefill_split)
+    unsigned* tickets;               // [num_kv_heads][part_cap][2] parts finished of a split tile's two sub-tiles
+    float2* part_ml;                 // [num_kv_heads][part_cap][part_rows] (reference maximum in log2 units, sum)
+    float* part_o;                   // [num_kv_heads][part_cap][part_rows][D] unnormalised partial outputs
+    unsigned* err;
+    int64_t num_blocks;
+    int64_t num_tokens;
+    int max_blocks_per_seq;
+    int num_seqs;
+    int max_seq_len;
+    int num_heads;
+    int num_kv_heads;
+    int group;                       // num_heads / num_kv_heads
+    int block_size;
+    int capacity;                    // entries of `items`
+    int part_cap;                    // partial slots per KV head
+    int part_rows;                   // rows of a partial slot: min(256, num_tokens * group)
+    int slots;                       // CTAs the grid may hold at once
+    float scale_log2;                // |scale| * log2(e)
+    int negate_q;                    // scale < 0: q's signs are flipped as it is loaded
+    const float* k_scale;            // [num_kv_heads] (E4M3 pools only, else nullptr)
+    const float* v_scale;
+};
+
+// A split tile's item: parts, this part, first partial slot.
+__host__ __device__ inline int prefill_split(int nparts, int part, int base) { return base << 16 | part << 8 | nparts; }
+
+// Workspace: [header | items | tickets | (max, sum) pairs | partial outputs], each 256-byte aligned.
+struct PrefillWorkspace {
+    size_t items, tickets, ml, o, total;           // offsets and size
+    int capacity, part_cap, part_rows;
+};
+PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads,
+                                          int head_dim, int slots);
+cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype, int head_dim,
+                           cudaStream_t s);
+
 // Record `msg` as the calling thread's pkv_last_error() message and return `st`.
 int set_error_message(int st, const char* msg);
 

@@ -1,0 +1,752 @@
+// paged_attention_prefill: the attention of a ragged batch of new tokens over
+// the paged cache, on the fifth-generation tensor cores (tcgen05).
+//
+// What is computed.  Sequence s has L_s cached positions, the last n_s of them
+// its new tokens' own; new token i attends over positions t < L_s - n_s + i + 1:
+//     out = sum_t p_t V_t,   p = softmax(scale * q . K_t).
+// Rows are (token, query head) pairs of one KV head, token-major, so a KV
+// head's whole group shares every K/V byte that reaches the SM.
+//
+// How.  A work item is 256 rows (two tiles of 128, the MMA's M) over a run of
+// 128-position steps; the plan kernel lists the items, longest first, and one
+// persistent CTA per SM takes them round robin.  Per step and tile i
+//     S_i = Q_i K^T    tcgen05.mma 128 x 128, Q_i and K from shared memory, S_i
+//                      fp32 in tensor memory (TMEM)
+//     P_i = 2^(S_i - ref)   one thread a row; the reference maximum moves only
+//                      when a score passes it by more than 2^8 (O_i is then
+//                      rescaled in TMEM); P_i, rounded to the input type (the
+//                      MMA's operand type), takes S_i's place in TMEM; the row
+//                      sum stays fp32 and sums the weights before rounding
+//     O_i += P_i V     tcgen05.mma, A from TMEM, V from shared memory read as an
+//                      MN-major operand, O_i fp32 in TMEM
+// The two tiles are a step's ping and pong: while one tile's softmax runs, the
+// tensor cores work on the other's products.  TMEM is full: S_0 S_1 O_0 O_1 of
+// 128 columns each.
+//
+// Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (they also load Q, write the
+// output and merge split tiles), 8 streams the K/V blocks (TMA, one box per
+// block and 128-byte column plane, its lanes side by side), 9 issues every MMA
+// (its program order is what orders S_i after the O_i that reads P_i), 10 and
+// 11 clean V tiles.
+//
+// Masked positions.  A masked score is replaced before the maximum, whatever K
+// holds there.  A masked position's weight is 0, but 0 * V is NaN where V is
+// not finite, so on the steps that some row sees only in part, and on a
+// sequence's last, two warps look through the V rows that not every row sees:
+// slots past the end become zeros, non-finite elements too, after their first
+// position per column is noted; the epilogue then gives inf or NaN to exactly
+// the rows that see them.
+//
+// Every wait is bounded in wall time; a CTA that gives up raises the error
+// word, gives its copies and products in flight time to land and frees its TMEM.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "pkv_decode_common.cuh"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kStep = kPrefillStep;
+constexpr int kSub = kPrefillSub;
+
+template <int D>
+struct PfGeo {
+    static constexpr int kThreads = 384;
+    static constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10, kFixWarps = 2;
+    static constexpr int kHalves = D * 2 / 128;             // 128-byte column planes of a tile
+    static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
+    static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
+    static constexpr int kStages = D == 128 ? 5 : 10;       // ring of K and V tiles, in turn
+    static constexpr size_t kRing = 2 * size_t(kTile);      // after the two Q tiles
+    static constexpr size_t kBars = kRing + size_t(kStages) * kTile;
+    static constexpr int kNumBars = 2 * kStages + 11;
+    static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, epilogue count, tags
+    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // [2 warps][+inf, -inf][D] first positions
+    static constexpr size_t kBytes = kBad + size_t(kFixWarps) * 2 * D * 4;
+    static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+    // registers a thread: 384 threads start with 168; the softmax warpgroups take 208, the third keeps 88
+    static constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+    static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "the split fits the launch's registers");
+    static_assert(kBytes <= 232448, "fits one SM");
+};
+
+// One work item as every role sees it (all derive it from the same plan entry).
+struct Item {
+    int s, kvh, tile, step0, step1, qs, n, L, split;
+    int rows;                        // query rows of the item (0: nothing to do)
+    int nst[2];                      // steps of each tile
+    int end[2];                      // position after the last one each tile sees in the item
+    int lim0;                        // positions every row of the item sees
+    __device__ __forceinline__ int steps() const { return max(nst[0], nst[1]); }
+    __device__ __forceinline__ int stop() const { return max(end[0], end[1]); }
+    // V rows [lo, nv16) of step j that not every row sees (nv: the item's positions in the step)
+    __device__ __forceinline__ void partial(int j, int& lo, int& nv, int& nv16) const {
+        const int tok0 = (step0 + j) * kStep;
+        nv = min(kStep, stop() - tok0);
+        nv16 = (nv + 15) & ~15;
+        lo = max(0, lim0 - tok0);
+    }
+};
+
+// (Plan, tables and q are read with ld.cg, never ld.nc: the compiler may move an ld.nc above the
+// wait for the kernel that writes them.)
+__device__ __forceinline__ bool load_item(const PrefillArgs& a, int total, int round, Item& it) {
+    const int g = gridDim.x, b = blockIdx.x;
+    const long long w = static_cast<long long>(round) * g + ((round & 1) ? g - 1 - b : b);
+    if (w >= total) return false;
+    const int e = static_cast<int>(w) / a.num_kv_heads;
+    it.kvh = static_cast<int>(w) - e * a.num_kv_heads;
+    const int4 x = __ldcg(a.items + 2 * e), y = __ldcg(a.items + 2 * e + 1);
+    it.s = x.x;
+    it.tile = x.y;
+    it.step0 = x.z;
+    it.step1 = x.w;
+    it.qs = y.x;
+    it.n = y.y;
+    it.L = y.z;
+    it.split = y.w;
+    it.rows = 0;
+    it.nst[0] = it.nst[1] = it.end[0] = it.end[1] = 0;
+    it.lim0 = 0;
+    const int nparts = it.split & 255, part = (it.split >> 8) & 255, base = it.split >> 16;
+    // a plan of other arguments: skip the entry rather than leave the buffers
+    if (it.s < 0 || it.s >= a.num_seqs || it.tile < 0 || it.step0 < 0 || it.step1 < it.step0 || it.qs < 0 || it.n <= 0 ||
+        it.qs + static_cast<long long>(it.n) > a.num_tokens || it.L < 0 || it.L > a.max_seq_len ||
+        static_cast<long long>(it.tile) * kPrefillRows >= static_cast<long long>(it.n) * a.group || it.split < 0 ||
+        (it.split != 0 && (part >= nparts || base + nparts > a.part_cap))) {
+        if (threadIdx.x == 0) raise_error(a.err, kErrBounds);
+        return true;
+    }
+    const int row0 = it.tile * kPrefillRows;
+    it.rows = min(kPrefillRows, it.n * a.group - row0);
+    const int past = it.L - it.n;
+    it.lim0 = max(0, past + row0 / a.group + 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = min(kSub, it.rows - i * kSub);
+        if (r > 0) {
+            const int lim = past + (row0 + i * kSub + r - 1) / a.group + 1;      // the tile's last row's
+            it.end[i] = max(0, min(it.step1 < (1 << 23) ? it.step1 * kStep : it.L, min(lim, it.L)));
+            it.nst[i] = max(0, (it.end[i] + kStep - 1) / kStep - it.step0);
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ uint64_t pack64(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack64(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Element offset / D of row r of the item's tile in q / out.
+__device__ __forceinline__ int64_t qo_row(const PrefillArgs& a, const Item& it, int r) {
+    const int rr = it.tile * kPrefillRows + r;
+    const int tok = rr / a.group;
+    return (static_cast<int64_t>(it.qs) + tok) * a.num_heads + it.kvh * a.group + (rr - tok * a.group);
+}
+
+// A warp's 32 rows of a Q tile into shared memory (128-byte swizzle, zeros past the rows).
+template <typename T, int D>
+__device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& it, int wg, uint32_t qtile) {
+    using G = PfGeo<D>;
+    constexpr int kCh = D / 8;                               // 16-byte chunks of a row
+    constexpr int kRowsAt = 32 / kCh;                        // rows a warp loads at once
+    const int lane = threadIdx.x & 31, w0 = ((threadIdx.x >> 5) & 3) * 32;
+    const int ch = lane % kCh, sub = lane / kCh;
+    const uint32_t keep = a.scale_log2 == 0.0f ? 0u : 0xffffffffu, flip = a.negate_q ? 0x80008000u : 0u;
+    constexpr int kBatch = 8;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += kRowsAt * kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = wg * kSub + w0 + r0 + u * kRowsAt + sub;
+            x[u] = r < it.rows ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qo_row(a, it, r) * D) + ch)
+                               : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = w0 + r0 + u * kRowsAt + sub;
+            const uint32_t addr = dec::swz(qtile + (ch >> 3) * G::kPlane, r, ch & 7);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"((x[u].x & keep) ^ flip),
+                         "r"((x[u].y & keep) ^ flip), "r"((x[u].z & keep) ^ flip), "r"((x[u].w & keep) ^ flip)
+                         : "memory");
+        }
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmk,
+                                                                        const __grid_constant__ CUtensorMap tmv,
+                                                                        const PrefillArgs a) {
+    using G = PfGeo<D>;
+    constexpr int ST = G::kStages;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* ring = smem + G::kRing;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kBars);
+    uint64_t* full = bars;                          // [ST] a tile landed (TMA bytes)
+    uint64_t* empty = bars + ST;                    // [ST] the products that read it are done (MMA commit)
+    uint64_t* q_full = bars + 2 * ST;               // [2] an item's Q tile is in shared memory (softmax threads)
+    uint64_t* s_full = q_full + 2;                  // [2] a step's S in TMEM, all earlier products done (MMA commit)
+    uint64_t* p_full = q_full + 4;                  // [2] a step's P in TMEM, O rescaled (softmax threads)
+    uint64_t* o_full = q_full + 6;                  // [2] an item's last O product done (MMA commit)
+    uint64_t* fix_req = q_full + 8;                 // a V tile landed that wants cleaning (MMA thread)
+    uint64_t* fix_done = q_full + 9;                // it is clean (both cleaning warps)
+    uint64_t* fin = q_full + 10;                    // every product issued is done (MMA commit)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kMisc + 4);
+    volatile int* epilogues = abort_flag + 1;       // epilogues finished, counted per softmax warp
+    volatile int* bad_tag = abort_flag + 2;         // [2] the item a cleaning warp noted bad elements of (-1: none)
+    volatile int* merge_flag = abort_flag + 4;      // [2]
+    int* bad = reinterpret_cast<int*>(smem + G::kBad);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], kSub);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], kSub);
+            mbar_init(&o_full[i], 1);
+            bad_tag[i] = -1;
+        }
+        mbar_init(fix_req, 1);
+        mbar_init(fix_done, G::kFixWarps);
+        mbar_init(fin, 1);
+        *epilogues = 0;
+        // the 128B swizzle and the MMA descriptors assume 1 KB aligned tiles
+        const bool misaligned = (smem_u32(smem) & 1023u) != 0;
+        if (misaligned) raise_error(a.err, kErrTimeout);
+        *abort_flag = misaligned;
+        fence_barrier_init();
+    }
+    if (warp == G::kMmaWarp) tc::tmem_alloc(tmem_slot, G::kTmemCols);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();
+    const int total = min(__ldcg(a.header), a.capacity) * a.num_kv_heads;
+
+    if (warp >= 8) {
+        regs_dec<G::kRegsOther>();
+        if (warp == G::kLoadWarp) {
+            // ======================================================== the K/V ring
+            const int bs = a.block_size;
+            const int boxes = kStep / bs * G::kHalves;       // TMA boxes of a full tile (at most 32: one a lane)
+            const int blk = lane / G::kHalves, hf = lane % G::kHalves;
+            unsigned c = 0;                                  // tiles streamed
+            Item it;
+            bool ok = !*abort_flag;
+            if (lane == 0) {
+                prefetch_tensormap(&tmk);
+                prefetch_tensormap(&tmv);
+            }
+            for (int r = 0; ok && load_item(a, total, r, it); ++r) {
+                const int n = it.steps(), stop = it.stop();
+                const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
+                auto id_of = [&](int j) {                    // this lane's block id in step j (-1: no block)
+                    const int pos = (it.step0 + j) * kStep + blk * bs;
+                    return lane < boxes && j < n && pos < stop ? __ldcg(trow + pos / bs) : -1;
+                };
+                int nxt = id_of(0);
+                for (int j = 0; j < n && ok; ++j) {
+                    int id = nxt;
+                    nxt = id_of(j + 1);
+                    const int tok0 = (it.step0 + j) * kStep;
+                    const int nb = (min(stop, tok0 + kStep) - tok0 + bs - 1) / bs;
+                    const bool mine = lane < boxes && blk < nb;
+                    if (mine && (id < 0 || static_cast<int64_t>(id) >= a.num_blocks)) {
+                        raise_error(a.err, kErrBounds);
+                        id = -1;                             // outside the tensor map: TMA fills zeros
+                    }
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const unsigned st = c % ST, ph = (c / ST) & 1;
+                        ok = dec::wait_or_abort(&empty[st], ph ^ 1, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<unsigned>(nb * bs * D * 2));
+                        __syncwarp();
+                        if (mine)
+                            tma_load_4d(ring + st * G::kTile + hf * G::kPlane + blk * bs * 128, kv == 0 ? &tmk : &tmv,
+                                        hf * 64, it.kvh, 0, id, &full[st]);
+                        ++c;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                dec::raise_abort(a.err, abort_flag);
+                const unsigned long long t0 = globaltimer_ns();       // copies in flight land before the CTA ends
+                while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
+            }
+        } else if (warp == G::kMmaWarp) {
+            // ======================================================== every MMA, one thread
+            if (lane == 0) {
+                constexpr uint32_t kIdS = tc::idesc_f16(kSub, kStep, kBf16, false);   // S = Q K^T
+                constexpr uint32_t kIdO = tc::idesc_f16(kSub, D, kBf16, true);        // O += P V
+                unsigned c = 0;                              // tiles of the ring seen by finished items
+                unsigned nq[2] = {0, 0}, np[2] = {0, 0}, nfix = 0;
+                Item it;
+                bool ok = !*abort_flag;
+                for (int r = 0; ok && load_item(a, total, r, it); ++r) {
+                    const int n = it.steps();
+                    if (n == 0) continue;
+                    auto wait_tile = [&](unsigned k) { return dec::wait_or_abort(&full[k % ST], (k / ST) & 1, abort_flag); };
+                    auto product_s = [&](int i, unsigned k) {
+                        const uint32_t qt = smem_u32(smem + i * G::kTile), kt = smem_u32(ring + (k % ST) * G::kTile);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t off = (ks >> 2) * G::kPlane + (ks & 3) * 32;
+                            tc::mma_ss(tmem + G::kColS + i * 128, tc::smem_desc_sw128(qt + off, 16, 1024),
+                                       tc::smem_desc_sw128(kt + off, 16, 1024), kIdS, ks > 0);
+                        }
+                        tc::commit(&s_full[i]);
+                    };
+                    ok = wait_tile(c);
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        if (it.nst[i] == 0) continue;
+                        ok = dec::wait_or_abort(&q_full[i], nq[i] & 1, abort_flag);
+                        ++nq[i];
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        product_s(i, c);
+                    }
+                    if (!ok) break;
+                    tc::commit(&empty[c % ST]);
+                    for (int j = 0; j < n && ok; ++j) {
+                        const unsigned kv = c + 2 * j + 1, kn = kv + 1;
+                        ok = wait_tile(kv);
+                        if (!ok) break;
+                        int lo, nv, nv16;
+                        it.partial(j, lo, nv, nv16);
+                        bool fix = lo < nv16;
+                        if (fix) mbar_arrive(fix_req);
+                        bool k_here = false;
+                        for (int i = 0; i < 2 && ok; ++i) {
+                            if (j < it.nst[i]) {
+                                ok = dec::wait_or_abort(&p_full[i], np[i] & 1, abort_flag);
+                                ++np[i];
+                                if (ok && fix) {
+                                    ok = dec::wait_or_abort(fix_done, nfix & 1, abort_flag);
+                                    ++nfix;
+                                    fix = false;
+                                }
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                                const uint32_t vt = smem_u32(ring + (kv % ST) * G::kTile);
+                                const int nk = (min(kStep, it.end[i] - (it.step0 + j) * kStep) + 15) / 16;
+#pragma unroll
+                                for (int kk = 0; kk < kStep / 16; ++kk) {
+                                    if (kk >= nk) break;
+                                    tc::mma_ts(tmem + G::kColO + i * 128, tmem + G::kColS + i * 128 + kk * 8,
+                                               tc::smem_desc_sw128(vt + kk * 2048, G::kPlane, 1024), kIdO,
+                                               (j > 0 || kk > 0) ? 1u : 0u);
+                                }
+                                if (j == it.nst[i] - 1) tc::commit(&o_full[i]);
+                            }
+                            if (i == 1) tc::commit(&empty[kv % ST]);
+                            if (j + 1 < it.nst[i]) {
+                                if (!k_here) ok = wait_tile(kn);
+                                if (!ok) break;
+                                k_here = true;
+                                product_s(i, kn);
+                            }
+                        }
+                        if (ok && j + 1 < n) tc::commit(&empty[kn % ST]);
+                    }
+                    c += 2 * n;
+                }
+                if (!ok) dec::raise_abort(a.err, abort_flag);
+                tc::commit(fin);
+                dec::wait_or_abort(fin, 0, abort_flag);
+                if (*abort_flag) {                           // (an abort may leave MMAs running: give them a moment)
+                    const unsigned long long t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ======================================================== V tiles that some row sees only in part
+            const int fw = warp - G::kFixWarp;
+            constexpr int kCh = D / 8;
+            constexpr uint32_t kCarry = kBf16 ? 0x00800080u : 0x04000400u;   // exponent all ones -> bit 15
+            int* bad_pos = bad + fw * 2 * D;                 // [+inf or NaN | -inf or NaN][D] first positions
+            unsigned c = 0, nreq = 0;
+            Item it;
+            bool ok = !*abort_flag;
+            for (int r = 0; ok && load_item(a, total, r, it); ++r) {
+                const int n = it.steps();
+                for (int j = 0; j < n && ok; ++j) {
+                    int lo, nv, nv16;
+                    it.partial(j, lo, nv, nv16);
+                    if (lo >= nv16) continue;
+                    ok = dec::wait_or_abort(fix_req, nreq & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ++nreq;
+                    if (!ok) break;
+                    const uint32_t vt = smem_u32(ring + ((c + 2 * j + 1) % ST) * G::kTile);
+                    const int tok0 = (it.step0 + j) * kStep;
+                    for (int i0 = lo * kCh + fw * 32; i0 < nv16 * kCh; i0 += 32 * G::kFixWarps) {   // (warp-uniform)
+                        const int i = i0 + lane, row = i / kCh, ch = i % kCh;
+                        const uint32_t addr = dec::swz(vt + (ch >> 3) * G::kPlane, row, ch & 7);
+                        uint32_t x[4] = {0u, 0u, 0u, 0u};
+                        if (row < nv)
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                         : "r"(addr));
+                        uint32_t hit = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) hit |= ((x[e] & 0x7fff7fffu) + kCarry) & 0x80008000u;
+                        if (__any_sync(0xffffffffu, hit != 0)) {             // rare
+                            if (bad_tag[fw] != r) {          // (warp-uniform: this warp alone writes it)
+                                // the softmax warps read the table in their epilogues: those of earlier items first
+                                const unsigned long long t0 = globaltimer_ns();
+                                while (*epilogues < 8 * r && !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
+                                for (int k = lane; k < 2 * D; k += 32) bad_pos[k] = 0x7fffffff;
+                                __syncwarp();
+                                if (lane == 0) bad_tag[fw] = r;
+                                __syncwarp();
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                                if ((((h & 0x7fffu) + (kCarry & 0xffffu)) & 0x8000u) == 0) continue;
+                                const bool nan = (h & 0x7fffu) != (0x8000u - (kCarry & 0xffffu));
+                                if (nan || h < 0x8000u) atomicMin(&bad_pos[8 * ch + e], tok0 + row);
+                                if (nan || h >= 0x8000u) atomicMin(&bad_pos[D + 8 * ch + e], tok0 + row);
+                                x[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+                            }
+                        }
+                        if (hit != 0 || (row >= nv && row < nv16))
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]),
+                                         "r"(x[2]), "r"(x[3])
+                                         : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(fix_done);
+                }
+                c += 2 * n;
+            }
+            if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
+        }
+    } else {
+        // ============================================================ softmax: one row a thread
+        regs_inc<G::kRegsSoftmax>();
+        const int wg = warp >> 2;
+        const int t = threadIdx.x & 127;
+        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t ts = tl + G::kColS + wg * 128, to = tl + G::kColO + wg * 128;
+        const uint32_t qtile = smem_u32(smem + wg * G::kTile);
+        const float sl2 = a.scale_log2 == 0.0f ? 1.0f : a.scale_log2;   // (scale 0: q was zeroed)
+        const uint64_t sl2x2 = pack64(sl2, sl2);
+        T* out = static_cast<T*>(a.out);
+        unsigned ns = 0, no = 0;
+        Item it, next;
+        bool ok = !*abort_flag;
+        bool more = load_item(a, total, 0, it);
+        auto fetch_q = [&](const Item& x) {
+            if (x.nst[wg] == 0) return;
+            load_q<T, D>(a, x, wg, qtile);
+            fence_proxy_async_smem();
+            mbar_arrive(&q_full[wg]);
+        };
+        if (more && ok) fetch_q(it);
+        for (int r = 0; more && ok; ++r) {
+            const int myrow = wg * kSub + t;                 // row of the item
+            const bool has = myrow < it.rows;
+            // positions this row sees (rows past the end: all, their weights go nowhere)
+            const int lim = has ? max(0, min(it.L, it.L - it.n + (it.tile * kPrefillRows + myrow) / a.group + 1)) : 0x7fffffff;
+            const int n = it.nst[wg];
+            const int seen = min(lim, it.end[wg]);           // (dummy rows too stop at the tile's end)
+            float m_ref = -INFINITY, l = 0.0f;
+            for (int j = 0; j < n; ++j) {
+                ok = dec::wait_or_abort(&s_full[wg], ns & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                ++ns;
+                if (!ok) break;
+                tc::fence_after_sync();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::ld32(x[c], ts + 32 * c);
+                tc::wait_ld();
+                const int vis = seen - (it.step0 + j) * kStep;
+                if (__any_sync(0xffffffffu, vis < kStep)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= vis) x[c][e] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                float alpha = 1.0f;
+                if (top > m_ref + 8.0f) {
+                    if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - top);
+                    m_ref = top;
+                }
+                if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+                    // (S of this step was issued after the last O product: that is done)
+                    l *= alpha;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t o[16];
+                        tc::ld16(o, to + c0);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc::st16(to + c0, o);
+                    }
+                }
+                // (a row that has seen nothing keeps ref = -inf: every weight 2^-inf = 0)
+                const float off = m_ref == -INFINITY ? -INFINITY : -m_ref;
+                const uint64_t offx2 = pack64(off, off);
+                uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const uint32_t* y = &x[2 * h + (e >> 4)][2 * (e & 15)];
+                        const float2 z = unpack64(fma2(pack64(__uint_as_float(y[0]), __uint_as_float(y[1])), sl2x2, offx2));
+                        const float p0 = fast_exp2(z.x), p1 = fast_exp2(z.y);
+                        if (e & 1) sum1 = add2(sum1, pack64(p0, p1));
+                        else sum0 = add2(sum0, pack64(p0, p1));
+                        w[e] = Mma<T>::pack(p0, p1);
+                    }
+                    tc::st32(ts + 32 * h, w);
+                }
+                const float2 sm = unpack64(add2(sum0, sum1));
+                l += sm.x + sm.y;
+                tc::wait_st();
+                tc::fence_before_sync();
+                mbar_arrive(&p_full[wg]);
+            }
+            if (!ok) break;
+
+            // ---- the next item's Q (this item's last S is done), then this one's output
+            more = load_item(a, total, r + 1, next);
+            if (more) fetch_q(next);
+            const int rows_wg = min(kSub, it.rows - wg * kSub);          // (<= 0: no rows in this tile)
+            const int nparts = it.split & 255, part = (it.split >> 8) & 255, base = it.split >> 16;
+            const int64_t slot0 = static_cast<int64_t>(it.kvh) * a.part_cap + base;
+            if (n > 0) {
+                ok = dec::wait_or_abort(&o_full[wg], no & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                ++no;
+                if (!ok) break;
+                tc::fence_after_sync();
+                const bool bad_any = bad_tag[0] == r || bad_tag[1] == r;
+                const float inv = it.split ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;   // (a NaN sum stays)
+                T* orow = out + (has ? qo_row(a, it, myrow) : 0) * D;
+                float* prow = a.part_o + ((slot0 + part) * a.part_rows + myrow) * D;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tc::ld32(o, to + c0);
+                    tc::wait_ld();
+                    if (bad_any) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            bool up = false, down = false;
+                            for (int f = 0; f < G::kFixWarps; ++f) {
+                                if (bad_tag[f] != r) continue;
+                                const int* bp = bad + f * 2 * D + c0 + e;
+                                up = up || bp[0] < seen;
+                                down = down || bp[D] < seen;
+                            }
+                            if (up) o[e] = __float_as_uint(__uint_as_float(o[e]) + INFINITY);
+                            if (down) o[e] = __float_as_uint(__uint_as_float(o[e]) - INFINITY);
+                        }
+                    }
+                    if (!has) continue;
+                    if (it.split) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            reinterpret_cast<uint4*>(prow + c0)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = Mma<T>::pack(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                            reinterpret_cast<uint4*>(orow + c0)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                tc::fence_before_sync();
+            } else if (has && !it.split) {                   // rows that see nothing
+                uint4* o = reinterpret_cast<uint4*>(out + qo_row(a, it, myrow) * D);
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (it.split && rows_wg > 0) {
+                // ---- a part of a split tile: the last one to finish merges them all
+                if (has) a.part_ml[(slot0 + part) * a.part_rows + myrow] = make_float2(m_ref, l);
+                __threadfence();
+                group_sync(1 + wg);
+                if (t == 0) {
+                    unsigned* ticket = a.tickets + 2 * slot0 + wg;
+                    const bool last = atomicAdd(ticket, 1u) == static_cast<unsigned>(nparts - 1);
+                    if (last) *ticket = 0u;                  // for the next run over this plan
+                    merge_flag[wg] = last;
+                    __threadfence();
+                }
+                group_sync(1 + wg);
+                if (merge_flag[wg]) {
+                    // a lane's own row: its maximum and denominator over the parts
+                    const float2* ml = a.part_ml + slot0 * a.part_rows + myrow;
+                    float mm = -INFINITY, den = 0.0f;
+                    if (has) {
+#pragma unroll 4
+                        for (int p = 0; p < nparts; ++p) mm = fmaxf(mm, __ldcg(ml + static_cast<int64_t>(p) * a.part_rows).x);
+#pragma unroll 4
+                        for (int p = 0; p < nparts; ++p) {
+                            const float2 e = __ldcg(ml + static_cast<int64_t>(p) * a.part_rows);
+                            den += e.x == -INFINITY ? 0.0f : fast_exp2(e.x - mm) * e.y;
+                        }
+                    }
+                    const float inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
+                    // a row at a time, a warp across its columns
+                    constexpr int kPer = D / 32;
+                    const int w0 = wg * kSub + (warp & 3) * 32;
+                    const int last_row = min(32, it.rows - w0);
+#pragma unroll 1
+                    for (int q = 0; q < last_row; q += 4) {
+                        float acc[4][kPer];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+#pragma unroll
+                            for (int k = 0; k < kPer; ++k) acc[u][k] = 0.0f;
+#pragma unroll 2
+                        for (int p = 0; p < nparts; ++p) {
+                            const float e = has ? __ldcg(ml + static_cast<int64_t>(p) * a.part_rows).x : -INFINITY;
+                            const float w = e == -INFINITY ? 0.0f : fast_exp2(e - mm);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const float wu = __shfl_sync(0xffffffffu, w, (q + u) & 31);
+                                const bool none = __shfl_sync(0xffffffffu, e, (q + u) & 31) == -INFINITY;
+                                if (q + u >= last_row || none) continue;      // (an empty part's row was not written)
+                                const float* src = a.part_o + ((slot0 + p) * a.part_rows + w0 + q + u) * D + lane * kPer;
+                                float v[kPer];
+                                if constexpr (kPer == 4) {
+                                    const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+                                    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+                                } else {
+                                    const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+                                    v[0] = f.x; v[1] = f.y;
+                                }
+#pragma unroll
+                                for (int k = 0; k < kPer; ++k) acc[u][k] += wu * v[k];
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const float iu = __shfl_sync(0xffffffffu, inv, (q + u) & 31);
+                            if (q + u >= last_row) continue;
+                            uint32_t* dst = reinterpret_cast<uint32_t*>(out + qo_row(a, it, w0 + q + u) * D + lane * kPer);
+                            if constexpr (kPer == 4)
+                                *reinterpret_cast<uint2*>(dst) = make_uint2(Mma<T>::pack(acc[u][0] * iu, acc[u][1] * iu),
+                                                                            Mma<T>::pack(acc[u][2] * iu, acc[u][3] * iu));
+                            else
+                                *dst = Mma<T>::pack(acc[u][0] * iu, acc[u][1] * iu);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) atomicAdd(const_cast<int*>(epilogues), 1);
+            it = next;
+        }
+        if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
+    }
+    tc::fence_before_sync();
+    __syncthreads();                                // every role is through: TMEM is no longer used
+    launch_dependents();
+    if (warp == G::kMmaWarp) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, G::kTmemCols);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
+    using G = PfGeo<D>;
+    static_assert(G::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
+    auto kern = prefill_kernel<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kBytes));
+    if (e != cudaSuccess) return e;
+    // the warpgroups' register split must fit what a block is launched with, or it would wait for ever
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes fa{};
+        if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+        regs.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) * G::kThreads < 256 * G::kRegsSoftmax + 128 * G::kRegsOther)
+        return cudaErrorLaunchOutOfResources;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.slots, static_cast<int64_t>(a.capacity) * a.num_kv_heads)));
+    cfg.blockDim = dim3(G::kThreads);
+    cfg.dynamicSmemBytes = G::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tmk, tmv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype, int head_dim,
+                           cudaStream_t s) {
+    if (dtype == 0)
+        return head_dim == 128 ? launch_t<__half, 128>(a, tmk, tmv, s) : launch_t<__half, 64>(a, tmk, tmv, s);
+    return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(a, tmk, tmv, s) : launch_t<__nv_bfloat16, 64>(a, tmk, tmv, s);
+}
+
+}  // namespace pkv

@@ -1,0 +1,304 @@
+// Prefill work plan: one small kernel that turns a ragged batch's lengths into
+// the work list of the prefill kernel (pkv_prefill.cu).
+//
+// A tile is 256 query rows of a sequence (rows are (token, query head of the
+// KV head's group) pairs), and its work is the number of 128-position steps
+// its last row sees.  Tiles are listed longest first, so that the persistent
+// CTAs, which take items round robin, end at about the same time.  When a few
+// long tiles would leave SMs idle (a handful of rows over a long cache), every
+// tile is cut into parts of P steps whose partial softmax states the last part
+// to finish merges.  P is the candidate with the smallest estimated end:
+//
+//     (steps + kItemCost * items + kSplitCost * parts) * KV heads / SMs
+//         + half the largest item             when the items outnumber the SMs,
+//     the largest item                        otherwise
+//
+// (the first line is the average load plus the expected overhang of a
+// longest-first schedule).  The order of equally long items, and which partial
+// slot a tile gets, vary from run to run; no result depends on either, since
+// the merge sums parts in part order.
+//
+// One CTA: a few bytes per sequence, latency-bound.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCand = 24;
+__constant__ const int kParts[kCand] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 19, 21, 25, 30, 38, 50, 64, 76, 100, 128, 152};
+static_assert(kPrefillMaxParts == 152, "the last candidate");
+constexpr int kItemCost = 2;         // steps' worth of an item's query load and epilogue
+constexpr int kSplitCost = 3;        // and of a part's partial output and its share of the merge
+constexpr int kMinPart = 2;          // steps of a part at least
+constexpr int kBuckets = 128;
+
+struct Seq {
+    int start, n, len;
+};
+
+__device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int s, bool report) {
+    Seq q{__ldcg(a.query_starts + s), 0, __ldcg(a.seq_lens + s)};
+    const int end = __ldcg(a.query_starts + s + 1);
+    if (q.len > a.max_seq_len) {
+        if (report) raise_error(a.err, kErrBounds);
+        q.len = a.max_seq_len;
+    }
+    q.len = max(q.len, 0);
+    if (q.start < 0 || end < q.start || end > a.num_tokens) {
+        if (report) raise_error(a.err, kErrBounds);
+    } else {
+        q.n = end - q.start;
+    }
+    return q;
+}
+
+// Steps the last row of a tile sees.
+__device__ __forceinline__ int tile_steps(const Seq& q, int group, int tile) {
+    const int rows = q.n * group;
+    const int last = min(rows, (tile + 1) * kPrefillRows) - 1;
+    const int lim = min(q.len, max(0, q.len - q.n + last / group + 1));
+    return (lim + kPrefillStep - 1) / kPrefillStep;
+}
+
+__device__ __forceinline__ int warp_scan(int v) {            // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+struct Shared {
+    int start[kThreads], n[kThreads], len[kThreads];
+    int first[kThreads + 1];                                 // first tile of each of this chunk's sequences
+    int scan[kWarps];
+    int tiles, max_steps;
+    unsigned long long sum_steps;
+    unsigned long long items[kCand], parts[kCand];           // per candidate: all items; parts of split tiles
+    int bucket[kBuckets], at[kBuckets];
+    int part_len, max_item, next_slot;
+};
+
+// Loads a chunk of sequences and their tile offsets; the caller has synchronised.
+__device__ void load_chunk(const PrefillArgs& a, Shared& sh, int base, bool report) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int s = base + t;
+    Seq q{0, 0, 0};
+    if (s < a.num_seqs) q = load_seq(a, s, report);
+    sh.start[t] = q.start;
+    sh.n[t] = q.n;
+    sh.len[t] = q.len;
+    const int mine = static_cast<int>((static_cast<long long>(q.n) * a.group + kPrefillRows - 1) / kPrefillRows);
+    const int inc = warp_scan(mine);
+    if (lane == 31) sh.scan[warp] = inc;
+    __syncthreads();
+    if (warp == 0) sh.scan[lane] = warp_scan(sh.scan[lane]);
+    __syncthreads();
+    sh.first[t + 1] = inc + (warp > 0 ? sh.scan[warp - 1] : 0);
+    if (t == 0) sh.first[0] = 0;
+    __syncthreads();
+}
+
+// The chunk's sequence (0 .. 1023) that holds a tile.
+__device__ __forceinline__ int find_seq(const Shared& sh, int tile) {
+    int lo = 0;
+#pragma unroll
+    for (int w = kThreads / 2; w > 0; w >>= 1)
+        if (sh.first[lo + w] <= tile) lo += w;
+    return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArgs a) {
+    __shared__ Shared sh;
+    const int t = threadIdx.x, lane = t & 31;
+    grid_dependency_wait();
+    launch_dependents();
+    if (t == 0) {
+        sh.tiles = 0;
+        sh.max_steps = 0;
+        sh.sum_steps = 0;
+        sh.next_slot = 0;
+    }
+    if (t < kCand) sh.items[t] = sh.parts[t] = 0;
+    if (t < kBuckets) sh.bucket[t] = 0;
+    for (int i = t; i < a.num_kv_heads * a.part_cap * 2; i += kThreads) a.tickets[i] = 0u;
+    const bool one_chunk = a.num_seqs <= kThreads;
+
+    // ---- tiles, their steps' sum and maximum
+    for (int base = 0; base < a.num_seqs; base += kThreads) {
+        __syncthreads();
+        load_chunk(a, sh, base, true);
+        const int tiles = sh.first[kThreads];
+        int mx = 0;
+        unsigned long long sum = 0;
+        for (int i = t; i < tiles; i += kThreads) {
+            const int k = find_seq(sh, i);
+            const int st = tile_steps(Seq{sh.start[k], sh.n[k], sh.len[k]}, a.group, i - sh.first[k]);
+            mx = max(mx, st);
+            sum += st;
+        }
+        if (t < (tiles + 31) / 32 * 32) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            }
+            if (lane == 0) {
+                atomicMax(&sh.max_steps, mx);
+                atomicAdd(&sh.sum_steps, sum);
+            }
+        }
+        if (t == 0) sh.tiles += tiles;
+    }
+    __syncthreads();
+    const int maxs = sh.max_steps;
+
+    // ---- the part length: one candidate a thread group, every tile's parts counted at each
+    const long long nh = a.num_kv_heads;
+    const bool may_split = maxs > kMinPart && sh.tiles * nh < 8ll * a.slots;
+    if (may_split) {
+        for (int base = 0; base < a.num_seqs; base += kThreads) {
+            if (!one_chunk) {
+                __syncthreads();
+                load_chunk(a, sh, base, false);
+            }
+            const int tiles = sh.first[kThreads];
+            for (int i0 = t - lane; i0 < tiles; i0 += kThreads) {
+                const int i = i0 + lane;
+                int st = 0;
+                if (i < tiles) {
+                    const int k = find_seq(sh, i);
+                    st = tile_steps(Seq{sh.start[k], sh.n[k], sh.len[k]}, a.group, i - sh.first[k]);
+                }
+                for (int c = 0; c < kCand; ++c) {
+                    const int P = max(kMinPart, (maxs + kParts[c] - 1) / kParts[c]);
+                    const int parts = i < tiles ? max(1, (st + P - 1) / P) : 0;
+                    const int all = __reduce_add_sync(0xffffffffu, parts);
+                    const int split = __reduce_add_sync(0xffffffffu, parts > 1 ? parts : 0);
+                    if (lane == 0) {
+                        atomicAdd(&sh.items[c], static_cast<unsigned long long>(all));
+                        atomicAdd(&sh.parts[c], static_cast<unsigned long long>(split));
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (t < 32) {
+        long long best = 1ll << 62;
+        if (may_split && lane < kCand) {
+            const int P = max(kMinPart, (maxs + kParts[lane] - 1) / kParts[lane]);
+            const long long items = sh.items[lane], parts = sh.parts[lane];
+            const bool fits = parts <= a.part_cap && sh.tiles + parts <= a.capacity &&
+                              (maxs + P - 1) / P <= kPrefillMaxParts;
+            const long long top = min(P, maxs) + kItemCost + (parts > 0 ? kSplitCost : 0);
+            const long long load = (static_cast<long long>(sh.sum_steps) + kItemCost * items + kSplitCost * parts) * nh;
+            // in sixteenths of a step, the candidate's index breaking ties towards fewer parts
+            long long est = items * nh <= a.slots ? 16 * top : max(16 * top, 16 * load / a.slots + 8 * top);
+            if (fits) best = est * 32 + lane;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if (lane == 0) {
+            const int k = best == (1ll << 62) ? 1 : kParts[best & 31];
+            int P = max(kMinPart, (maxs + k - 1) / k);
+            if (!may_split || k == 1) P = max(1, maxs);
+            sh.part_len = P;
+            sh.max_item = min(P, max(1, maxs));
+        }
+    }
+    __syncthreads();
+    const int P = sh.part_len, top = sh.max_item;
+
+    // ---- items by length: count, offsets, write
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int base = 0; base < a.num_seqs; base += kThreads) {
+            if (!one_chunk) {
+                __syncthreads();
+                load_chunk(a, sh, base, false);
+            }
+            const int tiles = sh.first[kThreads];
+            for (int i = t; i < tiles; i += kThreads) {
+                const int k = find_seq(sh, i);
+                const int tile = i - sh.first[k];
+                const Seq q{sh.start[k], sh.n[k], sh.len[k]};
+                const int st = tile_steps(q, a.group, tile);
+                const int parts = max(1, (st + P - 1) / P);
+                const int len = (st + parts - 1) / parts;           // equal parts
+                int slot = 0;
+                if (pass == 1 && parts > 1) slot = atomicAdd(&sh.next_slot, parts);
+                for (int p = 0; p < parts; ++p) {
+                    const int s0 = p * len, s1 = min(st, s0 + len);
+                    const int b = min(kBuckets - 1, (top - max(0, s1 - s0)) * kBuckets / (top + 1));
+                    if (pass == 0) {
+                        atomicAdd(&sh.bucket[b], 1);
+                    } else {
+                        const int at = atomicAdd(&sh.at[b], 1);
+                        if (at < a.capacity) {
+                            a.items[2 * at] = make_int4(base + k, tile, s0, max(s0, s1));
+                            a.items[2 * at + 1] =
+                                make_int4(q.start, q.n, q.len, parts > 1 ? prefill_split(parts, p, slot) : 0);
+                        }
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (pass == 0 && t < 32) {
+            int carry = 0;
+            for (int b0 = 0; b0 < kBuckets; b0 += 32) {
+                const int v = sh.bucket[b0 + lane];
+                const int inc = warp_scan(v);
+                sh.at[b0 + lane] = carry + inc - v;
+                carry += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (lane == 0) a.header[0] = min(carry, a.capacity);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads,
+                                          int head_dim, int slots) {
+    PrefillWorkspace w{};
+    auto pad = [](size_t x) { return (x + 255) / 256 * 256; };
+    const int64_t rows = num_tokens * (num_heads / num_kv_heads);
+    w.part_rows = static_cast<int>(std::min<int64_t>(kPrefillRows, std::max<int64_t>(rows, 1)));
+    // two parts for every CTA, and one tile split as far as it goes
+    w.part_cap = std::max((2 * slots + num_kv_heads - 1) / num_kv_heads, 16);
+    w.capacity = static_cast<int>(rows / kPrefillRows + std::min<int64_t>(num_seqs, rows) + w.part_cap);
+    const size_t parts = static_cast<size_t>(num_kv_heads) * w.part_cap;
+    w.items = 256;
+    w.tickets = w.items + pad(static_cast<size_t>(w.capacity) * 32);
+    w.ml = w.tickets + pad(parts * 2 * sizeof(unsigned));
+    w.o = w.ml + pad(parts * w.part_rows * sizeof(float2));
+    w.total = w.o + pad(parts * w.part_rows * head_dim * sizeof(float));
+    return w;
+}
+
+cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_plan_kernel, a);
+}
+
+}  // namespace pkv
