@@ -369,7 +369,7 @@ PKV_API pkv_status pkv_paged_attention_verify(void* out, const void* q, const vo
  *   block_tables, max_blocks_per_seq, max_seq_len, block_size, num_blocks and
  *   the pools as for pkv_paged_attention_decode
  * head_dim in {64, 128}; block_size in {8, 16, 32}; num_heads a multiple of
- * num_kv_heads; num_tokens * (num_heads / num_kv_heads) below 2^30.
+ * num_kv_heads; num_tokens * num_heads below 2^30.
  * num_seqs == 0 or num_tokens == 0 is a no-op.
  */
 PKV_API size_t pkv_prefill_workspace_bytes(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads,

@@ -464,7 +464,7 @@ def prefill_plan(workspace, seq_lens, query_starts, num_tokens, num_heads, num_k
 
 @_one_device
 def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, scale=None,
-                            max_seq_len=None, workspace=None, planned=False) -> None:
+                            max_seq_len=None, workspace=None, planned=False, k_scale=None, v_scale=None) -> None:
     """Attention of a ragged batch of new tokens over the paged cache.  q, out: [T, Hq, d]; sequence s owns rows
     query_starts[s] .. query_starts[s + 1] - 1 (int32 [B + 1]), whose K/V are its last positions in the pools; row i
     of n attends over positions [0, seq_lens[s] - n + i].  Rows of no sequence are left as they are.  ``workspace``:

@@ -617,8 +617,8 @@ pkv_status prefill_args(pkv::PrefillArgs& a, pkv::PrefillWorkspace& lay, const i
     pkv_status st = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len);
     if (st != PKV_OK) return st;
     const int group = num_heads / num_kv_heads;
-    if (num_tokens < 0 || num_tokens * group >= (int64_t(1) << 30))
-        return fail(PKV_ERR_INVALID, "num_tokens %lld: at least 0, num_tokens * (num_heads / num_kv_heads) below 2^30",
+    if (num_tokens < 0 || num_tokens >= (int64_t(1) << 30) / num_heads)
+        return fail(PKV_ERR_INVALID, "num_tokens %lld: at least 0, num_tokens * num_heads below 2^30",
                     static_cast<long long>(num_tokens));
     if (num_seqs == 0 || num_tokens == 0) return ok();
     if (!seq_lens || !query_starts) return fail(PKV_ERR_INVALID, "null pointer");
@@ -702,7 +702,7 @@ extern "C" {
 
 size_t pkv_prefill_workspace_bytes(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads, int head_dim) {
     if (check_decode_shape(num_seqs, num_heads, num_kv_heads, head_dim, 0) != PKV_OK || num_tokens < 0 ||
-        num_tokens * (num_heads / num_kv_heads) >= (int64_t(1) << 30))
+        num_tokens >= (int64_t(1) << 30) / num_heads)
         return (size_t)-1;
     const int sms = sm_count_of(current_device());
     return pkv::prefill_workspace_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, sms > 0 ? sms : 152).total;

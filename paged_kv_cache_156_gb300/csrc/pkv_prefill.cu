@@ -24,15 +24,15 @@
 // 128 columns each.
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (they also load Q, write the
-// output and merge split tiles), 8 streams the K/V blocks (TMA, one box per
-// block and 128-byte column plane, its lanes side by side), 9 issues every MMA
-// (its program order is what orders S_i after the O_i that reads P_i), 10 and
-// 11 clean V tiles.
+// output and merge split tiles), 8 and 10 stream the K and V blocks (TMA, one
+// box per block and 128-byte column plane), 9 and 11 issue tile 0's and 1's
+// MMAs (a warp's program order is what orders S_i after the O_i that reads P_i),
+// 12 cleans V tiles.
 //
 // Masked positions.  A masked score is replaced before the maximum, whatever K
 // holds there.  A masked position's weight is 0, but 0 * V is NaN where V is
 // not finite, so on the steps that some row sees only in part, and on a
-// sequence's last, two warps look through the V rows that not every row sees:
+// sequence's last, a warp looks through the V rows that not every row sees:
 // slots past the end become zeros, non-finite elements too, after their first
 // position per column is noted; the epilogue then gives inf or NaN to exactly
 // the rows that see them.
@@ -55,24 +55,35 @@ constexpr int kSub = kPrefillSub;
 
 template <int D>
 struct PfGeo {
-    static constexpr int kThreads = 384;
-    static constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10, kFixWarps = 2;
+    static constexpr int kThreads = 512;
+    static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12;   // (9 and 11: MMAs; 13 to 15 idle)
     static constexpr int kHalves = D * 2 / 128;             // 128-byte column planes of a tile
     static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
     static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
     static constexpr int kStages = D == 128 ? 5 : 10;       // ring of K and V tiles, in turn
     static constexpr size_t kRing = 2 * size_t(kTile);      // after the two Q tiles
     static constexpr size_t kBars = kRing + size_t(kStages) * kTile;
-    static constexpr int kNumBars = 2 * kStages + 11;
+    static constexpr int kNumBars = 2 * kStages + 15;
     static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, epilogue count, tags
-    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // [2 warps][+inf, -inf][D] first positions
-    static constexpr size_t kBytes = kBad + size_t(kFixWarps) * 2 * D * 4;
+    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // [+inf, -inf][D] first positions
+    static constexpr size_t kBytes = kBad + size_t(2) * D * 4;
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
-    // registers a thread: 384 threads start with 168; the softmax warpgroups take 208, the third keeps 88
-    static constexpr int kRegsSoftmax = 208, kRegsOther = 88;
-    static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "the split fits the launch's registers");
+    // registers a thread: 512 threads start with 128; the softmax warpgroups take 192, the others keep 64
+    static constexpr int kRegsSoftmax = 192, kRegsOther = 64;
+    static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "the split fits the launch's registers");
     static_assert(kBytes <= 232448, "fits one SM");
 };
+
+// A bounded wait (false: gave up, or another role did).  Short code: every role waits in its inner loop,
+// and the roles share the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, unsigned parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
 
 // One work item as every role sees it (all derive it from the same plan entry).
 struct Item {
@@ -81,6 +92,8 @@ struct Item {
     int nst[2];                      // steps of each tile
     int end[2];                      // position after the last one each tile sees in the item
     int lim0;                        // positions every row of the item sees
+    __device__ __forceinline__ int steps_of(int i) const { return i ? nst[1] : nst[0]; }
+    __device__ __forceinline__ int end_of(int i) const { return i ? end[1] : end[0]; }
     __device__ __forceinline__ int steps() const { return max(nst[0], nst[1]); }
     __device__ __forceinline__ int stop() const { return max(end[0], end[1]); }
     // V rows [lo, nv16) of step j that not every row sees (nv: the item's positions in the step)
@@ -157,6 +170,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -164,6 +182,29 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// One lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A place in the ring: its slot, and the parity its barriers have there.
+template <int N>
+struct Ring {
+    int slot = 0;
+    unsigned phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+template <typename T>
+__device__ __forceinline__ T from_float(float x) {
+    const uint32_t w = Mma<T>::pack(x, x);
+    return *reinterpret_cast<const T*>(&w);
 }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
@@ -180,23 +221,24 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& it, int
     using G = PfGeo<D>;
     constexpr int kCh = D / 8;                               // 16-byte chunks of a row
     constexpr int kRowsAt = 32 / kCh;                        // rows a warp loads at once
+    constexpr int kBatch = 8;                                // loads in flight a lane
     const int lane = threadIdx.x & 31, w0 = ((threadIdx.x >> 5) & 3) * 32;
     const int ch = lane % kCh, sub = lane / kCh;
     const uint32_t keep = a.scale_log2 == 0.0f ? 0u : 0xffffffffu, flip = a.negate_q ? 0x80008000u : 0u;
-    constexpr int kBatch = 8;
+    const int mine = wg * kSub + w0 + lane;                  // each lane places one row, the others ask it
+    const int at = mine < it.rows ? static_cast<int>(qo_row(a, it, mine)) : -1;
+    const uint4* q = static_cast<const uint4*>(a.q) + ch;
 #pragma unroll 1
     for (int r0 = 0; r0 < 32; r0 += kRowsAt * kBatch) {
         uint4 x[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int r = wg * kSub + w0 + r0 + u * kRowsAt + sub;
-            x[u] = r < it.rows ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qo_row(a, it, r) * D) + ch)
-                               : make_uint4(0u, 0u, 0u, 0u);
+            const int row = __shfl_sync(0xffffffffu, at, r0 + u * kRowsAt + sub);
+            x[u] = row >= 0 ? __ldcg(q + static_cast<int64_t>(row) * kCh) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int r = w0 + r0 + u * kRowsAt + sub;
-            const uint32_t addr = dec::swz(qtile + (ch >> 3) * G::kPlane, r, ch & 7);
+            const uint32_t addr = dec::swz(qtile + (ch >> 3) * G::kPlane, w0 + r0 + u * kRowsAt + sub, ch & 7);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"((x[u].x & keep) ^ flip),
                          "r"((x[u].y & keep) ^ flip), "r"((x[u].z & keep) ^ flip), "r"((x[u].w & keep) ^ flip)
                          : "memory");
@@ -215,46 +257,49 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
     uint8_t* ring = smem + G::kRing;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kBars);
     uint64_t* full = bars;                          // [ST] a tile landed (TMA bytes)
-    uint64_t* empty = bars + ST;                    // [ST] the products that read it are done (MMA commit)
+    uint64_t* empty = bars + ST;                    // [ST] the products that read it are done (both MMA warps' commits)
     uint64_t* q_full = bars + 2 * ST;               // [2] an item's Q tile is in shared memory (softmax threads)
     uint64_t* s_full = q_full + 2;                  // [2] a step's S in TMEM, all earlier products done (MMA commit)
-    uint64_t* p_full = q_full + 4;                  // [2] a step's P in TMEM, O rescaled (softmax threads)
-    uint64_t* o_full = q_full + 6;                  // [2] an item's last O product done (MMA commit)
-    uint64_t* fix_req = q_full + 8;                 // a V tile landed that wants cleaning (MMA thread)
-    uint64_t* fix_done = q_full + 9;                // it is clean (both cleaning warps)
-    uint64_t* fin = q_full + 10;                    // every product issued is done (MMA commit)
+    uint64_t* p_full = q_full + 4;                  // [2][2] half a step's P in TMEM, O rescaled (softmax threads)
+    uint64_t* o_full = q_full + 8;                  // [2] an item's last O product done (MMA commit)
+    uint64_t* fix_req = q_full + 10;                // a V tile landed that wants cleaning (an MMA warp)
+    uint64_t* fix_done = q_full + 11;               // it is clean (cleaning warp)
+    uint64_t* turn = q_full + 12;                   // [2] the tile may issue its next round (the other's MMA warp)
+    uint64_t* fin = q_full + 14;                    // every product issued is done (both MMA warps' commits)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kMisc + 4);
     volatile int* epilogues = abort_flag + 1;       // epilogues finished, counted per softmax warp
-    volatile int* bad_tag = abort_flag + 2;         // [2] the item a cleaning warp noted bad elements of (-1: none)
-    volatile int* merge_flag = abort_flag + 4;      // [2]
-    int* bad = reinterpret_cast<int*>(smem + G::kBad);
+    volatile int* bad_tag = abort_flag + 2;         // the item whose non-finite V elements `bad` lists (-1: none)
+    volatile int* merge_flag = abort_flag + 3;      // [2]
+    int* bad = reinterpret_cast<int*>(smem + G::kBad);      // [+inf or NaN | -inf or NaN][D] first positions
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], kSub);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kSub);
+            mbar_init(&p_full[2 * i], kSub);
+            mbar_init(&p_full[2 * i + 1], kSub);
             mbar_init(&o_full[i], 1);
-            bad_tag[i] = -1;
+            mbar_init(&turn[i], 1);
         }
         mbar_init(fix_req, 1);
-        mbar_init(fix_done, G::kFixWarps);
-        mbar_init(fin, 1);
-        *epilogues = 0;
+        mbar_init(fix_done, 1);
+        mbar_init(fin, 2);
+        *epilogues = -8;                            // (the softmax warps' first round has no item)
+        *bad_tag = -1;
         // the 128B swizzle and the MMA descriptors assume 1 KB aligned tiles
         const bool misaligned = (smem_u32(smem) & 1023u) != 0;
         if (misaligned) raise_error(a.err, kErrTimeout);
         *abort_flag = misaligned;
         fence_barrier_init();
     }
-    if (warp == G::kMmaWarp) tc::tmem_alloc(tmem_slot, G::kTmemCols);
+    if (warp == G::kMma) tc::tmem_alloc(tmem_slot, G::kTmemCols);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -264,49 +309,53 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
 
     if (warp >= 8) {
         regs_dec<G::kRegsOther>();
-        if (warp == G::kLoadWarp) {
-            // ======================================================== the K/V ring
+        if (warp == G::kLoadK || warp == G::kLoadV) {
+            // ======================================================== the K/V ring: one warp for K, one for V
+            // An elected lane issues the boxes one after another (some 40 cycles each; left to the lanes
+            // side by side the compiler serialises them at 65, and one warp for both K and V then took
+            // 2100 cycles a step, as long as the step's products).
+            const int kv = warp == G::kLoadV;
+            const CUtensorMap* tm = kv ? &tmv : &tmk;
             const int bs = a.block_size;
-            const int boxes = kStep / bs * G::kHalves;       // TMA boxes of a full tile (at most 32: one a lane)
-            const int blk = lane / G::kHalves, hf = lane % G::kHalves;
-            unsigned c = 0;                                  // tiles streamed
+            const bool leader = elect_one();
+            Ring<ST> c;
+            if (kv) c.next();
             Item it;
             bool ok = !*abort_flag;
-            if (lane == 0) {
-                prefetch_tensormap(&tmk);
-                prefetch_tensormap(&tmv);
-            }
+            if (leader) prefetch_tensormap(tm);
             for (int r = 0; ok && load_item(a, total, r, it); ++r) {
                 const int n = it.steps(), stop = it.stop();
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
-                auto id_of = [&](int j) {                    // this lane's block id in step j (-1: no block)
-                    const int pos = (it.step0 + j) * kStep + blk * bs;
-                    return lane < boxes && j < n && pos < stop ? __ldcg(trow + pos / bs) : -1;
+                auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
+                    const int pos = (it.step0 + j) * kStep + lane * bs;
+                    return lane * bs < kStep && j < n && pos < stop ? __ldcg(trow + pos / bs) : -1;
                 };
                 int nxt = id_of(0);
-                for (int j = 0; j < n && ok; ++j) {
+                for (int j = 0; j < n; ++j) {
                     int id = nxt;
                     nxt = id_of(j + 1);
                     const int tok0 = (it.step0 + j) * kStep;
                     const int nb = (min(stop, tok0 + kStep) - tok0 + bs - 1) / bs;
-                    const bool mine = lane < boxes && blk < nb;
-                    if (mine && (id < 0 || static_cast<int64_t>(id) >= a.num_blocks)) {
+                    if (lane < nb && (id < 0 || static_cast<int64_t>(id) >= a.num_blocks)) {
                         raise_error(a.err, kErrBounds);
                         id = -1;                             // outside the tensor map: TMA fills zeros
                     }
+                    ok = wait_bar(&empty[c.slot], c.phase ^ 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int slot = __shfl_sync(0xffffffffu, c.slot, 0);
+                    if (leader) mbar_arrive_expect_tx(&full[slot], static_cast<unsigned>(nb * bs * D * 2));
+                    uint8_t* dst = ring + slot * G::kTile;
+                    for (int b = 0; b < nb; ++b) {
+                        const int pb = __shfl_sync(0xffffffffu, id, b);
+                        if (leader) {
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const unsigned st = c % ST, ph = (c / ST) & 1;
-                        ok = dec::wait_or_abort(&empty[st], ph ^ 1, abort_flag);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<unsigned>(nb * bs * D * 2));
-                        __syncwarp();
-                        if (mine)
-                            tma_load_4d(ring + st * G::kTile + hf * G::kPlane + blk * bs * 128, kv == 0 ? &tmk : &tmv,
-                                        hf * 64, it.kvh, 0, id, &full[st]);
-                        ++c;
+                            for (int hf = 0; hf < G::kHalves; ++hf)
+                                tma_load_4d(dst + hf * G::kPlane + b * bs * 128, tm, hf * 64, it.kvh, 0, pb, &full[slot]);
+                        }
                     }
+                    c.next();
+                    c.next();
                 }
             }
             if (!ok && lane == 0) {
@@ -314,114 +363,128 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                 const unsigned long long t0 = globaltimer_ns();       // copies in flight land before the CTA ends
                 while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
             }
-        } else if (warp == G::kMmaWarp) {
-            // ======================================================== every MMA, one thread
-            if (lane == 0) {
-                constexpr uint32_t kIdS = tc::idesc_f16(kSub, kStep, kBf16, false);   // S = Q K^T
-                constexpr uint32_t kIdO = tc::idesc_f16(kSub, D, kBf16, true);        // O += P V
-                unsigned c = 0;                              // tiles of the ring seen by finished items
-                unsigned nq[2] = {0, 0}, np[2] = {0, 0}, nfix = 0;
-                Item it;
-                bool ok = !*abort_flag;
-                for (int r = 0; ok && load_item(a, total, r, it); ++r) {
-                    const int n = it.steps();
-                    if (n == 0) continue;
-                    auto wait_tile = [&](unsigned k) { return dec::wait_or_abort(&full[k % ST], (k / ST) & 1, abort_flag); };
-                    auto product_s = [&](int i, unsigned k) {
-                        const uint32_t qt = smem_u32(smem + i * G::kTile), kt = smem_u32(ring + (k % ST) * G::kTile);
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off = (ks >> 2) * G::kPlane + (ks & 3) * 32;
-                            tc::mma_ss(tmem + G::kColS + i * 128, tc::smem_desc_sw128(qt + off, 16, 1024),
-                                       tc::smem_desc_sw128(kt + off, 16, 1024), kIdS, ks > 0);
-                        }
-                        tc::commit(&s_full[i]);
-                    };
-                    ok = wait_tile(c);
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        if (it.nst[i] == 0) continue;
-                        ok = dec::wait_or_abort(&q_full[i], nq[i] & 1, abort_flag);
-                        ++nq[i];
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        product_s(i, c);
-                    }
-                    if (!ok) break;
-                    tc::commit(&empty[c % ST]);
-                    for (int j = 0; j < n && ok; ++j) {
-                        const unsigned kv = c + 2 * j + 1, kn = kv + 1;
-                        ok = wait_tile(kv);
-                        if (!ok) break;
+        } else if (warp == G::kMma || warp == G::kMma + 2) {
+            // ======================================================== one warp a tile issues its MMAs
+            // The warp runs the control flow together and one elected lane issues.  These warps run a few
+            // hundred instructions a step between the softmax warps' thousands on the same schedulers, so
+            // nearly every instruction line is fetched anew; with a warp for each tile one's waits and
+            // bookkeeping run beside the other's products.
+            constexpr uint32_t kIdS = tc::idesc_f16(kSub, kStep, kBf16, false);   // S = Q K^T
+            constexpr uint32_t kIdO = tc::idesc_f16(kSub, D, kBf16, true);        // O += P V
+            const int i = warp != G::kMma;
+            const uint64_t dq = tc::smem_desc_sw128(smem_u32(smem) + i * G::kTile, 16, 1024);
+            const uint64_t dk = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);            // ring slot 0 as K
+            const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring), G::kPlane, 1024);     // and as V
+            const uint32_t ts = __shfl_sync(0xffffffffu, tmem, 0) + G::kColS + i * 128, to = ts + G::kColO;
+            const bool leader = elect_one();
+            Ring<ST> c;                                      // the next tile of the ring
+            unsigned np = 0, nq = 0, nfix = 0, nturn = i == 0;   // parities (tile 0 goes first: its turn's phase before the first)
+            Item it;
+            bool ok = !*abort_flag;
+            auto wait = [&](uint64_t* bar, unsigned parity) { return wait_bar(bar, parity, abort_flag); };
+            for (int r = 0; ok && load_item(a, total, r, it); ++r) {
+                const int n = it.steps(), ni = it.steps_of(i);
+                // round j: O += P V of step j, then S of step j + 1 (round -1: the first S alone)
+#pragma unroll 1
+                for (int j = -1; j < n; ++j) {
+                    const Ring<ST> v = c;                    // V of this step, then K of the next
+                    if (j >= 0) {
+                        c.next();
+                        ok = wait(&full[v.slot], v.phase);
                         int lo, nv, nv16;
                         it.partial(j, lo, nv, nv16);
-                        bool fix = lo < nv16;
-                        if (fix) mbar_arrive(fix_req);
-                        bool k_here = false;
-                        for (int i = 0; i < 2 && ok; ++i) {
-                            if (j < it.nst[i]) {
-                                ok = dec::wait_or_abort(&p_full[i], np[i] & 1, abort_flag);
-                                ++np[i];
-                                if (ok && fix) {
-                                    ok = dec::wait_or_abort(fix_done, nfix & 1, abort_flag);
-                                    ++nfix;
-                                    fix = false;
-                                }
-                                if (!ok) break;
-                                tc::fence_after_sync();
-                                const uint32_t vt = smem_u32(ring + (kv % ST) * G::kTile);
-                                const int nk = (min(kStep, it.end[i] - (it.step0 + j) * kStep) + 15) / 16;
+                        if (ok && lo < nv16) {               // (both warps wait, even one whose tile has no step j)
+                            if (leader && i == (j < it.nst[0] ? 0 : 1)) mbar_arrive(fix_req);
+                            ok = wait(fix_done, nfix);
+                            nfix ^= 1u;
+                        }
+                    }
+                    const bool more_k = j + 1 < n;
+                    if (ok && more_k) ok = wait(&full[c.slot], c.phase);
+                    if (!ok) break;
+                    // the tiles take turns, a round's O product and S product at a time: left to themselves
+                    // they fall into step, both on the tensor cores, then both in their softmax
+                    ok = wait(&turn[i], nturn);
+                    nturn ^= 1u;
+                    if (!ok) break;
+                    if (j >= 0 && j < ni) {
+                        const int left = it.end_of(i) - (it.step0 + j) * kStep;   // (16 a product, none wholly past the end)
+                        const uint64_t d = dv + static_cast<uint64_t>(v.slot * (G::kTile >> 4));
 #pragma unroll
-                                for (int kk = 0; kk < kStep / 16; ++kk) {
-                                    if (kk >= nk) break;
-                                    tc::mma_ts(tmem + G::kColO + i * 128, tmem + G::kColS + i * 128 + kk * 8,
-                                               tc::smem_desc_sw128(vt + kk * 2048, G::kPlane, 1024), kIdO,
-                                               (j > 0 || kk > 0) ? 1u : 0u);
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && wait(&p_full[2 * i + half], np);
+                            tc::fence_after_sync();
+                            if (ok && leader) {
+                                if (left >= kStep - 15) {
+#pragma unroll
+                                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                        tc::mma_ts(to, ts + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                                } else {
+#pragma unroll 1
+                                    for (int kk = 4 * half; kk < 4 * half + 4 && kk * 16 < left; ++kk)
+                                        tc::mma_ts(to, ts + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
                                 }
-                                if (j == it.nst[i] - 1) tc::commit(&o_full[i]);
-                            }
-                            if (i == 1) tc::commit(&empty[kv % ST]);
-                            if (j + 1 < it.nst[i]) {
-                                if (!k_here) ok = wait_tile(kn);
-                                if (!ok) break;
-                                k_here = true;
-                                product_s(i, kn);
                             }
                         }
-                        if (ok && j + 1 < n) tc::commit(&empty[kn % ST]);
+                        np ^= 1u;
+                        if (!ok) break;
                     }
-                    c += 2 * n;
-                }
-                if (!ok) dec::raise_abort(a.err, abort_flag);
-                tc::commit(fin);
-                dec::wait_or_abort(fin, 0, abort_flag);
-                if (*abort_flag) {                           // (an abort may leave MMAs running: give them a moment)
-                    const unsigned long long t0 = globaltimer_ns();
-                    while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
+                    if (j < 0 && ni > 0) {
+                        ok = wait(&q_full[i], nq);
+                        nq ^= 1u;
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                    }
+                    if (leader) {
+                        if (j + 1 < ni) {
+                            const uint64_t d = dk + static_cast<uint64_t>(c.slot * (G::kTile >> 4));
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint64_t off = ((ks >> 2) * G::kPlane + (ks & 3) * 32) >> 4;
+                                tc::mma_ss(ts, dq + off, d + off, kIdS, ks > 0);
+                            }
+                            tc::commit(&s_full[i]);
+                        }
+                        mbar_arrive(&turn[1 - i]);
+                        if (j >= 0 && j == ni - 1) tc::commit(&o_full[i]);
+                        if (j >= 0) tc::commit(&empty[v.slot]);
+                        if (more_k) tc::commit(&empty[c.slot]);
+                    }
+                    if (more_k) c.next();
                 }
             }
+            if (!ok && leader) dec::raise_abort(a.err, abort_flag);
+            if (leader) tc::commit(fin);
+            wait_bar(fin, 0, abort_flag);
+            if (*abort_flag) {                               // (an abort may leave MMAs running: give them a moment)
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
+            }
             __syncwarp();
-        } else {
+        } else if (warp == G::kClean) {
             // ======================================================== V tiles that some row sees only in part
-            const int fw = warp - G::kFixWarp;
             constexpr int kCh = D / 8;
             constexpr uint32_t kCarry = kBf16 ? 0x00800080u : 0x04000400u;   // exponent all ones -> bit 15
-            int* bad_pos = bad + fw * 2 * D;                 // [+inf or NaN | -inf or NaN][D] first positions
-            unsigned c = 0, nreq = 0;
+            unsigned nreq = 0;
+            Ring<ST> c;
             Item it;
             bool ok = !*abort_flag;
             for (int r = 0; ok && load_item(a, total, r, it); ++r) {
                 const int n = it.steps();
                 for (int j = 0; j < n && ok; ++j) {
+                    c.next();                                // (past the step's K)
+                    const int slot = c.slot;
+                    c.next();
                     int lo, nv, nv16;
                     it.partial(j, lo, nv, nv16);
                     if (lo >= nv16) continue;
-                    ok = dec::wait_or_abort(fix_req, nreq & 1, abort_flag);
+                    ok = wait_bar(fix_req, nreq & 1, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     ++nreq;
                     if (!ok) break;
-                    const uint32_t vt = smem_u32(ring + ((c + 2 * j + 1) % ST) * G::kTile);
+                    const uint32_t vt = smem_u32(ring + slot * G::kTile);
                     const int tok0 = (it.step0 + j) * kStep;
-                    for (int i0 = lo * kCh + fw * 32; i0 < nv16 * kCh; i0 += 32 * G::kFixWarps) {   // (warp-uniform)
+                    for (int i0 = lo * kCh; i0 < nv16 * kCh; i0 += 32) {   // (warp-uniform)
                         const int i = i0 + lane, row = i / kCh, ch = i % kCh;
                         const uint32_t addr = dec::swz(vt + (ch >> 3) * G::kPlane, row, ch & 7);
                         uint32_t x[4] = {0u, 0u, 0u, 0u};
@@ -432,36 +495,34 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                         uint32_t hit = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) hit |= ((x[e] & 0x7fff7fffu) + kCarry) & 0x80008000u;
+                        if (row >= nv && row < nv16)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
                         if (__any_sync(0xffffffffu, hit != 0)) {             // rare
-                            if (bad_tag[fw] != r) {          // (warp-uniform: this warp alone writes it)
+                            if (*bad_tag != r) {             // (warp-uniform: this warp alone writes it)
                                 // the softmax warps read the table in their epilogues: those of earlier items first
                                 const unsigned long long t0 = globaltimer_ns();
                                 while (*epilogues < 8 * r && !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
-                                for (int k = lane; k < 2 * D; k += 32) bad_pos[k] = 0x7fffffff;
+                                for (int k = lane; k < 2 * D; k += 32) bad[k] = 0x7fffffff;
                                 __syncwarp();
-                                if (lane == 0) bad_tag[fw] = r;
+                                if (lane == 0) *bad_tag = r;
                                 __syncwarp();
                             }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                                if ((((h & 0x7fffu) + (kCarry & 0xffffu)) & 0x8000u) == 0) continue;
-                                const bool nan = (h & 0x7fffu) != (0x8000u - (kCarry & 0xffffu));
-                                if (nan || h < 0x8000u) atomicMin(&bad_pos[8 * ch + e], tok0 + row);
-                                if (nan || h >= 0x8000u) atomicMin(&bad_pos[D + 8 * ch + e], tok0 + row);
-                                x[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+#pragma unroll 1
+                            for (int e = 0; e < 8 && hit != 0; ++e) {
+                                uint16_t h;
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr + 2 * e));
+                                const uint32_t mag = h & 0x7fffu, inf = 0x8000u - (kCarry & 0xffffu);
+                                if (mag < inf) continue;
+                                if (mag > inf || h < 0x8000u) atomicMin(&bad[8 * ch + e], tok0 + row);
+                                if (mag > inf || h >= 0x8000u) atomicMin(&bad[D + 8 * ch + e], tok0 + row);
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr + 2 * e), "h"(uint16_t(0)) : "memory");
                             }
                         }
-                        if (hit != 0 || (row >= nv && row < nv16))
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]),
-                                         "r"(x[2]), "r"(x[3])
-                                         : "memory");
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(fix_done);
                 }
-                c += 2 * n;
             }
             if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
         }
@@ -478,25 +539,20 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
         T* out = static_cast<T*>(a.out);
         unsigned ns = 0, no = 0;
         Item it, next;
-        bool ok = !*abort_flag;
-        bool more = load_item(a, total, 0, it);
-        auto fetch_q = [&](const Item& x) {
-            if (x.nst[wg] == 0) return;
-            load_q<T, D>(a, x, wg, qtile);
-            fence_proxy_async_smem();
-            mbar_arrive(&q_full[wg]);
-        };
-        if (more && ok) fetch_q(it);
-        for (int r = 0; more && ok; ++r) {
+        it.rows = it.nst[0] = it.nst[1] = it.end[0] = it.end[1] = 0;         // round -1: no item, only the first one's Q
+        it.L = it.n = it.tile = it.split = it.step0 = 0;
+        bool ok = !*abort_flag, more = true;
+#pragma unroll 1
+        for (int r = -1; more && ok; ++r) {
             const int myrow = wg * kSub + t;                 // row of the item
             const bool has = myrow < it.rows;
             // positions this row sees (rows past the end: all, their weights go nowhere)
             const int lim = has ? max(0, min(it.L, it.L - it.n + (it.tile * kPrefillRows + myrow) / a.group + 1)) : 0x7fffffff;
-            const int n = it.nst[wg];
-            const int seen = min(lim, it.end[wg]);           // (dummy rows too stop at the tile's end)
+            const int n = it.steps_of(wg);
+            const int seen = min(lim, it.end_of(wg));           // (dummy rows too stop at the tile's end)
             float m_ref = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
-                ok = dec::wait_or_abort(&s_full[wg], ns & 1, abort_flag);
+                ok = wait_bar(&s_full[wg], ns & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 ++ns;
                 if (!ok) break;
@@ -516,11 +572,12 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mx[c] = __uint_as_float(x[c][0]);
+                    mx[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
 #pragma unroll
-                    for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
+                    for (int e = 3; e < 31; e += 2) mx[c] = max3(mx[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                    mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sl2;
                 float alpha = 1.0f;
                 if (top > m_ref + 8.0f) {
                     if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - top);
@@ -529,7 +586,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                 if (__any_sync(0xffffffffu, alpha != 1.0f)) {
                     // (S of this step was issued after the last O product: that is done)
                     l *= alpha;
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 16) {
                         uint32_t o[16];
                         tc::ld16(o, to + c0);
@@ -556,50 +613,39 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                         w[e] = Mma<T>::pack(p0, p1);
                     }
                     tc::st32(ts + 32 * h, w);
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    mbar_arrive(&p_full[2 * wg + h]);
                 }
                 const float2 sm = unpack64(add2(sum0, sum1));
                 l += sm.x + sm.y;
-                tc::wait_st();
-                tc::fence_before_sync();
-                mbar_arrive(&p_full[wg]);
             }
             if (!ok) break;
 
             // ---- the next item's Q (this item's last S is done), then this one's output
             more = load_item(a, total, r + 1, next);
-            if (more) fetch_q(next);
+            if (more && next.steps_of(wg) > 0) {
+                load_q<T, D>(a, next, wg, qtile);
+                fence_proxy_async_smem();
+                mbar_arrive(&q_full[wg]);
+            }
             const int rows_wg = min(kSub, it.rows - wg * kSub);          // (<= 0: no rows in this tile)
             const int nparts = it.split & 255, part = (it.split >> 8) & 255, base = it.split >> 16;
             const int64_t slot0 = static_cast<int64_t>(it.kvh) * a.part_cap + base;
             if (n > 0) {
-                ok = dec::wait_or_abort(&o_full[wg], no & 1, abort_flag);
+                ok = wait_bar(&o_full[wg], no & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 ++no;
                 if (!ok) break;
                 tc::fence_after_sync();
-                const bool bad_any = bad_tag[0] == r || bad_tag[1] == r;
                 const float inv = it.split ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;   // (a NaN sum stays)
                 T* orow = out + (has ? qo_row(a, it, myrow) : 0) * D;
                 float* prow = a.part_o + ((slot0 + part) * a.part_rows + myrow) * D;
-#pragma unroll
+#pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
                     tc::ld32(o, to + c0);
                     tc::wait_ld();
-                    if (bad_any) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            bool up = false, down = false;
-                            for (int f = 0; f < G::kFixWarps; ++f) {
-                                if (bad_tag[f] != r) continue;
-                                const int* bp = bad + f * 2 * D + c0 + e;
-                                up = up || bp[0] < seen;
-                                down = down || bp[D] < seen;
-                            }
-                            if (up) o[e] = __float_as_uint(__uint_as_float(o[e]) + INFINITY);
-                            if (down) o[e] = __float_as_uint(__uint_as_float(o[e]) - INFINITY);
-                        }
-                    }
                     if (!has) continue;
                     if (it.split) {
 #pragma unroll
@@ -614,6 +660,15 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                                 w[e] = Mma<T>::pack(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
                             reinterpret_cast<uint4*>(orow + c0)[k] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
+                    }
+                }
+                if (*bad_tag == r && has) {                  // rare: V elements that the cleaning warp took out
+#pragma unroll 1
+                    for (int c = 0; c < D; ++c) {
+                        const float x = (bad[c] < seen ? INFINITY : 0.0f) + (bad[D + c] < seen ? -INFINITY : 0.0f);
+                        if (x == 0.0f) continue;
+                        if (it.split) prow[c] += x;
+                        else orow[c] = from_float<T>(x);
                     }
                 }
                 tc::fence_before_sync();
@@ -660,7 +715,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                         for (int u = 0; u < 4; ++u)
 #pragma unroll
                             for (int k = 0; k < kPer; ++k) acc[u][k] = 0.0f;
-#pragma unroll 2
+#pragma unroll 1
                         for (int p = 0; p < nparts; ++p) {
                             const float e = has ? __ldcg(ml + static_cast<int64_t>(p) * a.part_rows).x : -INFINITY;
                             const float w = e == -INFINITY ? 0.0f : fast_exp2(e - mm);
@@ -705,7 +760,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
     tc::fence_before_sync();
     __syncthreads();                                // every role is through: TMEM is no longer used
     launch_dependents();
-    if (warp == G::kMmaWarp) {
+    if (warp == G::kMma) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, G::kTmemCols);
     }
@@ -725,7 +780,7 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmk, const CUtenso
         if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
         regs.store(fa.numRegs, std::memory_order_relaxed);
     }
-    if (regs.load(std::memory_order_relaxed) * G::kThreads < 256 * G::kRegsSoftmax + 128 * G::kRegsOther)
+    if (regs.load(std::memory_order_relaxed) * G::kThreads < 256 * G::kRegsSoftmax + 256 * G::kRegsOther)
         return cudaErrorLaunchOutOfResources;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.slots, static_cast<int64_t>(a.capacity) * a.num_kv_heads)));
