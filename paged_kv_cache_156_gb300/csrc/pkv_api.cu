@@ -638,9 +638,9 @@ pkv_status prefill_args(pkv::PrefillArgs& a, pkv::PrefillWorkspace& lay, const i
     a.query_starts = query_starts;
     a.header = reinterpret_cast<int*>(ws);
     a.items = reinterpret_cast<int4*>(ws + lay.items);
-    a.tickets = reinterpret_cast<unsigned*>(ws + lay.tickets);
+    a.merges = reinterpret_cast<int4*>(ws + lay.merges);
     a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
-    a.part_o = reinterpret_cast<float*>(ws + lay.o);
+    a.part_o = reinterpret_cast<float4*>(ws + lay.o);
     a.num_tokens = num_tokens;
     a.num_seqs = num_seqs;
     a.max_seq_len = max_seq_len;
@@ -651,7 +651,26 @@ pkv_status prefill_args(pkv::PrefillArgs& a, pkv::PrefillWorkspace& lay, const i
     a.part_cap = lay.part_cap;
     a.part_rows = lay.part_rows;
     a.slots = sms;
+    a.may_split = pkv::prefill_may_split(num_tokens, max_seq_len, num_heads, num_kv_heads, sms);
     return ok();
+}
+
+// TMA descriptor of q [num_tokens][num_heads][head_dim]: a box is 128 rows (the group's heads of 128 / group
+// tokens) of one 128-byte column plane, 128-byte swizzled.
+pkv_status encode_queries(CUtensorMap* map, const void* base, int64_t num_tokens, int num_heads, int group, int d) {
+    auto enc = encode_fn();
+    if (!enc) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(num_heads),
+                          static_cast<cuuint64_t>(num_tokens), 1};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(num_heads) * d * 2,
+                             static_cast<cuuint64_t>(num_tokens) * num_heads * d * 2};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(pkv::kPrefillSub / group), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return PKV_OK;
 }
 
 pkv_status prefill_call(void* out, const void* q, const void* key_cache, const void* value_cache,
@@ -684,14 +703,17 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.block_size = block_size;
     a.num_blocks = num_blocks;
     a.err = error_word(current_device());
-    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    // (a zero scale becomes one that no finite score survives, so that a masked score, -inf, stays -inf)
+    a.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-30f);
     a.negate_q = scale < 0.0f;
-    CUtensorMap tmk{}, tmv{};
+    a.q_tma = pkv::kPrefillSub % a.group == 0;
+    CUtensorMap tmq{}, tmk{}, tmv{};
+    if (a.q_tma && (st = encode_queries(&tmq, q, num_tokens, num_heads, a.group, head_dim)) != PKV_OK) return st;
     if ((st = encode_pool(&tmk, key_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return st;
     if ((st = encode_pool(&tmv, value_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = planned ? cudaSuccess : pkv::launch_prefill_plan(a, s);
-    if (e == cudaSuccess) e = pkv::launch_prefill(a, tmk, tmv, dt == PKV_F16 ? 0 : 1, head_dim, s);
+    if (e == cudaSuccess) e = pkv::launch_prefill(a, tmq, tmk, tmv, dt == PKV_F16 ? 0 : 1, head_dim, s);
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
     return ok();
 }

@@ -216,12 +216,12 @@ struct PrefillArgs {
     const int32_t* block_tables;     // [B][max_blocks_per_seq]
     const int32_t* seq_lens;         // [B]
     const int32_t* query_starts;     // [B + 1]
-    int* header;                     // [0] number of work items
+    int* header;                     // [0] work items, [1] split tiles
     int4* items;                     // [capacity][2]: (sequence, tile, first step, end step),
                                      // (first query row of q, tokens, length, split: 0, or see prefill_split)
-    unsigned* tickets;               // [num_kv_heads][part_cap][2] parts finished of a split tile's two sub-tiles
+    int4* merges;                    // [part_cap / 2] split tiles: (split of part 0, tile, first query row, tokens)
     float2* part_ml;                 // [num_kv_heads][part_cap][part_rows] (reference maximum in log2 units, sum)
-    float* part_o;                   // [num_kv_heads][part_cap][part_rows][D] unnormalised partial outputs
+    float4* part_o;                  // [num_kv_heads][part_cap][D / 4][part_rows] unnormalised partial outputs
     unsigned* err;
     int64_t num_blocks;
     int64_t num_tokens;
@@ -234,27 +234,32 @@ struct PrefillArgs {
     int block_size;
     int capacity;                    // entries of `items`
     int part_cap;                    // partial slots per KV head
-    int part_rows;                   // rows of a partial slot: min(256, num_tokens * group)
+    int part_rows;                   // rows of a partial slot: min(256, num_tokens * group), a multiple of 32
     int slots;                       // CTAs the grid may hold at once
+    int may_split;                   // 0: the plan splits no tile (no merge kernel follows)
+    int q_tma;                       // 1: a Q tile is one TMA box a column plane (the group divides 128)
+    int negate_q;                    // scale < 0
     float scale_log2;                // |scale| * log2(e)
-    int negate_q;                    // scale < 0: q's signs are flipped as it is loaded
     const float* k_scale;            // [num_kv_heads] (E4M3 pools only, else nullptr)
     const float* v_scale;
 };
 
-// A split tile's item: parts, this part, first partial slot.
+// A split tile's part: number of parts, this part, first partial slot.
 __host__ __device__ inline int prefill_split(int nparts, int part, int base) { return base << 16 | part << 8 | nparts; }
 
-// Workspace: [header | items | tickets | (max, sum) pairs | partial outputs], each 256-byte aligned.
+// Workspace: [header | items | split tiles | (max, sum) pairs | partial outputs], each 256-byte aligned.
 struct PrefillWorkspace {
-    size_t items, tickets, ml, o, total;           // offsets and size
+    size_t items, merges, ml, o, total;            // offsets and size
     int capacity, part_cap, part_rows;
 };
 PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads,
                                           int head_dim, int slots);
+// Whether the plan may split a tile of such a batch: long enough sequences, and not so many tiles that
+// every SM has several anyway.
+bool prefill_may_split(int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots);
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
-cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype, int head_dim,
-                           cudaStream_t s);
+cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                           int dtype, int head_dim, cudaStream_t s);
 
 // Record `msg` as the calling thread's pkv_last_error() message and return `st`.
 int set_error_message(int st, const char* msg);

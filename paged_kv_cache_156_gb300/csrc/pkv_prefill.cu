@@ -23,16 +23,16 @@
 // tensor cores work on the other's products.  TMEM is full: S_0 S_1 O_0 O_1 of
 // 128 columns each.
 //
-// Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (they also load Q, write the
-// output and merge split tiles), 8 and 10 stream the K and V blocks (TMA, one
+// Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (they also write the output),
+// 13 loads Q tiles, 8 and 10 stream the K and V blocks (TMA, one
 // box per block and 128-byte column plane), 9 and 11 issue tile 0's and 1's
 // MMAs (a warp's program order is what orders S_i after the O_i that reads P_i),
-// 12 cleans V tiles.
+// 12 and 14 clean V tiles, 15 decodes the work items.
 //
 // Masked positions.  A masked score is replaced before the maximum, whatever K
 // holds there.  A masked position's weight is 0, but 0 * V is NaN where V is
 // not finite, so on the steps that some row sees only in part, and on a
-// sequence's last, a warp looks through the V rows that not every row sees:
+// sequence's last, two warps look through the V rows that not every row sees:
 // slots past the end become zeros, non-finite elements too, after their first
 // position per column is noted; the epilogue then gives inf or NaN to exactly
 // the rows that see them.
@@ -56,17 +56,20 @@ constexpr int kSub = kPrefillSub;
 template <int D>
 struct PfGeo {
     static constexpr int kThreads = 512;
-    static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12;   // (9 and 11: MMAs; 13 to 15 idle)
+    static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12, kLoadQ = 13, kPlan = 15;   // (9 and 11: MMAs; 12 and 14: cleaning)
     static constexpr int kHalves = D * 2 / 128;             // 128-byte column planes of a tile
     static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
     static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
     static constexpr int kStages = D == 128 ? 5 : 10;       // ring of K and V tiles, in turn
     static constexpr size_t kRing = 2 * size_t(kTile);      // after the two Q tiles
     static constexpr size_t kBars = kRing + size_t(kStages) * kTile;
-    static constexpr int kNumBars = 2 * kStages + 15;
+    static constexpr int kItems = 4;                        // items decoded ahead
+    static constexpr int kItemReaders = 15;                 // warps that read each
+    static constexpr int kNumBars = 3 * kStages + 15 + 2 * kItems;
     static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, epilogue count, tags
-    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // [+inf, -inf][D] first positions
-    static constexpr size_t kBytes = kBad + size_t(2) * D * 4;
+    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // [2 warps][+inf, -inf][D] first positions
+    static constexpr size_t kList = kBad + size_t(4) * D * 4;    // [kItems] decoded items
+    static constexpr size_t kBytes = kList + kItems * 64;
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
     // registers a thread: 512 threads start with 128; the softmax warpgroups take 192, the others keep 64
     static constexpr int kRegsSoftmax = 192, kRegsOther = 64;
@@ -85,13 +88,15 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, unsigned parity, volatil
     return true;
 }
 
-// One work item as every role sees it (all derive it from the same plan entry).
-struct Item {
-    int s, kvh, tile, step0, step1, qs, n, L, split;
-    int rows;                        // query rows of the item (0: nothing to do)
+// One work item, decoded by the plan warp into shared memory and read by every other role.
+struct alignas(16) Item {
+    int s, kvh, tile, step0;
+    int qs, n, L, split;
+    int rows;                        // query rows of the item (0: an entry to skip; -1: no more items)
     int nst[2];                      // steps of each tile
-    int end[2];                      // position after the last one each tile sees in the item
     int lim0;                        // positions every row of the item sees
+    int end[2];                      // position after the last one each tile sees in the item
+    int pad[2];
     __device__ __forceinline__ int steps_of(int i) const { return i ? nst[1] : nst[0]; }
     __device__ __forceinline__ int end_of(int i) const { return i ? end[1] : end[0]; }
     __device__ __forceinline__ int steps() const { return max(nst[0], nst[1]); }
@@ -107,17 +112,32 @@ struct Item {
 
 // (Plan, tables and q are read with ld.cg, never ld.nc: the compiler may move an ld.nc above the
 // wait for the kernel that writes them.)
-__device__ __forceinline__ bool load_item(const PrefillArgs& a, int total, int round, Item& it) {
+// The entry of this CTA's item in a round: fetched a round ahead of its use.
+struct Entry {
+    int4 x, y;
+    int kvh;
+    bool live;
+};
+__device__ __forceinline__ Entry fetch_entry(const PrefillArgs& a, int total, int round) {
     const int g = gridDim.x, b = blockIdx.x;
     const long long w = static_cast<long long>(round) * g + ((round & 1) ? g - 1 - b : b);
-    if (w >= total) return false;
-    const int e = static_cast<int>(w) / a.num_kv_heads;
-    it.kvh = static_cast<int>(w) - e * a.num_kv_heads;
-    const int4 x = __ldcg(a.items + 2 * e), y = __ldcg(a.items + 2 * e + 1);
+    Entry n{};
+    n.live = w < total;
+    if (n.live) {
+        const int e = static_cast<int>(w) / a.num_kv_heads;
+        n.kvh = static_cast<int>(w) - e * a.num_kv_heads;
+        n.x = __ldcg(a.items + 2 * e);
+        n.y = __ldcg(a.items + 2 * e + 1);
+    }
+    return n;
+}
+__device__ __forceinline__ void read_item(const PrefillArgs& a, const Entry& n, Item& it) {
+    const int4 x = n.x, y = n.y;
+    it.kvh = n.kvh;
     it.s = x.x;
     it.tile = x.y;
     it.step0 = x.z;
-    it.step1 = x.w;
+    const int step1 = x.w;
     it.qs = y.x;
     it.n = y.y;
     it.L = y.z;
@@ -127,12 +147,12 @@ __device__ __forceinline__ bool load_item(const PrefillArgs& a, int total, int r
     it.lim0 = 0;
     const int nparts = it.split & 255, part = (it.split >> 8) & 255, base = it.split >> 16;
     // a plan of other arguments: skip the entry rather than leave the buffers
-    if (it.s < 0 || it.s >= a.num_seqs || it.tile < 0 || it.step0 < 0 || it.step1 < it.step0 || it.qs < 0 || it.n <= 0 ||
+    if (it.s < 0 || it.s >= a.num_seqs || it.tile < 0 || it.step0 < 0 || step1 < it.step0 || it.qs < 0 || it.n <= 0 ||
         it.qs + static_cast<long long>(it.n) > a.num_tokens || it.L < 0 || it.L > a.max_seq_len ||
         static_cast<long long>(it.tile) * kPrefillRows >= static_cast<long long>(it.n) * a.group || it.split < 0 ||
         (it.split != 0 && (part >= nparts || base + nparts > a.part_cap))) {
-        if (threadIdx.x == 0) raise_error(a.err, kErrBounds);
-        return true;
+        if ((threadIdx.x & 31) == 0) raise_error(a.err, kErrBounds);
+        return;
     }
     const int row0 = it.tile * kPrefillRows;
     it.rows = min(kPrefillRows, it.n * a.group - row0);
@@ -143,11 +163,10 @@ __device__ __forceinline__ bool load_item(const PrefillArgs& a, int total, int r
         const int r = min(kSub, it.rows - i * kSub);
         if (r > 0) {
             const int lim = past + (row0 + i * kSub + r - 1) / a.group + 1;      // the tile's last row's
-            it.end[i] = max(0, min(it.step1 < (1 << 23) ? it.step1 * kStep : it.L, min(lim, it.L)));
+            it.end[i] = max(0, min(step1 < (1 << 23) ? step1 * kStep : it.L, min(lim, it.L)));
             it.nst[i] = max(0, (it.end[i] + kStep - 1) / kStep - it.step0);
         }
     }
-    return true;
 }
 
 __device__ __forceinline__ uint64_t pack64(float x, float y) {
@@ -206,7 +225,24 @@ __device__ __forceinline__ T from_float(float x) {
     const uint32_t w = Mma<T>::pack(x, x);
     return *reinterpret_cast<const T*>(&w);
 }
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool keep) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(keep ? 16 : 0) : "memory");
+}
+// 4 x 4 transposition over a quad: lane q's register i becomes lane i's register q.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4]) {
+    const int q = threadIdx.x & 3;
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & s) continue;
+            const uint32_t give = (q & s) ? w[i] : w[i ^ s];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
+            if (q & s) w[i] = got;
+            else w[i ^ s] = got;
+        }
+    }
+}
 
 // Element offset / D of row r of the item's tile in q / out.
 __device__ __forceinline__ int64_t qo_row(const PrefillArgs& a, const Item& it, int r) {
@@ -215,39 +251,36 @@ __device__ __forceinline__ int64_t qo_row(const PrefillArgs& a, const Item& it, 
     return (static_cast<int64_t>(it.qs) + tok) * a.num_heads + it.kvh * a.group + (rr - tok * a.group);
 }
 
-// A warp's 32 rows of a Q tile into shared memory (128-byte swizzle, zeros past the rows).
+// A Q tile into shared memory by one warp's 16-byte asynchronous copies (128-byte swizzle, zeros past the
+// rows): the form for group sizes that no TMA box fits.
 template <typename T, int D>
-__device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& it, int wg, uint32_t qtile) {
+__device__ __forceinline__ void copy_q(const PrefillArgs& a, const Item& it, int tile, uint32_t qtile) {
     using G = PfGeo<D>;
     constexpr int kCh = D / 8;                               // 16-byte chunks of a row
-    constexpr int kRowsAt = 32 / kCh;                        // rows a warp loads at once
-    constexpr int kBatch = 8;                                // loads in flight a lane
-    const int lane = threadIdx.x & 31, w0 = ((threadIdx.x >> 5) & 3) * 32;
+    constexpr int kRowsAt = 32 / kCh;                        // rows the warp copies at once
+    const int lane = threadIdx.x & 31;
     const int ch = lane % kCh, sub = lane / kCh;
-    const uint32_t keep = a.scale_log2 == 0.0f ? 0u : 0xffffffffu, flip = a.negate_q ? 0x80008000u : 0u;
-    const int mine = wg * kSub + w0 + lane;                  // each lane places one row, the others ask it
-    const int at = mine < it.rows ? static_cast<int>(qo_row(a, it, mine)) : -1;
     const uint4* q = static_cast<const uint4*>(a.q) + ch;
 #pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += kRowsAt * kBatch) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int row = __shfl_sync(0xffffffffu, at, r0 + u * kRowsAt + sub);
-            x[u] = row >= 0 ? __ldcg(q + static_cast<int64_t>(row) * kCh) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const uint32_t addr = dec::swz(qtile + (ch >> 3) * G::kPlane, w0 + r0 + u * kRowsAt + sub, ch & 7);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"((x[u].x & keep) ^ flip),
-                         "r"((x[u].y & keep) ^ flip), "r"((x[u].z & keep) ^ flip), "r"((x[u].w & keep) ^ flip)
-                         : "memory");
+    for (int r0 = 0; r0 < kSub; r0 += 32) {
+        const int mine = tile * kSub + r0 + lane;            // each lane places one row, the others ask it
+        const int at = mine < it.rows ? static_cast<int>(qo_row(a, it, mine)) : -1;
+#pragma unroll 4
+        for (int u = 0; u < 32; u += kRowsAt) {
+            const int row = __shfl_sync(0xffffffffu, at, u + sub);
+            cp_async_16_or_zero(dec::swz(qtile + (ch >> 3) * G::kPlane, r0 + u + sub, ch & 7),
+                                q + static_cast<int64_t>(max(row, 0)) * kCh, row >= 0);
         }
     }
+    cp_async_commit();
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmk,
+__global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
+                                                                        const __grid_constant__ CUtensorMap tmk,
                                                                         const __grid_constant__ CUtensorMap tmv,
                                                                         const PrefillArgs a) {
     using G = PfGeo<D>;
@@ -257,42 +290,47 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
     uint8_t* ring = smem + G::kRing;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kBars);
     uint64_t* full = bars;                          // [ST] a tile landed (TMA bytes)
-    uint64_t* empty = bars + ST;                    // [ST] the products that read it are done (both MMA warps' commits)
-    uint64_t* q_full = bars + 2 * ST;               // [2] an item's Q tile is in shared memory (softmax threads)
-    uint64_t* s_full = q_full + 2;                  // [2] a step's S in TMEM, all earlier products done (MMA commit)
-    uint64_t* p_full = q_full + 4;                  // [2][2] half a step's P in TMEM, O rescaled (softmax threads)
-    uint64_t* o_full = q_full + 8;                  // [2] an item's last O product done (MMA commit)
-    uint64_t* fix_req = q_full + 10;                // a V tile landed that wants cleaning (an MMA warp)
-    uint64_t* fix_done = q_full + 11;               // it is clean (cleaning warp)
+    uint64_t* empty = bars + ST;                    // [ST] the products that read it are done (both MMA warps' commits), the cleaning warps past it
+    uint64_t* clean = bars + 2 * ST;                // [ST] the cleaning warps are past the tile
+    uint64_t* q_full = bars + 3 * ST;               // [2] an item's Q tile is in shared memory (TMA bytes, or the Q warp)
+    uint64_t* q_empty = q_full + 2;                 // [2] an item's last S product done: its Q is read (MMA commit)
+    uint64_t* s_full = q_full + 4;                  // [2] a step's S in TMEM, all earlier products done (MMA commit)
+    uint64_t* p_full = q_full + 6;                  // [2][2] half a step's P in TMEM, O rescaled (softmax threads)
+    uint64_t* o_full = q_full + 10;                 // [2] an item's last O product done (MMA commit)
     uint64_t* turn = q_full + 12;                   // [2] the tile may issue its next round (the other's MMA warp)
     uint64_t* fin = q_full + 14;                    // every product issued is done (both MMA warps' commits)
+    uint64_t* item_full = q_full + 15;              // [kItems] an item is decoded (plan warp)
+    uint64_t* item_empty = item_full + G::kItems;   // [kItems] every reader has read it
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kMisc + 4);
     volatile int* epilogues = abort_flag + 1;       // epilogues finished, counted per softmax warp
-    volatile int* bad_tag = abort_flag + 2;         // the item whose non-finite V elements `bad` lists (-1: none)
-    volatile int* merge_flag = abort_flag + 3;      // [2]
-    int* bad = reinterpret_cast<int*>(smem + G::kBad);      // [+inf or NaN | -inf or NaN][D] first positions
+    volatile int* bad_tag = abort_flag + 2;         // [2] the item whose non-finite V elements a warp's table lists (-1: none)
+    int* bad = reinterpret_cast<int*>(smem + G::kBad);      // [2 warps][+inf or NaN | -inf or NaN][D] first positions
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 2);
+            mbar_init(&empty[i], 4);
+            mbar_init(&clean[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], kSub);
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[2 * i], kSub);
             mbar_init(&p_full[2 * i + 1], kSub);
             mbar_init(&o_full[i], 1);
             mbar_init(&turn[i], 1);
         }
-        mbar_init(fix_req, 1);
-        mbar_init(fix_done, 1);
+        for (int i = 0; i < G::kItems; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], G::kItemReaders);
+        }
         mbar_init(fin, 2);
-        *epilogues = -8;                            // (the softmax warps' first round has no item)
-        *bad_tag = -1;
+        *epilogues = 0;
+        bad_tag[0] = bad_tag[1] = -1;
         // the 128B swizzle and the MMA descriptors assume 1 KB aligned tiles
         const bool misaligned = (smem_u32(smem) & 1023u) != 0;
         if (misaligned) raise_error(a.err, kErrTimeout);
@@ -305,7 +343,21 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();
-    const int total = min(__ldcg(a.header), a.capacity) * a.num_kv_heads;
+    Item* list = reinterpret_cast<Item*>(smem + G::kList);
+    // The round's item for one warp; false: none is left, or a wait gave up.
+    auto get_item = [&](int r, Item& it, bool& ok) {
+        const int k = r % G::kItems;
+        ok = wait_bar(&item_full[k], (r / G::kItems) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        const int4* src = reinterpret_cast<const int4*>(list + k);
+        int4* dst = reinterpret_cast<int4*>(&it);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = src[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[k]);
+        return it.rows >= 0;
+    };
 
     if (warp >= 8) {
         regs_dec<G::kRegsOther>();
@@ -323,7 +375,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
             Item it;
             bool ok = !*abort_flag;
             if (leader) prefetch_tensormap(tm);
-            for (int r = 0; ok && load_item(a, total, r, it); ++r) {
+            for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps(), stop = it.stop();
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
                 auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
@@ -369,7 +421,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
             // hundred instructions a step between the softmax warps' thousands on the same schedulers, so
             // nearly every instruction line is fetched anew; with a warp for each tile one's waits and
             // bookkeeping run beside the other's products.
-            constexpr uint32_t kIdS = tc::idesc_f16(kSub, kStep, kBf16, false);   // S = Q K^T
+            const uint32_t kIdS = tc::idesc_f16(kSub, kStep, kBf16, false) | (a.negate_q ? 1u << 13 : 0u);   // S = Q K^T, -Q K^T
             constexpr uint32_t kIdO = tc::idesc_f16(kSub, D, kBf16, true);        // O += P V
             const int i = warp != G::kMma;
             const uint64_t dq = tc::smem_desc_sw128(smem_u32(smem) + i * G::kTile, 16, 1024);
@@ -378,11 +430,11 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
             const uint32_t ts = __shfl_sync(0xffffffffu, tmem, 0) + G::kColS + i * 128, to = ts + G::kColO;
             const bool leader = elect_one();
             Ring<ST> c;                                      // the next tile of the ring
-            unsigned np = 0, nq = 0, nfix = 0, nturn = i == 0;   // parities (tile 0 goes first: its turn's phase before the first)
+            unsigned np = 0, nq = 0, nturn = i == 0;   // parities (tile 0 goes first: its turn's phase before the first)
             Item it;
             bool ok = !*abort_flag;
             auto wait = [&](uint64_t* bar, unsigned parity) { return wait_bar(bar, parity, abort_flag); };
-            for (int r = 0; ok && load_item(a, total, r, it); ++r) {
+            for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps(), ni = it.steps_of(i);
                 // round j: O += P V of step j, then S of step j + 1 (round -1: the first S alone)
 #pragma unroll 1
@@ -393,10 +445,8 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                         ok = wait(&full[v.slot], v.phase);
                         int lo, nv, nv16;
                         it.partial(j, lo, nv, nv16);
-                        if (ok && lo < nv16) {               // (both warps wait, even one whose tile has no step j)
-                            if (leader && i == (j < it.nst[0] ? 0 : 1)) mbar_arrive(fix_req);
-                            ok = wait(fix_done, nfix);
-                            nfix ^= 1u;
+                        if (ok && lo < nv16) {               // V that some row sees only in part
+                            ok = wait(&clean[v.slot], v.phase);
                         }
                     }
                     const bool more_k = j + 1 < n;
@@ -444,6 +494,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                                 tc::mma_ss(ts, dq + off, d + off, kIdS, ks > 0);
                             }
                             tc::commit(&s_full[i]);
+                            if (j + 2 == ni) tc::commit(&q_empty[i]);
                         }
                         mbar_arrive(&turn[1 - i]);
                         if (j >= 0 && j == ni - 1) tc::commit(&o_full[i]);
@@ -461,67 +512,165 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                 while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
             }
             __syncwarp();
-        } else if (warp == G::kClean) {
+        } else if (warp == G::kLoadQ) {
+            // ======================================================== Q tiles, as soon as the last S product read them
+            const bool leader = elect_one();
+            Item it;
+            const int sub_tokens = kSub / a.group;           // (when the group divides a tile)
+            unsigned ph = 3u;                                // parities of q_empty (a bit a tile): both tiles start empty
+            bool ok = !*abort_flag;
+            if (leader && a.q_tma) prefetch_tensormap(&tmq);
+            for (int r = 0; ok && get_item(r, it, ok); ++r) {
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    if (it.steps_of(i) == 0) continue;
+                    ok = wait_bar(&q_empty[i], (ph >> i) & 1u, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ph ^= 1u << i;
+                    if (!ok) break;
+                    uint8_t* dst = smem + i * G::kTile;
+                    if (a.q_tma) {
+                        // (rows of the box past the item's are other tokens' queries, or zeros past the last:
+                        // their scores go nowhere)
+                        const int tok = it.qs + (2 * it.tile + i) * sub_tokens;
+                        if (leader) {
+                            mbar_arrive_expect_tx(&q_full[i], G::kTile);
+#pragma unroll
+                            for (int hf = 0; hf < G::kHalves; ++hf)
+                                tma_load_4d(dst + hf * G::kPlane, &tmq, hf * 64, it.kvh * a.group, tok, 0, &q_full[i]);
+                        }
+                    } else {
+                        copy_q<T, D>(a, it, i, smem_u32(dst));
+                        if (leader) mbar_arrive(&q_full[i]);
+                    }
+                }
+            }
+            if (!ok && leader) {
+                dec::raise_abort(a.err, abort_flag);
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
+            }
+        } else if (warp == G::kPlan) {
+            // ======================================================== items, decoded a few ahead
+            // (the first entry is read beside the count of items, not after it: entries past the count are stale)
+            Entry next = fetch_entry(a, a.capacity * a.num_kv_heads, 0);
+            const int total = min(max(__ldcg(a.header), 0), a.capacity) * a.num_kv_heads;
+            next.live = static_cast<int>(blockIdx.x) < total;
+            bool ok = !*abort_flag, more = true;
+            for (int r = 0; ok && more; ++r) {
+                const int k = r % G::kItems;
+                Item it;
+                more = next.live;
+                if (more) {
+                    read_item(a, next, it);
+                    next = fetch_entry(a, total, r + 1);
+                } else {
+                    it.rows = -1;
+                }
+                ok = wait_bar(&item_empty[k], ((r / G::kItems) & 1) ^ 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    list[k] = it;
+                    mbar_arrive(&item_full[k]);
+                }
+                __syncwarp();
+            }
+            if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
+        } else if (warp == G::kClean || warp == G::kClean + 2) {
             // ======================================================== V tiles that some row sees only in part
+            const int fw = warp != G::kClean;
+            int* mine = bad + fw * 2 * D;
             constexpr int kCh = D / 8;
+            constexpr int kBatch = 4;                        // loads in flight a lane
             constexpr uint32_t kCarry = kBf16 ? 0x00800080u : 0x04000400u;   // exponent all ones -> bit 15
-            unsigned nreq = 0;
             Ring<ST> c;
             Item it;
             bool ok = !*abort_flag;
-            for (int r = 0; ok && load_item(a, total, r, it); ++r) {
+            for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps();
                 for (int j = 0; j < n && ok; ++j) {
-                    c.next();                                // (past the step's K)
+                    // (these warps pass every slot of the ring in order, so that they clean V as it lands)
+                    ok = wait_bar(&full[c.slot], c.phase, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive(&clean[c.slot]);
+                        mbar_arrive(&empty[c.slot]);
+                    }
+                    c.next();
                     const int slot = c.slot;
+                    ok = wait_bar(&full[slot], c.phase, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     c.next();
                     int lo, nv, nv16;
                     it.partial(j, lo, nv, nv16);
-                    if (lo >= nv16) continue;
-                    ok = wait_bar(fix_req, nreq & 1, abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
-                    ++nreq;
-                    if (!ok) break;
+                    if (lo >= nv16) {
+                        if (lane == 0) {
+                            mbar_arrive(&clean[slot]);
+                            mbar_arrive(&empty[slot]);
+                        }
+                        continue;
+                    }
                     const uint32_t vt = smem_u32(ring + slot * G::kTile);
                     const int tok0 = (it.step0 + j) * kStep;
-                    for (int i0 = lo * kCh; i0 < nv16 * kCh; i0 += 32) {   // (warp-uniform)
-                        const int i = i0 + lane, row = i / kCh, ch = i % kCh;
-                        const uint32_t addr = dec::swz(vt + (ch >> 3) * G::kPlane, row, ch & 7);
-                        uint32_t x[4] = {0u, 0u, 0u, 0u};
-                        if (row < nv)
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                         : "r"(addr));
-                        uint32_t hit = 0;
+                    auto addr_of = [&](int i) { return dec::swz(vt + (i % kCh >> 3) * G::kPlane, i / kCh, i % kCh & 7); };
+                    const int end = nv16 * kCh;
+#pragma unroll 1
+                    for (int i0 = lo * kCh + fw * 32 * kBatch; i0 < end; i0 += 64 * kBatch) {       // (warp-uniform)
+                        uint32_t hit = 0;                    // bit u: piece u holds a non-finite element
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) hit |= ((x[e] & 0x7fff7fffu) + kCarry) & 0x80008000u;
-                        if (row >= nv && row < nv16)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+                        for (int u = 0; u < kBatch; ++u) {
+                            const int i = i0 + 32 * u + lane, row = i / kCh;
+                            uint32_t x[4] = {0u, 0u, 0u, 0u}, any = 0;
+                            if (row < nv)
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                             : "r"(addr_of(i)));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) any |= ((x[e] & 0x7fff7fffu) + kCarry) & 0x80008000u;
+                            hit |= any ? 1u << u : 0u;
+                        }
+                        if (i0 + 32 * kBatch > nv * kCh) {   // slots past the end
+                            for (int u = 0; u < kBatch; ++u) {
+                                const int i = i0 + 32 * u + lane;
+                                if (i / kCh >= nv && i < end)
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr_of(i)), "r"(0u) : "memory");
+                            }
+                        }
                         if (__any_sync(0xffffffffu, hit != 0)) {             // rare
-                            if (*bad_tag != r) {             // (warp-uniform: this warp alone writes it)
+                            if (bad_tag[fw] != r) {          // (warp-uniform: this warp alone writes it)
                                 // the softmax warps read the table in their epilogues: those of earlier items first
                                 const unsigned long long t0 = globaltimer_ns();
                                 while (*epilogues < 8 * r && !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
-                                for (int k = lane; k < 2 * D; k += 32) bad[k] = 0x7fffffff;
+                                for (int k = lane; k < 2 * D; k += 32) mine[k] = 0x7fffffff;
                                 __syncwarp();
-                                if (lane == 0) *bad_tag = r;
+                                if (lane == 0) bad_tag[fw] = r;
                                 __syncwarp();
                             }
 #pragma unroll 1
-                            for (int e = 0; e < 8 && hit != 0; ++e) {
+                            for (int e = 0; e < 8 * kBatch && hit != 0; ++e) {
+                                if (!(hit >> (e >> 3) & 1u)) continue;
+                                const int i = i0 + 32 * (e >> 3) + lane;
+                                const uint32_t addr = addr_of(i) + 2 * (e & 7);
                                 uint16_t h;
-                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr + 2 * e));
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr));
                                 const uint32_t mag = h & 0x7fffu, inf = 0x8000u - (kCarry & 0xffffu);
                                 if (mag < inf) continue;
-                                if (mag > inf || h < 0x8000u) atomicMin(&bad[8 * ch + e], tok0 + row);
-                                if (mag > inf || h >= 0x8000u) atomicMin(&bad[D + 8 * ch + e], tok0 + row);
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr + 2 * e), "h"(uint16_t(0)) : "memory");
+                                const int col = 8 * (i % kCh) + (e & 7), pos = tok0 + i / kCh;
+                                if (mag > inf || h < 0x8000u) atomicMin(&mine[col], pos);
+                                if (mag > inf || h >= 0x8000u) atomicMin(&mine[D + col], pos);
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(uint16_t(0)) : "memory");
                             }
                         }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(fix_done);
+                    if (lane == 0) {
+                        mbar_arrive(&clean[slot]);
+                        mbar_arrive(&empty[slot]);
+                    }
                 }
             }
             if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
@@ -533,21 +682,20 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
         const int t = threadIdx.x & 127;
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t ts = tl + G::kColS + wg * 128, to = tl + G::kColO + wg * 128;
-        const uint32_t qtile = smem_u32(smem + wg * G::kTile);
-        const float sl2 = a.scale_log2 == 0.0f ? 1.0f : a.scale_log2;   // (scale 0: q was zeroed)
+        const float sl2 = a.scale_log2;
         const uint64_t sl2x2 = pack64(sl2, sl2);
         T* out = static_cast<T*>(a.out);
         unsigned ns = 0, no = 0;
-        Item it, next;
-        it.rows = it.nst[0] = it.nst[1] = it.end[0] = it.end[1] = 0;         // round -1: no item, only the first one's Q
-        it.L = it.n = it.tile = it.split = it.step0 = 0;
-        bool ok = !*abort_flag, more = true;
+        Item it;
+        bool ok = !*abort_flag;
 #pragma unroll 1
-        for (int r = -1; more && ok; ++r) {
+        for (int r = 0; ok && get_item(r, it, ok); ++r) {
             const int myrow = wg * kSub + t;                 // row of the item
             const bool has = myrow < it.rows;
+            const int rr = it.tile * kPrefillRows + myrow, tok = rr / a.group;
+            const int at = has ? (it.qs + tok) * a.num_heads + it.kvh * a.group + (rr - tok * a.group) : -1;   // row of out
             // positions this row sees (rows past the end: all, their weights go nowhere)
-            const int lim = has ? max(0, min(it.L, it.L - it.n + (it.tile * kPrefillRows + myrow) / a.group + 1)) : 0x7fffffff;
+            const int lim = has ? max(0, min(it.L, it.L - it.n + tok + 1)) : 0x7fffffff;
             const int n = it.steps_of(wg);
             const int seen = min(lim, it.end_of(wg));           // (dummy rows too stop at the tile's end)
             float m_ref = -INFINITY, l = 0.0f;
@@ -622,138 +770,88 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
             }
             if (!ok) break;
 
-            // ---- the next item's Q (this item's last S is done), then this one's output
-            more = load_item(a, total, r + 1, next);
-            if (more && next.steps_of(wg) > 0) {
-                load_q<T, D>(a, next, wg, qtile);
-                fence_proxy_async_smem();
-                mbar_arrive(&q_full[wg]);
-            }
-            const int rows_wg = min(kSub, it.rows - wg * kSub);          // (<= 0: no rows in this tile)
-            const int nparts = it.split & 255, part = (it.split >> 8) & 255, base = it.split >> 16;
-            const int64_t slot0 = static_cast<int64_t>(it.kvh) * a.part_cap + base;
+            // ---- the output, or a split tile's partial one
+            const bool split = it.split != 0;
+            const int64_t slot = static_cast<int64_t>(it.kvh) * a.part_cap + (it.split >> 16) + ((it.split >> 8) & 255);
+            float4* prow = a.part_o + slot * (D / 4) * a.part_rows + myrow;      // [column / 4][row]
             if (n > 0) {
                 ok = wait_bar(&o_full[wg], no & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 ++no;
                 if (!ok) break;
                 tc::fence_after_sync();
-                const float inv = it.split ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;   // (a NaN sum stays)
-                T* orow = out + (has ? qo_row(a, it, myrow) : 0) * D;
-                float* prow = a.part_o + ((slot0 + part) * a.part_rows + myrow) * D;
+                if (split) {
+                    // a row a thread, 16 bytes of 32 neighbouring rows side by side
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tc::ld32(o, to + c0);
-                    tc::wait_ld();
-                    if (!has) continue;
-                    if (it.split) {
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tc::ld32(o, to + c0);
+                        tc::wait_ld();
+                        if (has) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            reinterpret_cast<uint4*>(prow + c0)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = Mma<T>::pack(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                            reinterpret_cast<uint4*>(orow + c0)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int k = 0; k < 8; ++k)
+                                prow[static_cast<int64_t>(c0 / 4 + k) * a.part_rows] =
+                                    make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                         }
                     }
-                }
-                if (*bad_tag == r && has) {                  // rare: V elements that the cleaning warp took out
+                } else {
+                    // The 16x256b shape gives a quad two rows' columns; transposed over the quad, four lanes
+                    // write 64 contiguous bytes of a row (a row a thread would touch 32 lines a store, 2 us
+                    // an item in the load-store unit).
+                    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;             // (a NaN sum stays)
 #pragma unroll 1
-                    for (int c = 0; c < D; ++c) {
-                        const float x = (bad[c] < seen ? INFINITY : 0.0f) + (bad[D + c] < seen ? -INFINITY : 0.0f);
-                        if (x == 0.0f) continue;
-                        if (it.split) prow[c] += x;
-                        else orow[c] = from_float<T>(x);
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int ra = 16 * hh + (lane >> 2);                                 // rows ra and ra + 8 of the warp
+                        const float ia = __shfl_sync(0xffffffffu, inv, ra), ib = __shfl_sync(0xffffffffu, inv, ra + 8);
+                        const int aa = __shfl_sync(0xffffffffu, at, ra), ab = __shfl_sync(0xffffffffu, at, ra + 8);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 64) {
+                            uint32_t o[32];
+                            tc::ld16x256_x8(o, to + (static_cast<uint32_t>(16 * hh) << 16) + c0);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int g = 0; g < 8; g += 4) {
+                                uint32_t wa[4], wb[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t* y = &o[4 * (g + e)];
+                                    wa[e] = Mma<T>::pack(__uint_as_float(y[0]) * ia, __uint_as_float(y[1]) * ia);
+                                    wb[e] = Mma<T>::pack(__uint_as_float(y[2]) * ib, __uint_as_float(y[3]) * ib);
+                                }
+                                quad_transpose(wa);
+                                quad_transpose(wb);
+                                const int col = c0 + 8 * (g + (lane & 3));
+                                if (aa >= 0)
+                                    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(aa) * D + col) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                                if (ab >= 0)
+                                    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(ab) * D + col) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                            }
+                        }
                     }
                 }
                 tc::fence_before_sync();
-            } else if (has && !it.split) {                   // rows that see nothing
-                uint4* o = reinterpret_cast<uint4*>(out + qo_row(a, it, myrow) * D);
+                const bool bad0 = bad_tag[0] == r, bad1 = bad_tag[1] == r;
+                if (bad0 || bad1) {                          // rare: V elements that the cleaning warps took out
+                    __syncwarp();
+#pragma unroll 1
+                    for (int c = 0; has && c < D; ++c) {
+                        const bool up = (bad0 && bad[c] < seen) || (bad1 && bad[2 * D + c] < seen);
+                        const bool down = (bad0 && bad[D + c] < seen) || (bad1 && bad[3 * D + c] < seen);
+                        if (!up && !down) continue;
+                        const float x = (up ? INFINITY : 0.0f) + (down ? -INFINITY : 0.0f);
+                        if (split) reinterpret_cast<float*>(prow + static_cast<int64_t>(c / 4) * a.part_rows)[c & 3] += x;
+                        else out[static_cast<int64_t>(at) * D + c] = from_float<T>(x);
+                    }
+                }
+            } else if (has && !split) {                      // rows that see nothing
+                uint4* o = reinterpret_cast<uint4*>(out + static_cast<int64_t>(at) * D);
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (it.split && rows_wg > 0) {
-                // ---- a part of a split tile: the last one to finish merges them all
-                if (has) a.part_ml[(slot0 + part) * a.part_rows + myrow] = make_float2(m_ref, l);
-                __threadfence();
-                group_sync(1 + wg);
-                if (t == 0) {
-                    unsigned* ticket = a.tickets + 2 * slot0 + wg;
-                    const bool last = atomicAdd(ticket, 1u) == static_cast<unsigned>(nparts - 1);
-                    if (last) *ticket = 0u;                  // for the next run over this plan
-                    merge_flag[wg] = last;
-                    __threadfence();
-                }
-                group_sync(1 + wg);
-                if (merge_flag[wg]) {
-                    // a lane's own row: its maximum and denominator over the parts
-                    const float2* ml = a.part_ml + slot0 * a.part_rows + myrow;
-                    float mm = -INFINITY, den = 0.0f;
-                    if (has) {
-#pragma unroll 4
-                        for (int p = 0; p < nparts; ++p) mm = fmaxf(mm, __ldcg(ml + static_cast<int64_t>(p) * a.part_rows).x);
-#pragma unroll 4
-                        for (int p = 0; p < nparts; ++p) {
-                            const float2 e = __ldcg(ml + static_cast<int64_t>(p) * a.part_rows);
-                            den += e.x == -INFINITY ? 0.0f : fast_exp2(e.x - mm) * e.y;
-                        }
-                    }
-                    const float inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
-                    // a row at a time, a warp across its columns
-                    constexpr int kPer = D / 32;
-                    const int w0 = wg * kSub + (warp & 3) * 32;
-                    const int last_row = min(32, it.rows - w0);
-#pragma unroll 1
-                    for (int q = 0; q < last_row; q += 4) {
-                        float acc[4][kPer];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-#pragma unroll
-                            for (int k = 0; k < kPer; ++k) acc[u][k] = 0.0f;
-#pragma unroll 1
-                        for (int p = 0; p < nparts; ++p) {
-                            const float e = has ? __ldcg(ml + static_cast<int64_t>(p) * a.part_rows).x : -INFINITY;
-                            const float w = e == -INFINITY ? 0.0f : fast_exp2(e - mm);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float wu = __shfl_sync(0xffffffffu, w, (q + u) & 31);
-                                const bool none = __shfl_sync(0xffffffffu, e, (q + u) & 31) == -INFINITY;
-                                if (q + u >= last_row || none) continue;      // (an empty part's row was not written)
-                                const float* src = a.part_o + ((slot0 + p) * a.part_rows + w0 + q + u) * D + lane * kPer;
-                                float v[kPer];
-                                if constexpr (kPer == 4) {
-                                    const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                                    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-                                } else {
-                                    const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-                                    v[0] = f.x; v[1] = f.y;
-                                }
-#pragma unroll
-                                for (int k = 0; k < kPer; ++k) acc[u][k] += wu * v[k];
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float iu = __shfl_sync(0xffffffffu, inv, (q + u) & 31);
-                            if (q + u >= last_row) continue;
-                            uint32_t* dst = reinterpret_cast<uint32_t*>(out + qo_row(a, it, w0 + q + u) * D + lane * kPer);
-                            if constexpr (kPer == 4)
-                                *reinterpret_cast<uint2*>(dst) = make_uint2(Mma<T>::pack(acc[u][0] * iu, acc[u][1] * iu),
-                                                                            Mma<T>::pack(acc[u][2] * iu, acc[u][3] * iu));
-                            else
-                                *dst = Mma<T>::pack(acc[u][0] * iu, acc[u][1] * iu);
-                        }
-                    }
-                }
-            }
+            if (split && has) a.part_ml[slot * a.part_rows + myrow] = make_float2(m_ref, l);
             __syncwarp();
             if (lane == 0) atomicAdd(const_cast<int*>(epilogues), 1);
-            it = next;
         }
         if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
     }
@@ -766,8 +864,88 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
     }
 }
 
+// The split tiles' parts merged: 32 rows a CTA, a row a lane, its columns over the warps.
+//     m = max_p m_p,  out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
+// summed in part order.  A kernel of its own, since the merge of a 256-row tile is a megabyte of reads:
+// by the last CTA to finish it took 70 us of a 177 us call (33 tokens x 64 heads over 65549 positions).
+constexpr int kMergeThreads = 128, kMergeRows = 32;
 template <typename T, int D>
-cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
+__global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const PrefillArgs a) {
+    constexpr int kQuads = D / 4 / (kMergeThreads / 32);      // 4-column pieces a thread merges
+    __shared__ uint2 tile[kMergeRows][D / 4 + 1];
+    __shared__ int rows_at[kMergeRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    launch_dependents();
+    const int groups = a.part_rows / kMergeRows;
+    const long long units = static_cast<long long>(min(__ldcg(a.header + 1), a.part_cap / 2)) * a.num_kv_heads * groups;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int g = static_cast<int>(u % groups);
+        const int kvh = static_cast<int>((u / groups) % a.num_kv_heads);
+        const int4 e = __ldcg(a.merges + u / groups / a.num_kv_heads);
+        const int nparts = e.x & 255, base = e.x >> 16;
+        Item it;
+        it.tile = e.y;
+        it.qs = e.z;
+        it.n = e.w;
+        it.kvh = kvh;
+        if (nparts < 1 || base < 0 || base + nparts > a.part_cap || it.tile < 0 || it.qs < 0 || it.n <= 0 ||
+            it.qs + static_cast<long long>(it.n) > a.num_tokens) {
+            if (threadIdx.x == 0) raise_error(a.err, kErrBounds);
+            continue;
+        }
+        const long long left = static_cast<long long>(it.n) * a.group - static_cast<long long>(it.tile) * kPrefillRows - g * kMergeRows;
+        if (left <= 0) continue;
+        const bool has = lane < left;
+        const int row = g * kMergeRows + lane;
+        const int64_t slot = static_cast<int64_t>(kvh) * a.part_cap + base;
+        const float2* ml = a.part_ml + slot * a.part_rows + row;
+        const float4* po = a.part_o + slot * (D / 4) * a.part_rows + row;
+        float m = -INFINITY, den = 0.0f;
+        if (has) {
+#pragma unroll 8
+            for (int p = 0; p < nparts; ++p) m = fmaxf(m, __ldcg(ml + static_cast<int64_t>(p) * a.part_rows).x);
+#pragma unroll 8
+            for (int p = 0; p < nparts; ++p) {
+                const float2 x = __ldcg(ml + static_cast<int64_t>(p) * a.part_rows);
+                den += x.x == -INFINITY && x.y == 0.0f ? 0.0f : fast_exp2(x.x - m) * x.y;
+            }
+        }
+        float4 acc[kQuads];
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+        for (int p = 0; p < nparts; ++p) {
+            const float2 x = has ? __ldcg(ml + static_cast<int64_t>(p) * a.part_rows) : make_float2(-INFINITY, 0.0f);
+            if (x.x == -INFINITY && x.y == 0.0f) continue;    // (a part the row sees nothing of: its O was not written)
+            const float w = fast_exp2(x.x - m);
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k) {
+                const float4 v = __ldcg(po + (static_cast<int64_t>(p) * (D / 4) + warp + k * (kMergeThreads / 32)) * a.part_rows);
+                acc[k].x += w * v.x;
+                acc[k].y += w * v.y;
+                acc[k].z += w * v.z;
+                acc[k].w += w * v.w;
+            }
+        }
+        const float inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k)
+            tile[lane][warp + k * (kMergeThreads / 32)] =
+                make_uint2(Mma<T>::pack(acc[k].x * inv, acc[k].y * inv), Mma<T>::pack(acc[k].z * inv, acc[k].w * inv));
+        if (warp == 0) rows_at[lane] = has ? static_cast<int>(qo_row(a, it, row)) : -1;
+        __syncthreads();
+        for (int i = threadIdx.x; i < kMergeRows * (D / 4); i += kMergeThreads) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            if (rows_at[r] >= 0) reinterpret_cast<uint2*>(static_cast<T*>(a.out) + static_cast<int64_t>(rows_at[r]) * D)[c] = tile[r][c];
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                     cudaStream_t s) {
     using G = PfGeo<D>;
     static_assert(G::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
     auto kern = prefill_kernel<T, D>;
@@ -792,16 +970,21 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmk, const CUtenso
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tmk, tmv, a);
+    e = cudaLaunchKernelEx(&cfg, kern, tmq, tmk, tmv, a);
+    if (e != cudaSuccess || !a.may_split) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * a.slots));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<T, D>, a);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype, int head_dim,
-                           cudaStream_t s) {
+cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                           int dtype, int head_dim, cudaStream_t s) {
     if (dtype == 0)
-        return head_dim == 128 ? launch_t<__half, 128>(a, tmk, tmv, s) : launch_t<__half, 64>(a, tmk, tmv, s);
-    return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(a, tmk, tmv, s) : launch_t<__nv_bfloat16, 64>(a, tmk, tmv, s);
+        return head_dim == 128 ? launch_t<__half, 128>(a, tmq, tmk, tmv, s) : launch_t<__half, 64>(a, tmq, tmk, tmv, s);
+    return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(a, tmq, tmk, tmv, s) : launch_t<__nv_bfloat16, 64>(a, tmq, tmk, tmv, s);
 }
 
 }  // namespace pkv

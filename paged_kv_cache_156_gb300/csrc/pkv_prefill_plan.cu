@@ -78,23 +78,27 @@ __device__ __forceinline__ int warp_scan(int v) {            // inclusive
     return v;
 }
 
+constexpr int kCached = 2048;        // tiles whose steps stay in shared memory between the phases
+
 struct Shared {
     int start[kThreads], n[kThreads], len[kThreads];
     int first[kThreads + 1];                                 // first tile of each of this chunk's sequences
     int scan[kWarps];
-    int tiles, max_steps;
-    unsigned long long sum_steps;
-    unsigned long long items[kCand], parts[kCand];           // per candidate: all items; parts of split tiles
+    int steps[kCached], seq[kCached];
+    int wmax[kWarps];
+    unsigned long long wsum[kWarps];
+    long long items[kCand], parts[kCand];                    // per candidate: all items; parts of split tiles
     int bucket[kBuckets], at[kBuckets];
-    int part_len, max_item, next_slot;
+    int part_len, max_item, next_slot, next_merge;
 };
 
-// Loads a chunk of sequences and their tile offsets; the caller has synchronised.
+// Loads a chunk of sequences and their tile offsets.
 __device__ void load_chunk(const PrefillArgs& a, Shared& sh, int base, bool report) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int s = base + t;
     Seq q{0, 0, 0};
     if (s < a.num_seqs) q = load_seq(a, s, report);
+    __syncthreads();
     sh.start[t] = q.start;
     sh.n[t] = q.n;
     sh.len[t] = q.len;
@@ -102,9 +106,9 @@ __device__ void load_chunk(const PrefillArgs& a, Shared& sh, int base, bool repo
     const int inc = warp_scan(mine);
     if (lane == 31) sh.scan[warp] = inc;
     __syncthreads();
-    if (warp == 0) sh.scan[lane] = warp_scan(sh.scan[lane]);
-    __syncthreads();
-    sh.first[t + 1] = inc + (warp > 0 ? sh.scan[warp - 1] : 0);
+    const int w = warp_scan(sh.scan[lane]);                  // (every warp scans the warps' totals)
+    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    sh.first[t + 1] = inc + (warp > 0 ? before : 0);
     if (t == 0) sh.first[0] = 0;
     __syncthreads();
 }
@@ -120,99 +124,93 @@ __device__ __forceinline__ int find_seq(const Shared& sh, int tile) {
 
 __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArgs a) {
     __shared__ Shared sh;
-    const int t = threadIdx.x, lane = t & 31;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     grid_dependency_wait();
     launch_dependents();
-    if (t == 0) {
-        sh.tiles = 0;
-        sh.max_steps = 0;
-        sh.sum_steps = 0;
-        sh.next_slot = 0;
-    }
-    if (t < kCand) sh.items[t] = sh.parts[t] = 0;
+    if (t == 0) sh.next_slot = sh.next_merge = 0;
     if (t < kBuckets) sh.bucket[t] = 0;
-    for (int i = t; i < a.num_kv_heads * a.part_cap * 2; i += kThreads) a.tickets[i] = 0u;
     const bool one_chunk = a.num_seqs <= kThreads;
+    // tile i of the current chunk: its sequence and steps
+    auto tile_of = [&](int i, bool cached, int& k) {
+        if (cached) {
+            k = sh.seq[i];
+            return sh.steps[i];
+        }
+        k = find_seq(sh, i);
+        return tile_steps(Seq{sh.start[k], sh.n[k], sh.len[k]}, a.group, i - sh.first[k]);
+    };
 
     // ---- tiles, their steps' sum and maximum
+    int mx = 0;
+    long long tiles_all = 0;
+    unsigned long long sum = 0;
     for (int base = 0; base < a.num_seqs; base += kThreads) {
-        __syncthreads();
         load_chunk(a, sh, base, true);
         const int tiles = sh.first[kThreads];
-        int mx = 0;
-        unsigned long long sum = 0;
+        const bool keep = one_chunk && tiles <= kCached;
         for (int i = t; i < tiles; i += kThreads) {
-            const int k = find_seq(sh, i);
-            const int st = tile_steps(Seq{sh.start[k], sh.n[k], sh.len[k]}, a.group, i - sh.first[k]);
+            int k;
+            const int st = tile_of(i, false, k);
+            if (keep) {
+                sh.steps[i] = st;
+                sh.seq[i] = k;
+            }
             mx = max(mx, st);
             sum += st;
         }
-        if (t < (tiles + 31) / 32 * 32) {
+        tiles_all += tiles;
+    }
+    const bool cached = one_chunk && tiles_all <= kCached;
+    mx = __reduce_max_sync(0xffffffffu, mx);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            }
-            if (lane == 0) {
-                atomicMax(&sh.max_steps, mx);
-                atomicAdd(&sh.sum_steps, sum);
-            }
-        }
-        if (t == 0) sh.tiles += tiles;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+        sh.wmax[warp] = mx;
+        sh.wsum[warp] = sum;
     }
     __syncthreads();
-    const int maxs = sh.max_steps;
+    const int maxs = __reduce_max_sync(0xffffffffu, sh.wmax[lane]);
 
-    // ---- the part length: one candidate a thread group, every tile's parts counted at each
+    // ---- the part length: a warp a candidate counts every tile's parts at it.  (The host rules splitting out
+    // by the same count of tiles; a batch that the plan would have to reload is not split either.)
     const long long nh = a.num_kv_heads;
-    const bool may_split = maxs > kMinPart && sh.tiles * nh < 8ll * a.slots;
-    if (may_split) {
-        for (int base = 0; base < a.num_seqs; base += kThreads) {
-            if (!one_chunk) {
-                __syncthreads();
-                load_chunk(a, sh, base, false);
-            }
-            const int tiles = sh.first[kThreads];
-            for (int i0 = t - lane; i0 < tiles; i0 += kThreads) {
-                const int i = i0 + lane;
-                int st = 0;
-                if (i < tiles) {
-                    const int k = find_seq(sh, i);
-                    st = tile_steps(Seq{sh.start[k], sh.n[k], sh.len[k]}, a.group, i - sh.first[k]);
-                }
-                for (int c = 0; c < kCand; ++c) {
-                    const int P = max(kMinPart, (maxs + kParts[c] - 1) / kParts[c]);
-                    const int parts = i < tiles ? max(1, (st + P - 1) / P) : 0;
-                    const int all = __reduce_add_sync(0xffffffffu, parts);
-                    const int split = __reduce_add_sync(0xffffffffu, parts > 1 ? parts : 0);
-                    if (lane == 0) {
-                        atomicAdd(&sh.items[c], static_cast<unsigned long long>(all));
-                        atomicAdd(&sh.parts[c], static_cast<unsigned long long>(split));
-                    }
-                }
-            }
+    const bool may_split = a.may_split && cached && maxs > kMinPart && tiles_all * nh < 8ll * a.slots;
+    if (may_split && warp < kCand) {
+        const int P = max(kMinPart, (maxs + kParts[warp] - 1) / kParts[warp]);
+        int all = 0, split = 0;
+        for (int i = lane; i < tiles_all; i += 32) {
+            const int parts = max(1, (sh.steps[i] + P - 1) / P);
+            all += parts;
+            split += parts > 1 ? parts : 0;
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        split = __reduce_add_sync(0xffffffffu, split);
+        if (lane == 0) {
+            sh.items[warp] = all;
+            sh.parts[warp] = split;
         }
     }
     __syncthreads();
-    if (t < 32) {
+    if (warp == 0) {
         long long best = 1ll << 62;
         if (may_split && lane < kCand) {
+            unsigned long long steps = 0;
+            for (int w = 0; w < kWarps; ++w) steps += sh.wsum[w];
             const int P = max(kMinPart, (maxs + kParts[lane] - 1) / kParts[lane]);
             const long long items = sh.items[lane], parts = sh.parts[lane];
-            const bool fits = parts <= a.part_cap && sh.tiles + parts <= a.capacity &&
+            const bool fits = parts <= a.part_cap && tiles_all + parts <= a.capacity &&
                               (maxs + P - 1) / P <= kPrefillMaxParts;
             const long long top = min(P, maxs) + kItemCost + (parts > 0 ? kSplitCost : 0);
-            const long long load = (static_cast<long long>(sh.sum_steps) + kItemCost * items + kSplitCost * parts) * nh;
+            const long long load = (static_cast<long long>(steps) + kItemCost * items + kSplitCost * parts) * nh;
             // in sixteenths of a step, the candidate's index breaking ties towards fewer parts
-            long long est = items * nh <= a.slots ? 16 * top : max(16 * top, 16 * load / a.slots + 8 * top);
+            const long long est = items * nh <= a.slots ? 16 * top : max(16 * top, 16 * load / a.slots + 8 * top);
             if (fits) best = est * 32 + lane;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
         if (lane == 0) {
             const int k = best == (1ll << 62) ? 1 : kParts[best & 31];
-            int P = max(kMinPart, (maxs + k - 1) / k);
-            if (!may_split || k == 1) P = max(1, maxs);
+            const int P = k == 1 ? max(1, maxs) : max(kMinPart, (maxs + k - 1) / k);
             sh.part_len = P;
             sh.max_item = min(P, max(1, maxs));
         }
@@ -223,46 +221,49 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     // ---- items by length: count, offsets, write
     for (int pass = 0; pass < 2; ++pass) {
         for (int base = 0; base < a.num_seqs; base += kThreads) {
-            if (!one_chunk) {
-                __syncthreads();
-                load_chunk(a, sh, base, false);
-            }
+            if (!one_chunk) load_chunk(a, sh, base, false);
             const int tiles = sh.first[kThreads];
             for (int i = t; i < tiles; i += kThreads) {
-                const int k = find_seq(sh, i);
+                int k;
+                const int st = tile_of(i, cached, k);
                 const int tile = i - sh.first[k];
-                const Seq q{sh.start[k], sh.n[k], sh.len[k]};
-                const int st = tile_steps(q, a.group, tile);
                 const int parts = max(1, (st + P - 1) / P);
                 const int len = (st + parts - 1) / parts;           // equal parts
                 int slot = 0;
-                if (pass == 1 && parts > 1) slot = atomicAdd(&sh.next_slot, parts);
+                if (pass == 1 && parts > 1) {
+                    slot = atomicAdd(&sh.next_slot, parts);
+                    a.merges[atomicAdd(&sh.next_merge, 1)] = make_int4(prefill_split(parts, 0, slot), tile, sh.start[k], sh.n[k]);
+                }
                 for (int p = 0; p < parts; ++p) {
-                    const int s0 = p * len, s1 = min(st, s0 + len);
-                    const int b = min(kBuckets - 1, (top - max(0, s1 - s0)) * kBuckets / (top + 1));
+                    const int s0 = min(st, p * len), s1 = min(st, s0 + len);
+                    const int b = min(kBuckets - 1, (top - (s1 - s0)) * kBuckets / (top + 1));
                     if (pass == 0) {
                         atomicAdd(&sh.bucket[b], 1);
                     } else {
                         const int at = atomicAdd(&sh.at[b], 1);
                         if (at < a.capacity) {
-                            a.items[2 * at] = make_int4(base + k, tile, s0, max(s0, s1));
+                            a.items[2 * at] = make_int4(base + k, tile, s0, s1);
                             a.items[2 * at + 1] =
-                                make_int4(q.start, q.n, q.len, parts > 1 ? prefill_split(parts, p, slot) : 0);
+                                make_int4(sh.start[k], sh.n[k], sh.len[k], parts > 1 ? prefill_split(parts, p, slot) : 0);
                         }
                     }
                 }
             }
         }
         __syncthreads();
-        if (pass == 0 && t < 32) {
-            int carry = 0;
-            for (int b0 = 0; b0 < kBuckets; b0 += 32) {
-                const int v = sh.bucket[b0 + lane];
-                const int inc = warp_scan(v);
-                sh.at[b0 + lane] = carry + inc - v;
-                carry += __shfl_sync(0xffffffffu, inc, 31);
+        if (pass == 0) {
+            if (warp == 0) {
+                int carry = 0;
+                for (int b0 = 0; b0 < kBuckets; b0 += 32) {
+                    const int v = sh.bucket[b0 + lane];
+                    const int inc = warp_scan(v);
+                    sh.at[b0 + lane] = carry + inc - v;
+                    carry += __shfl_sync(0xffffffffu, inc, 31);
+                }
+                if (lane == 0) a.header[0] = min(carry, a.capacity);
             }
-            if (lane == 0) a.header[0] = min(carry, a.capacity);
+        } else if (t == 0) {
+            a.header[1] = sh.next_merge;
         }
         __syncthreads();
     }
@@ -275,17 +276,22 @@ PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int 
     PrefillWorkspace w{};
     auto pad = [](size_t x) { return (x + 255) / 256 * 256; };
     const int64_t rows = num_tokens * (num_heads / num_kv_heads);
-    w.part_rows = static_cast<int>(std::min<int64_t>(kPrefillRows, std::max<int64_t>(rows, 1)));
+    w.part_rows = static_cast<int>((std::min<int64_t>(kPrefillRows, std::max<int64_t>(rows, 1)) + 31) / 32 * 32);
     // two parts for every CTA, and one tile split as far as it goes
     w.part_cap = std::max((2 * slots + num_kv_heads - 1) / num_kv_heads, 16);
     w.capacity = static_cast<int>(rows / kPrefillRows + std::min<int64_t>(num_seqs, rows) + w.part_cap);
     const size_t parts = static_cast<size_t>(num_kv_heads) * w.part_cap;
     w.items = 256;
-    w.tickets = w.items + pad(static_cast<size_t>(w.capacity) * 32);
-    w.ml = w.tickets + pad(parts * 2 * sizeof(unsigned));
+    w.merges = w.items + pad(static_cast<size_t>(w.capacity) * 32);
+    w.ml = w.merges + pad(static_cast<size_t>(w.part_cap) * 8);
     w.o = w.ml + pad(parts * w.part_rows * sizeof(float2));
     w.total = w.o + pad(parts * w.part_rows * head_dim * sizeof(float));
     return w;
+}
+
+bool prefill_may_split(int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots) {
+    const int64_t tiles = num_tokens * (num_heads / num_kv_heads) / kPrefillRows;       // at least
+    return max_seq_len > kMinPart * kPrefillStep && tiles * num_kv_heads < 8ll * slots;
 }
 
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
