@@ -447,6 +447,21 @@ PKV_API pkv_status pkv_paged_attention_verify_fp8(void* out, const void* q, cons
                                           size_t workspace_bytes, int partition_tokens, void* stream);
 
 /*
+ * pkv_paged_attention_prefill_fp8: pkv_paged_attention_prefill over uint8 E4M3
+ * pools, with K and V as in pkv_paged_attention_decode_fp8 (the products run in
+ * f16, where every code is exact; a bf16 query is converted to f16).  head_dim
+ * 128 only; the same plan and workspace as the 16-bit call.
+ */
+PKV_API pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void* key_cache,
+                                           const void* value_cache, const int32_t* block_tables,
+                                           int max_blocks_per_seq, const int32_t* seq_lens,
+                                           const int32_t* query_starts, int num_seqs, int64_t num_tokens,
+                                           int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                                           int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
+                                           const float* k_scale, const float* v_scale, void* workspace,
+                                           size_t workspace_bytes, int planned, void* stream);
+
+/*
  * copy_blocks -- the copy-on-write block copy at a fork.
  *
  * P2 §3.1 (the scheduler output's blocks_to_copy, "用于 Copy-on-Write") and

@@ -38,7 +38,7 @@ ABI_SYMBOLS = ("pkv_version", "pkv_last_error", "pkv_paged_kv_append", "pkv_deco
                "pkv_paged_attention_decode_fp8", "pkv_decode_plan", "pkv_paged_attention_decode_planned",
                "pkv_paged_attention_decode_fp8_planned", "pkv_paged_kv_append_decode",
                "pkv_paged_attention_verify_fp8", "pkv_prefill_workspace_bytes", "pkv_prefill_plan",
-               "pkv_paged_attention_prefill")
+               "pkv_paged_attention_prefill", "pkv_paged_attention_prefill_fp8")
 
 _lib = None
 
@@ -103,6 +103,9 @@ def load() -> ctypes.CDLL:
     lib.pkv_paged_attention_prefill.restype = c_i
     lib.pkv_paged_attention_prefill.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i, c_p, c_p, c_i, c_i64, c_i, c_i, c_i, c_i,
                                                 c_i, c_i64, c_f, c_i, c_p, c_sz, c_i, c_p]
+    lib.pkv_paged_attention_prefill_fp8.restype = c_i
+    lib.pkv_paged_attention_prefill_fp8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i, c_p, c_p, c_i, c_i64, c_i, c_i, c_i,
+                                                    c_i, c_i, c_i64, c_f, c_i, c_p, c_p, c_p, c_sz, c_i, c_p]
     lib.pkv_copy_blocks.restype = c_i
     lib.pkv_copy_blocks.argtypes = [ctypes.POINTER(c_p), ctypes.POINTER(c_p), c_i, c_p, c_i64, c_i64, c_i, c_i,
                                     c_i, c_i, c_p]
@@ -469,8 +472,10 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
     query_starts[s] .. query_starts[s + 1] - 1 (int32 [B + 1]), whose K/V are its last positions in the pools; row i
     of n attends over positions [0, seq_lens[s] - n + i].  Rows of no sequence are left as they are.  ``workspace``:
     see ``alloc_prefill_workspace`` (allocated here when omitted); ``planned``: run over the list ``prefill_plan``
-    put there for this batch.  ``max_seq_len`` is read from the device if omitted, which synchronises."""
-    NB, bs, Hkv, d = _pool("key_cache", key_cache)
+    put there for this batch.  ``max_seq_len`` is read from the device if omitted, which synchronises.  uint8 pools hold
+    E4M3 codes and take k_scale / v_scale (float32 [Hkv]) as paged_attention_decode_fp8 does."""
+    kv8 = key_cache.dtype == torch.uint8
+    NB, bs, Hkv, d = _pool("key_cache", key_cache, tuple(_POOL_DT))
     if value_cache.shape != key_cache.shape or value_cache.dtype != key_cache.dtype:
         raise ValueError("value_cache must match key_cache")
     if q.dim() != 3:
@@ -481,7 +486,8 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
     B = seq_lens.shape[0]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    ptrs = [_cuda("out", out, key_cache.dtype), _cuda("q", q, key_cache.dtype), _cuda("key_cache", key_cache),
+    qdt = (torch.float16, torch.bfloat16) if kv8 else key_cache.dtype
+    ptrs = [_cuda("out", out, qdt), _cuda("q", q, out.dtype), _cuda("key_cache", key_cache),
             _cuda("value_cache", value_cache), _cuda("block_tables", block_tables, torch.int32, 2)]
     lens = [_cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("query_starts", query_starts, torch.int32, 1)]
     if block_tables.shape[0] != B or query_starts.shape[0] != B + 1:
@@ -492,10 +498,14 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
         max_seq_len = int(seq_lens.max().item()) if B else 0
     if workspace is None:
         workspace = alloc_prefill_workspace(B, T, Hq, Hkv, d, q.device)
-    _check(load().pkv_paged_attention_prefill(
-        *ptrs, block_tables.shape[1], *lens, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB, float(scale),
-        _DT[key_cache.dtype], _cuda("workspace", workspace), workspace.numel() * workspace.element_size(),
-        PLANNED if planned else 0, _stream(q)))
+    args = [*ptrs, block_tables.shape[1], *lens, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB, float(scale), _DT[q.dtype]]
+    rest = [_cuda("workspace", workspace), workspace.numel() * workspace.element_size(), PLANNED if planned else 0,
+            _stream(q)]
+    if kv8:
+        _check(load().pkv_paged_attention_prefill_fp8(*args, _scales("k_scale", k_scale, Hkv),
+                                                      _scales("v_scale", v_scale, Hkv), *rest))
+    else:
+        _check(load().pkv_paged_attention_prefill(*args, *rest))
 
 
 @_one_device

@@ -677,7 +677,12 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
                         const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
                         const int32_t* query_starts, int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads,
                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
-                        void* workspace, size_t workspace_bytes, int planned, void* stream) {
+                        void* workspace, size_t workspace_bytes, int planned, void* stream,
+                        const float* k_scale = nullptr, const float* v_scale = nullptr) {
+    const bool kv8 = k_scale != nullptr;                 // an E4M3 pool (the _fp8 entry point)
+    if (kv8 && head_dim != 128) return fail(PKV_ERR_UNSUPPORTED, "E4M3 pools: head_dim 128 only");
+    if (kv8 && ((reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u)))
+        return fail(PKV_ERR_INVALID, "k_scale / v_scale must be 4-byte aligned");
     if (planned != 0 && planned != PKV_PLANNED) return fail(PKV_ERR_INVALID, "planned %d: 0 or PKV_PLANNED", planned);
     if (!valid_dtype(dt)) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", static_cast<int>(dt));
     if (!valid_block_size(block_size)) return fail(PKV_ERR_UNSUPPORTED, "block_size %d not built (8, 16, 32)", block_size);
@@ -709,8 +714,11 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.q_tma = pkv::kPrefillSub % a.group == 0;
     CUtensorMap tmq{}, tmk{}, tmv{};
     if (a.q_tma && (st = encode_queries(&tmq, q, num_tokens, num_heads, a.group, head_dim)) != PKV_OK) return st;
-    if ((st = encode_pool(&tmk, key_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return st;
-    if ((st = encode_pool(&tmv, value_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return st;
+    const int eb = kv8 ? 1 : 2;
+    if ((st = encode_pool(&tmk, key_cache, num_blocks, block_size, num_kv_heads, head_dim, eb)) != PKV_OK) return st;
+    if ((st = encode_pool(&tmv, value_cache, num_blocks, block_size, num_kv_heads, head_dim, eb)) != PKV_OK) return st;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = planned ? cudaSuccess : pkv::launch_prefill_plan(a, s);
     if (e == cudaSuccess) e = pkv::launch_prefill(a, tmq, tmk, tmv, dt == PKV_F16 ? 0 : 1, head_dim, s);
@@ -755,6 +763,20 @@ pkv_status pkv_paged_attention_prefill(void* out, const void* q, const void* key
     return prefill_call(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, query_starts,
                         num_seqs, num_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
                         scale, dt, workspace, workspace_bytes, planned, stream);
+}
+
+pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void* key_cache, const void* value_cache,
+                                           const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                           const int32_t* query_starts, int num_seqs, int64_t num_tokens,
+                                           int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                                           int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
+                                           const float* k_scale, const float* v_scale, void* workspace,
+                                           size_t workspace_bytes, int planned, void* stream) {
+    CallRange range_("pkv_paged_attention_prefill_fp8");
+    if (!k_scale || !v_scale) return fail(PKV_ERR_INVALID, "E4M3 pools need k_scale and v_scale");
+    return prefill_call(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, query_starts,
+                        num_seqs, num_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                        scale, dt, workspace, workspace_bytes, planned, stream, k_scale, v_scale);
 }
 
 }  // extern "C"

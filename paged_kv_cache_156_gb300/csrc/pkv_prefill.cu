@@ -37,6 +37,11 @@
 // position per column is noted; the epilogue then gives inf or NaN to exactly
 // the rows that see them.
 //
+// E4M3 pools.  Warp 8 streams tiles of codes, and three warps (10, 12, 14) expand
+// them into the ring as f16, where every code is exact, and clean V on the way;
+// K's scale multiplies the scores, V's the output.  The products run in f16: a
+// bf16 query tile is converted in place by its softmax warps.
+//
 // Every wait is bounded in wall time; a CTA that gives up raises the error
 // word, gives its copies and products in flight time to land and frees its TMEM.
 #include <algorithm>
@@ -53,23 +58,29 @@ namespace {
 constexpr int kStep = kPrefillStep;
 constexpr int kSub = kPrefillSub;
 
-template <int D>
+template <int D, bool KV8 = false>
 struct PfGeo {
     static constexpr int kThreads = 512;
     static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12, kLoadQ = 13, kPlan = 15;   // (9 and 11: MMAs; 12 and 14: cleaning)
     static constexpr int kHalves = D * 2 / 128;             // 128-byte column planes of a tile
     static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
     static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
-    static constexpr int kStages = D == 128 ? 5 : 10;       // ring of K and V tiles, in turn
+    // ring of K and V tiles, in turn; over an E4M3 pool a tile less in favour of two tiles of codes
+    static constexpr int kStages = KV8 ? 4 : D == 128 ? 5 : 10;
+    static constexpr int kCodes = KV8 ? 2 : 0;              // staged tiles of codes (128 rows of D bytes)
+    static constexpr int kCodeTile = 128 * D;
+    static constexpr int kConverters = 3;                   // warps 10, 12 and 14
     static constexpr size_t kRing = 2 * size_t(kTile);      // after the two Q tiles
-    static constexpr size_t kBars = kRing + size_t(kStages) * kTile;
+    static constexpr size_t kCode = kRing + size_t(kStages) * kTile;
+    static constexpr size_t kBars = kCode + size_t(kCodes) * kCodeTile;
     static constexpr int kItems = 4;                        // items decoded ahead
     static constexpr int kItemReaders = 15;                 // warps that read each
-    static constexpr int kNumBars = 3 * kStages + 15 + 2 * kItems;
+    static constexpr int kNumBars = 3 * kStages + 17 + 2 * kItems + 2 * kCodes;
     static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, epilogue count, tags
-    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // [2 warps][+inf, -inf][D] first positions
+    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // first positions of non-finite V elements: [2 warps][+inf, -inf][D], or [3 warps][NaN][D]
     static constexpr size_t kList = kBad + size_t(4) * D * 4;    // [kItems] decoded items
     static constexpr size_t kBytes = kList + kItems * 64;
+    static_assert(!KV8 || D == 128, "E4M3 pools: a row of codes is one 128-byte plane");
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
     // registers a thread: 512 threads start with 128; the softmax warpgroups take 192, the others keep 64
     static constexpr int kRegsSoftmax = 192, kRegsOther = 64;
@@ -228,6 +239,10 @@ __device__ __forceinline__ T from_float(float x) {
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool keep) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(keep ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+}
 // 4 x 4 transposition over a quad: lane q's register i becomes lane i's register q.
 __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4]) {
     const int q = threadIdx.x & 3;
@@ -278,14 +293,16 @@ __device__ __forceinline__ void copy_q(const PrefillArgs& a, const Item& it, int
     __syncwarp();
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
+// T: the products' type; KV8: E4M3 pools (codes expanded to f16, every one exact there); OT: q's and out's.
+template <typename T, int D, bool KV8, typename OT>
+__global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
                                                                         const __grid_constant__ CUtensorMap tmk,
                                                                         const __grid_constant__ CUtensorMap tmv,
                                                                         const PrefillArgs a) {
-    using G = PfGeo<D>;
+    using G = PfGeo<D, KV8>;
     constexpr int ST = G::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool kConvertQ = !std::is_same<T, OT>::value;     // bf16 queries over an E4M3 pool: to f16 in place
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem + G::kRing;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kBars);
@@ -298,25 +315,29 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
     uint64_t* p_full = q_full + 6;                  // [2][2] half a step's P in TMEM, O rescaled (softmax threads)
     uint64_t* o_full = q_full + 10;                 // [2] an item's last O product done (MMA commit)
     uint64_t* turn = q_full + 12;                   // [2] the tile may issue its next round (the other's MMA warp)
-    uint64_t* fin = q_full + 14;                    // every product issued is done (both MMA warps' commits)
-    uint64_t* item_full = q_full + 15;              // [kItems] an item is decoded (plan warp)
+    uint64_t* q_raw = q_full + 14;                  // [2] the tile before its conversion to f16 (kConvertQ)
+    uint64_t* fin = q_full + 16;                    // every product issued is done (both MMA warps' commits)
+    uint64_t* item_full = q_full + 17;              // [kItems] an item is decoded (plan warp)
     uint64_t* item_empty = item_full + G::kItems;   // [kItems] every reader has read it
+    uint64_t* code_full = item_empty + G::kItems;   // [kCodes] a tile of codes landed (TMA bytes)
+    uint64_t* code_empty = code_full + G::kCodes;   // [kCodes] it is expanded (converter warps)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kMisc + 4);
     volatile int* epilogues = abort_flag + 1;       // epilogues finished, counted per softmax warp
-    volatile int* bad_tag = abort_flag + 2;         // [2] the item whose non-finite V elements a warp's table lists (-1: none)
-    int* bad = reinterpret_cast<int*>(smem + G::kBad);      // [2 warps][+inf or NaN | -inf or NaN][D] first positions
+    volatile int* bad_tag = abort_flag + 2;         // [3] the item whose non-finite V elements a warp's table lists (-1: none)
+    int* bad = reinterpret_cast<int*>(smem + G::kBad);      // (kBad)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 4);
+            mbar_init(&full[i], KV8 ? G::kConverters : 1);
+            mbar_init(&empty[i], KV8 ? 2 : 4);
             mbar_init(&clean[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
+            mbar_init(&q_full[i], kConvertQ ? kSub : 1);
+            mbar_init(&q_raw[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[2 * i], kSub);
@@ -328,9 +349,13 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
             mbar_init(&item_full[i], 1);
             mbar_init(&item_empty[i], G::kItemReaders);
         }
+        for (int i = 0; i < G::kCodes; ++i) {
+            mbar_init(&code_full[i], 1);
+            mbar_init(&code_empty[i], G::kConverters);
+        }
         mbar_init(fin, 2);
         *epilogues = 0;
-        bad_tag[0] = bad_tag[1] = -1;
+        bad_tag[0] = bad_tag[1] = bad_tag[2] = -1;
         // the 128B swizzle and the MMA descriptors assume 1 KB aligned tiles
         const bool misaligned = (smem_u32(smem) & 1023u) != 0;
         if (misaligned) raise_error(a.err, kErrTimeout);
@@ -361,7 +386,133 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
 
     if (warp >= 8) {
         regs_dec<G::kRegsOther>();
-        if (warp == G::kLoadK || warp == G::kLoadV) {
+        if (KV8 && warp == G::kLoadK) {
+            // ======================================================== tiles of E4M3 codes, K and V in turn
+            const int bs = a.block_size;
+            const bool leader = elect_one();
+            Ring<G::kCodes> c;
+            Item it;
+            bool ok = !*abort_flag;
+            if (leader) {
+                prefetch_tensormap(&tmk);
+                prefetch_tensormap(&tmv);
+            }
+            for (int r = 0; ok && get_item(r, it, ok); ++r) {
+                const int n = it.steps(), stop = it.stop();
+                const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
+                auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
+                    const int pos = (it.step0 + j) * kStep + lane * bs;
+                    return lane * bs < kStep && j < n && pos < stop ? __ldcg(trow + pos / bs) : -1;
+                };
+                int nxt = id_of(0);
+                for (int j = 0; j < n && ok; ++j) {
+                    int id = nxt;
+                    nxt = id_of(j + 1);
+                    const int tok0 = (it.step0 + j) * kStep;
+                    const int nb = (min(stop, tok0 + kStep) - tok0 + bs - 1) / bs;
+                    if (lane < nb && (id < 0 || static_cast<int64_t>(id) >= a.num_blocks)) {
+                        raise_error(a.err, kErrBounds);
+                        id = -1;
+                    }
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = wait_bar(&code_empty[c.slot], c.phase ^ 1, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const int slot = __shfl_sync(0xffffffffu, c.slot, 0);
+                        if (leader) mbar_arrive_expect_tx(&code_full[slot], static_cast<unsigned>(nb * bs * D));
+                        uint8_t* dst = smem + G::kCode + slot * G::kCodeTile;
+                        for (int b = 0; b < nb; ++b) {
+                            const int pb = __shfl_sync(0xffffffffu, id, b);
+                            if (leader) tma_load_4d(dst + b * bs * D, kv ? &tmv : &tmk, 0, it.kvh, 0, pb, &code_full[slot]);
+                        }
+                        c.next();
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                dec::raise_abort(a.err, abort_flag);
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
+            }
+        } else if (KV8 && (warp == G::kLoadV || warp == G::kClean || warp == G::kClean + 2)) {
+            // ======================================================== codes to f16, V cleaned on the way
+            // A lane takes 16 codes (one 128-byte row over 8 lanes) and writes two 16-byte pieces; the lanes
+            // of a row's second half write theirs in the other order, so that no two meet in a bank.
+            const int cw = (warp - G::kLoadV) / 2;
+            int* mine = bad + cw * D;
+            const int ch = lane & 7, sub = lane >> 3;
+            Ring<ST> c;
+            Ring<G::kCodes> q;
+            Item it;
+            bool ok = !*abort_flag;
+            for (int r = 0; ok && get_item(r, it, ok); ++r) {
+                const int n = it.steps();
+                for (int t = 0; t < 2 * n && ok; ++t) {      // K and V of step t / 2
+                    int lo, nv, nv16;
+                    it.partial(t >> 1, lo, nv, nv16);
+                    const bool look = (t & 1) && lo < nv;    // V that some row does not see
+                    const int tok0 = (it.step0 + (t >> 1)) * kStep;
+                    ok = wait_bar(&code_full[q.slot], q.phase, abort_flag) && wait_bar(&empty[c.slot], c.phase ^ 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t src = smem_u32(smem + G::kCode + q.slot * G::kCodeTile), dst = smem_u32(ring + c.slot * G::kTile);
+#pragma unroll 2
+                    for (int g = cw; g < kStep / 4; g += G::kConverters) {
+                        const int row = 4 * g + sub;
+                        uint32_t x[4];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(dec::swz(src, row, ch)));
+                        if (4 * g + 3 >= nv && row >= nv) x[0] = x[1] = x[2] = x[3] = 0u;      // slots past the end
+                        if (look && 4 * g + 3 >= lo) {
+                            uint32_t hit = 0;                // (a code of seven ones is NaN)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) hit |= ((x[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                            if (row < lo) hit = 0;
+                            if (__any_sync(0xffffffffu, hit != 0)) {                           // rare
+                                if (bad_tag[cw] != r) {
+                                    const unsigned long long t0 = globaltimer_ns();
+                                    while (*epilogues < 8 * r && !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
+                                    for (int k = lane; k < D; k += 32) mine[k] = 0x7fffffff;
+                                    __syncwarp();
+                                    if (lane == 0) bad_tag[cw] = r;
+                                    __syncwarp();
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    for (int b = 0; b < 4 && hit != 0; ++b) {
+                                        if ((x[e] >> (8 * b) & 0x7fu) != 0x7fu) continue;
+                                        atomicMin(&mine[16 * ch + 4 * e + b], tok0 + row);
+                                        x[e] &= ~(0xffu << (8 * b));
+                                    }
+                                }
+                            }
+                        }
+                        uint32_t h[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = e4m3x2_to_f16x2(x[e >> 1] >> (16 * (e & 1)));
+                        const uint32_t plane = dst + (ch >> 2) * G::kPlane;
+                        const int c0 = 2 * (ch & 3) + (ch >> 2), c1 = c0 ^ 1;
+                        const bool back = (ch >> 2) != 0;    // (the piece with the later elements first)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dec::swz(plane, row, c0)),
+                                     "r"(back ? h[4] : h[0]), "r"(back ? h[5] : h[1]), "r"(back ? h[6] : h[2]), "r"(back ? h[7] : h[3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dec::swz(plane, row, c1)),
+                                     "r"(back ? h[0] : h[4]), "r"(back ? h[1] : h[5]), "r"(back ? h[2] : h[6]), "r"(back ? h[3] : h[7])
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&full[c.slot]);
+                        mbar_arrive(&code_empty[q.slot]);
+                    }
+                    c.next();
+                    q.next();
+                }
+            }
+            if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
+        } else if (warp == G::kLoadK || warp == G::kLoadV) {
             // ======================================================== the K/V ring: one warp for K, one for V
             // An elected lane issues the boxes one after another (some 40 cycles each; left to the lanes
             // side by side the compiler serialises them at 65, and one warp for both K and V then took
@@ -445,7 +596,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                         ok = wait(&full[v.slot], v.phase);
                         int lo, nv, nv16;
                         it.partial(j, lo, nv, nv16);
-                        if (ok && lo < nv16) {               // V that some row sees only in part
+                        if (!KV8 && ok && lo < nv16) {       // V that some row sees only in part
                             ok = wait(&clean[v.slot], v.phase);
                         }
                     }
@@ -534,14 +685,15 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                         // their scores go nowhere)
                         const int tok = it.qs + (2 * it.tile + i) * sub_tokens;
                         if (leader) {
-                            mbar_arrive_expect_tx(&q_full[i], G::kTile);
+                            uint64_t* bar = kConvertQ ? &q_raw[i] : &q_full[i];
+                            mbar_arrive_expect_tx(bar, G::kTile);
 #pragma unroll
                             for (int hf = 0; hf < G::kHalves; ++hf)
-                                tma_load_4d(dst + hf * G::kPlane, &tmq, hf * 64, it.kvh * a.group, tok, 0, &q_full[i]);
+                                tma_load_4d(dst + hf * G::kPlane, &tmq, hf * 64, it.kvh * a.group, tok, 0, bar);
                         }
                     } else {
                         copy_q<T, D>(a, it, i, smem_u32(dst));
-                        if (leader) mbar_arrive(&q_full[i]);
+                        if (leader) mbar_arrive(kConvertQ ? &q_raw[i] : &q_full[i]);
                     }
                 }
             }
@@ -682,10 +834,8 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
         const int t = threadIdx.x & 127;
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t ts = tl + G::kColS + wg * 128, to = tl + G::kColO + wg * 128;
-        const float sl2 = a.scale_log2;
-        const uint64_t sl2x2 = pack64(sl2, sl2);
-        T* out = static_cast<T*>(a.out);
-        unsigned ns = 0, no = 0;
+        OT* out = static_cast<OT*>(a.out);
+        unsigned ns = 0, no = 0, nraw = 0;
         Item it;
         bool ok = !*abort_flag;
 #pragma unroll 1
@@ -699,6 +849,34 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
             const int n = it.steps_of(wg);
             const int seen = min(lim, it.end_of(wg));           // (dummy rows too stop at the tile's end)
             float m_ref = -INFINITY, l = 0.0f;
+            const float sl2 = KV8 ? a.scale_log2 * __ldcg(a.k_scale + it.kvh) : a.scale_log2;
+            const uint64_t sl2x2 = pack64(sl2, sl2);
+            if constexpr (kConvertQ) {
+                if (n > 0) {                                 // the tile's bf16 queries to f16, in place
+                    ok = wait_bar(&q_raw[wg], nraw & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ++nraw;
+                    if (!ok) break;
+                    const uint32_t tile = smem_u32(smem + wg * G::kTile) + 16 * t;
+#pragma unroll 4
+                    for (int i = 0; i < G::kTile; i += 16 * kSub) {
+                        uint32_t x[4];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(tile + i));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = Mma<OT>::unpack(x[e]);
+                            x[e] = Mma<T>::pack(f.x, f.y);
+                        }
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + i), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                                     "r"(x[3])
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&q_full[wg]);
+                }
+            }
             for (int j = 0; j < n; ++j) {
                 ok = wait_bar(&s_full[wg], ns & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -780,6 +958,7 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                 ++no;
                 if (!ok) break;
                 tc::fence_after_sync();
+                const float vs = KV8 ? __ldcg(a.v_scale + it.kvh) : 1.0f;
                 if (split) {
                     // a row a thread, 16 bytes of 32 neighbouring rows side by side
 #pragma unroll 1
@@ -791,15 +970,15 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 prow[static_cast<int64_t>(c0 / 4 + k) * a.part_rows] =
-                                    make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                                    make_float4(__uint_as_float(o[4 * k]) * vs, __uint_as_float(o[4 * k + 1]) * vs,
+                                                __uint_as_float(o[4 * k + 2]) * vs, __uint_as_float(o[4 * k + 3]) * vs);
                         }
                     }
                 } else {
                     // The 16x256b shape gives a quad two rows' columns; transposed over the quad, four lanes
                     // write 64 contiguous bytes of a row (a row a thread would touch 32 lines a store, 2 us
                     // an item in the load-store unit).
-                    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;             // (a NaN sum stays)
+                    const float inv = l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l;              // (a NaN sum stays)
 #pragma unroll 1
                     for (int hh = 0; hh < 2; ++hh) {
                         const int ra = 16 * hh + (lane >> 2);                                 // rows ra and ra + 8 of the warp
@@ -816,8 +995,8 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const uint32_t* y = &o[4 * (g + e)];
-                                    wa[e] = Mma<T>::pack(__uint_as_float(y[0]) * ia, __uint_as_float(y[1]) * ia);
-                                    wb[e] = Mma<T>::pack(__uint_as_float(y[2]) * ib, __uint_as_float(y[3]) * ib);
+                                    wa[e] = Mma<OT>::pack(__uint_as_float(y[0]) * ia, __uint_as_float(y[1]) * ia);
+                                    wb[e] = Mma<OT>::pack(__uint_as_float(y[2]) * ib, __uint_as_float(y[3]) * ib);
                                 }
                                 quad_transpose(wa);
                                 quad_transpose(wb);
@@ -831,17 +1010,23 @@ __global__ void __launch_bounds__(PfGeo<D>::kThreads, 1) prefill_kernel(const __
                     }
                 }
                 tc::fence_before_sync();
-                const bool bad0 = bad_tag[0] == r, bad1 = bad_tag[1] == r;
-                if (bad0 || bad1) {                          // rare: V elements that the cleaning warps took out
+                const bool bad0 = bad_tag[0] == r, bad1 = bad_tag[1] == r, bad2 = KV8 && bad_tag[2] == r;
+                if (bad0 || bad1 || bad2) {                  // rare: V elements that were cleaned away
                     __syncwarp();
 #pragma unroll 1
                     for (int c = 0; has && c < D; ++c) {
-                        const bool up = (bad0 && bad[c] < seen) || (bad1 && bad[2 * D + c] < seen);
-                        const bool down = (bad0 && bad[D + c] < seen) || (bad1 && bad[3 * D + c] < seen);
+                        bool up, down;
+                        if (KV8) {
+                            up = (bad0 && bad[c] < seen) || (bad1 && bad[D + c] < seen) || (bad2 && bad[2 * D + c] < seen);
+                            down = up;
+                        } else {
+                            up = (bad0 && bad[c] < seen) || (bad1 && bad[2 * D + c] < seen);
+                            down = (bad0 && bad[D + c] < seen) || (bad1 && bad[3 * D + c] < seen);
+                        }
                         if (!up && !down) continue;
                         const float x = (up ? INFINITY : 0.0f) + (down ? -INFINITY : 0.0f);
                         if (split) reinterpret_cast<float*>(prow + static_cast<int64_t>(c / 4) * a.part_rows)[c & 3] += x;
-                        else out[static_cast<int64_t>(at) * D + c] = from_float<T>(x);
+                        else out[static_cast<int64_t>(at) * D + c] = from_float<OT>(x);
                     }
                 }
             } else if (has && !split) {                      // rows that see nothing
@@ -943,12 +1128,12 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool KV8 = false, typename OT = T>
 cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                      cudaStream_t s) {
-    using G = PfGeo<D>;
+    using G = PfGeo<D, KV8>;
     static_assert(G::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
-    auto kern = prefill_kernel<T, D>;
+    auto kern = prefill_kernel<T, D, KV8, OT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kBytes));
     if (e != cudaSuccess) return e;
     // the warpgroups' register split must fit what a block is launched with, or it would wait for ever
@@ -975,13 +1160,16 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtenso
     cfg.gridDim = dim3(static_cast<unsigned>(2 * a.slots));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<T, D>, a);
+    return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<OT, D>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            int dtype, int head_dim, cudaStream_t s) {
+    if (a.k_scale)
+        return dtype == 0 ? launch_t<__half, 128, true>(a, tmq, tmk, tmv, s)
+                          : launch_t<__half, 128, true, __nv_bfloat16>(a, tmq, tmk, tmv, s);
     if (dtype == 0)
         return head_dim == 128 ? launch_t<__half, 128>(a, tmq, tmk, tmv, s) : launch_t<__half, 64>(a, tmq, tmk, tmv, s);
     return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(a, tmq, tmk, tmv, s) : launch_t<__nv_bfloat16, 64>(a, tmq, tmk, tmv, s);

@@ -70,8 +70,8 @@ def build(news, totals, heads, kv_heads, dim, block, dtype="bf16", seed=0, scale
     if e4m3:
         ks = torch.rand(kv_heads, generator=g) * 0.02 + 0.01
         vs = torch.rand(kv_heads, generator=g) * 0.02 + 0.01
-        kc = (kf / ks[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
-        vc = (vf / vs[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+        kc = (kf / ks[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        vc = (vf / vs[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
     else:
         kc, vc = kf.to(dt), vf.to(dt)
     return Batch(q, kc, vc, tables, torch.tensor(totals, dtype=torch.int32), torch.tensor(starts, dtype=torch.int32),

@@ -28,7 +28,8 @@ def _clean_error_word():
 
 def run(b, **kw):
     out = torch.full_like(b.q, math.nan)
-    pkv.paged_attention_prefill(out, b.q, b.kc, b.vc, b.tables, b.lens, b.starts, b.scale, max_seq_len=b.max_len, **kw)
+    pkv.paged_attention_prefill(out, b.q, b.kc, b.vc, b.tables, b.lens, b.starts, b.scale, max_seq_len=b.max_len,
+                                k_scale=b.k_scale, v_scale=b.v_scale, **kw)
     return out
 
 
@@ -325,3 +326,58 @@ def test_repeats_bit_for_bit():
     first = run(b)
     for _ in range(5):
         assert torch.equal(run(b).view(torch.int16), first.view(torch.int16))
+
+
+E4M3_CASES = ["two_blocks", "tile_edges_g1", "tile_edges_g4", "group_7", "empty_sequences", "nothing_seen", "decode_rows",
+              "mixed", "long_cache"]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("name", E4M3_CASES)
+def test_e4m3_matches_the_reference(name, dtype):
+    """The products run in f16 whatever the queries' type: the weights round there."""
+    news, totals, heads, kv_heads, dim, block, _ = CASES[name]
+    b = build(news, totals, heads, kv_heads, 128, block, dtype, seed=len(name), pad_rows=3, gap=2, e4m3=True)
+    ref, bound = reference(b, torch.float16)
+    out = run(b.to("cuda"))
+    torch.cuda.synchronize()
+    worst = check(out, ref, bound, name)
+    print(f"{name}: {worst:.3f} of the bound")
+
+
+def test_e4m3_codes_a_token_does_not_see():
+    """NaN codes in the last new token's K and V: earlier tokens are the clean run's bit for bit; the token itself
+    has NaN in the columns whose V holds one."""
+    def batch():
+        return build([300, 5, 1], [700, 900, 257], 8, 2, 128, 16, "bf16", seed=5, e4m3=True)
+    clean = run(batch().to("cuda"))
+    b = batch()
+    for s, total in enumerate([700, 900, 257]):
+        blk = int(b.tables[s, (total - 1) // 16])
+        b.vc[blk, (total - 1) % 16, 1, 5] = 0x7f
+        b.vc[blk, (total - 1) % 16, 1, 70] = 0xff
+    got = run(b.to("cuda"))
+    torch.cuda.synchronize()
+    for s, n in enumerate([300, 5, 1]):
+        r0 = int(b.starts[s])
+        assert torch.equal(got[r0:r0 + n - 1].view(torch.int16), clean[r0:r0 + n - 1].view(torch.int16))
+        last = got[r0 + n - 1]
+        assert torch.isnan(last[4:, [5, 70]]).all()
+        assert torch.isnan(last).sum() == 8
+    b.kc[int(b.tables[1, 899 // 16]), 899 % 16] = 0x7f
+    got = run(b.to("cuda"))
+    torch.cuda.synchronize()
+    assert torch.isnan(got[304]).all() and torch.equal(got[300:304].view(torch.int16), clean[300:304].view(torch.int16))
+
+
+def test_e4m3_scales_and_planned():
+    b = build([64, 1, 130], [64, 900, 400], 8, 4, 128, 16, "bf16", seed=9, scale=-0.2, e4m3=True)
+    b.k_scale *= torch.tensor([1.0, 3.0, 0.2, 1.0])
+    b.v_scale *= torch.tensor([1.0, 0.1, 20.0, 1.0])
+    ref, bound = reference(b, torch.float16)
+    c = b.to("cuda")
+    ws = pkv.alloc_prefill_workspace(3, 195, 8, 4, 128)
+    pkv.prefill_plan(ws, c.lens, c.starts, 195, 8, 4, 128, c.max_len)
+    out = run(c, workspace=ws, planned=True)
+    torch.cuda.synchronize()
+    check(out, ref, bound)
