@@ -62,7 +62,8 @@ typedef enum {
 /* Element types.  PKV_E4M3 (8-bit OCP FP8 E4M3 codes) is a pool type only:
  * accepted by pkv_copy_blocks / pkv_swap_blocks and as the pool of the
  * *_fp8 calls, never for q, out or new K/V. */
-typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_E4M3 = 2 } pkv_dtype;
+/* PKV_F32 is a type of probabilities only (pkv_speculative_accept). */
+typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_E4M3 = 2, PKV_F32 = 3 } pkv_dtype;
 
 /* Library ABI version (major * 100 + minor). */
 PKV_API int pkv_version(void);
@@ -460,6 +461,79 @@ PKV_API pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, con
                                            int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
                                            const float* k_scale, const float* v_scale, void* workspace,
                                            size_t workspace_bytes, int planned, void* stream);
+
+/*
+ * paged_kv_gather -- a batch's cached K/V read back into dense rows.
+ *
+ * The inverse of the slot writes (P2 §2.3), through the same block tables
+ * (P4 §2.1): for every sequence s and position t < seq_lens[s]
+ *     k_out[row_starts[s] + t] = K_t,  v_out[row_starts[s] + t] = V_t,
+ * bit for bit.  For handing a cached prefix to another process, or to a
+ * kernel that takes dense rows.
+ *
+ *   k_out, v_out  [num_rows][num_kv_heads][head_dim], dtype `dt`; rows that no
+ *                 position maps to are left as they were
+ *   row_starts    int32 [num_seqs + 1], not decreasing, in [0, num_rows];
+ *                 row_starts[s + 1] - row_starts[s] >= seq_lens[s] (positions
+ *                 past it are not written; either failing raises the error
+ *                 word's bounds bit)
+ *   block_tables  int32 [num_seqs][max_blocks_per_seq] (a position whose table
+ *                 entry is out of range is not written and raises the bit)
+ * Any block_size; head_dim a multiple of 8; num_rows below 2^31.
+ *
+ * pkv_paged_kv_gather_fp8: over uint8 E4M3 pools (P3 §6.2);
+ * element = dt(e4m3_value(code) * scale[kv_head]), the product in float32,
+ * rounded to nearest even; NaN codes give NaN.  Caches 8-byte aligned.
+ */
+PKV_API pkv_status pkv_paged_kv_gather(void* k_out, void* v_out, const void* key_cache, const void* value_cache,
+                               const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                               const int32_t* row_starts, int num_seqs, int64_t num_rows, int64_t num_blocks,
+                               int block_size, int num_kv_heads, int head_dim, pkv_dtype dt, void* stream);
+
+PKV_API pkv_status pkv_paged_kv_gather_fp8(void* k_out, void* v_out, const void* key_cache, const void* value_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* row_starts, int num_seqs, int64_t num_rows, int64_t num_blocks,
+                                   int block_size, int num_kv_heads, int head_dim, pkv_dtype dt,
+                                   const float* k_scale, const float* v_scale, void* stream);
+
+/*
+ * speculative_accept -- drafted tokens against the target's probabilities.
+ *
+ * P3 §4.2 (speculative_verify: a draft is accepted with probability
+ * min(1, p / q), else the token is drawn again from the normalised positive
+ * part of p - q); P1 §4.4.2.  What follows pkv_paged_attention_verify once the
+ * target's probabilities at the drafts' positions are there.  For sequence s
+ * with n = num_drafts[s] drafts x_0 .. x_{n-1}, u = uniform[s]:
+ *     a = the number of leading drafts with u_i * q_i(x_i) < p_i(x_i)
+ *     weights  w = max(p_a - q_a, 0) if a < n, else p_n
+ *     y = the first token whose inclusive sum of w exceeds u_K times their total
+ *     tokens[s] = x_0 .. x_{a-1}, y, then -1;  num_accepted[s] = a
+ * Without draft_probs a draft counts as certain: q_i(x_i) = 1, and w is p_a
+ * without x_a.  When w sums to nothing, p_a's own weights are taken; when those
+ * do too, y is -1.
+ * The comparison is exact.  The sums are exact too: each weight (fp32
+ * difference, clipped to [0, 1], NaN as 0) counts in whole units of 2^-44,
+ * rounded down, so the answer does not depend on an order of summation; the
+ * mark is floor(fp64(u_K) * fp64(total)).
+ *
+ *   tokens        int64 [num_seqs][max_drafts + 1]
+ *   num_accepted  int32 [num_seqs]
+ *   draft_tokens  int64 [num_seqs][max_drafts]; a token outside [0, vocab) is
+ *                 refused and raises the error word's bounds bit
+ *   num_drafts    int32 [num_seqs], each in [0, max_drafts] (clipped to it, with
+ *                 the bounds bit), or NULL: max_drafts for every sequence
+ *   target_probs  [num_seqs][max_drafts + 1][vocab], dtype `dt` (PKV_F32, PKV_F16
+ *                 or PKV_BF16)
+ *   draft_probs   [num_seqs][max_drafts][vocab], dtype `dt`, or NULL
+ *   uniform       float32 [num_seqs][max_drafts + 1] in [0, 1): entry i decides
+ *                 draft i, entry max_drafts the draw of y
+ * vocab up to PKV_ACCEPT_MAX_VOCAB, max_drafts up to 1024.
+ */
+#define PKV_ACCEPT_MAX_VOCAB 524288
+PKV_API pkv_status pkv_speculative_accept(int64_t* tokens, int32_t* num_accepted, const int64_t* draft_tokens,
+                                  const int32_t* num_drafts, const void* target_probs, const void* draft_probs,
+                                  const float* uniform, int num_seqs, int max_drafts, int64_t vocab, pkv_dtype dt,
+                                  void* stream);
 
 /*
  * copy_blocks -- the copy-on-write block copy at a fork.

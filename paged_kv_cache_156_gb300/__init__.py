@@ -27,6 +27,8 @@ _DT = {torch.float16: 0, torch.bfloat16: 1}
 _POOL_DT = {torch.float16: 0, torch.bfloat16: 1, torch.uint8: 2}   # uint8 pools hold E4M3 codes
 PLAN_MAX_SEQS = 1024        # PKV_PLAN_MAX_SEQS: batches up to this size run through the plan kernel
 PLANNED = 1                 # PKV_PLANNED: run over the plan an earlier call wrote
+_PROB_DT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 3}   # PKV_F32: probabilities only
+ACCEPT_MAX_VOCAB = 524288   # PKV_ACCEPT_MAX_VOCAB
 INPUTS_READY = 2            # PKV_INPUTS_READY: nothing pending writes the pools, tables, lengths or plan
 
 # every symbol include/pkv.h declares
@@ -38,7 +40,8 @@ ABI_SYMBOLS = ("pkv_version", "pkv_last_error", "pkv_paged_kv_append", "pkv_deco
                "pkv_paged_attention_decode_fp8", "pkv_decode_plan", "pkv_paged_attention_decode_planned",
                "pkv_paged_attention_decode_fp8_planned", "pkv_paged_kv_append_decode",
                "pkv_paged_attention_verify_fp8", "pkv_prefill_workspace_bytes", "pkv_prefill_plan",
-               "pkv_paged_attention_prefill", "pkv_paged_attention_prefill_fp8")
+               "pkv_paged_attention_prefill", "pkv_paged_attention_prefill_fp8", "pkv_paged_kv_gather",
+               "pkv_paged_kv_gather_fp8", "pkv_speculative_accept")
 
 _lib = None
 
@@ -106,6 +109,14 @@ def load() -> ctypes.CDLL:
     lib.pkv_paged_attention_prefill_fp8.restype = c_i
     lib.pkv_paged_attention_prefill_fp8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i, c_p, c_p, c_i, c_i64, c_i, c_i, c_i,
                                                     c_i, c_i, c_i64, c_f, c_i, c_p, c_p, c_p, c_sz, c_i, c_p]
+    lib.pkv_paged_kv_gather.restype = c_i
+    lib.pkv_paged_kv_gather.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i, c_p, c_p, c_i, c_i64, c_i64, c_i, c_i, c_i, c_i,
+                                        c_p]
+    lib.pkv_paged_kv_gather_fp8.restype = c_i
+    lib.pkv_paged_kv_gather_fp8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i, c_p, c_p, c_i, c_i64, c_i64, c_i, c_i, c_i,
+                                            c_i, c_p, c_p, c_p]
+    lib.pkv_speculative_accept.restype = c_i
+    lib.pkv_speculative_accept.argtypes = [c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_i, c_i, c_i64, c_i, c_p]
     lib.pkv_copy_blocks.restype = c_i
     lib.pkv_copy_blocks.argtypes = [ctypes.POINTER(c_p), ctypes.POINTER(c_p), c_i, c_p, c_i64, c_i64, c_i, c_i,
                                     c_i, c_i, c_p]
@@ -506,6 +517,65 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
                                                       _scales("v_scale", v_scale, Hkv), *rest))
     else:
         _check(load().pkv_paged_attention_prefill(*args, *rest))
+
+
+@_one_device
+def paged_kv_gather(k_out, v_out, key_cache, value_cache, block_tables, seq_lens, row_starts, k_scale=None,
+                    v_scale=None) -> None:
+    """Rows row_starts[s] + t of k_out, v_out ([R, Hkv, d]) = position t < seq_lens[s] of sequence s (row_starts
+    int32 [B + 1]; other rows are left as they are).  uint8 pools hold E4M3 codes and take k_scale / v_scale
+    (float32 [Hkv]): the rows are then code value * scale, rounded to the outputs' fp16 / bf16."""
+    kv8 = key_cache.dtype == torch.uint8
+    NB, bs, Hkv, d = _pool("key_cache", key_cache, tuple(_POOL_DT))
+    if value_cache.shape != key_cache.shape or value_cache.dtype != key_cache.dtype:
+        raise ValueError("value_cache must match key_cache")
+    odt = (torch.float16, torch.bfloat16) if kv8 else key_cache.dtype
+    ptrs = [_cuda("k_out", k_out, odt, 3), _cuda("v_out", v_out, k_out.dtype, 3), _cuda("key_cache", key_cache),
+            _cuda("value_cache", value_cache), _cuda("block_tables", block_tables, torch.int32, 2)]
+    R = k_out.shape[0]
+    if tuple(k_out.shape) != (R, Hkv, d) or tuple(v_out.shape) != (R, Hkv, d):
+        raise ValueError("k_out and v_out must be [rows, num_kv_heads, head_dim]")
+    lens = [_cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("row_starts", row_starts, torch.int32, 1)]
+    B = seq_lens.shape[0]
+    if block_tables.shape[0] != B or row_starts.shape[0] != B + 1:
+        raise ValueError("block_tables must have num_seqs rows and row_starts num_seqs + 1 entries")
+    args = [*ptrs, block_tables.shape[1], *lens, B, R, NB, bs, Hkv, d, _DT[k_out.dtype]]
+    if kv8:
+        _check(load().pkv_paged_kv_gather_fp8(*args, _scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv),
+                                              _stream(key_cache)))
+    else:
+        _check(load().pkv_paged_kv_gather(*args, _stream(key_cache)))
+
+
+@_one_device
+def speculative_accept(tokens, num_accepted, draft_tokens, target_probs, uniform, draft_probs=None,
+                       num_drafts=None) -> None:
+    """Accept drafted tokens against the target's probabilities and draw the token that follows.
+
+    draft_tokens int64 [B, K]; target_probs [B, K + 1, V] and draft_probs [B, K, V] (None: drafts without
+    probabilities, taken as certain) float32 / float16 / bfloat16; uniform float32 [B, K + 1] in [0, 1): entry
+    i < K decides draft i, entry K the draw; num_drafts int32 [B] (None: K each).  tokens int64 [B, K + 1]
+    receives the accepted drafts, the drawn token, then -1; num_accepted int32 [B] the count of drafts kept."""
+    ptrs = [_cuda("tokens", tokens, torch.int64, 2), _cuda("num_accepted", num_accepted, torch.int32, 1),
+            _cuda("draft_tokens", draft_tokens, torch.int64, 2)]
+    target = _cuda("target_probs", target_probs, tuple(_PROB_DT), 3)
+    B, K = draft_tokens.shape
+    V = target_probs.shape[2]
+    if tuple(target_probs.shape) != (B, K + 1, V) or tuple(tokens.shape) != (B, K + 1) or num_accepted.shape[0] != B:
+        raise ValueError("target_probs must be [B, K + 1, V], tokens [B, K + 1] and num_accepted [B]")
+    if tuple(uniform.shape) != (B, K + 1):
+        raise ValueError("uniform must be [B, K + 1]")
+    counts = draft = None
+    if num_drafts is not None:
+        counts = _cuda("num_drafts", num_drafts, torch.int32, 1)
+        if num_drafts.shape[0] != B:
+            raise ValueError("num_drafts must be [B]")
+    if draft_probs is not None:
+        draft = _cuda("draft_probs", draft_probs, target_probs.dtype, 3)
+        if tuple(draft_probs.shape) != (B, K, V):
+            raise ValueError("draft_probs must be [B, K, V]")
+    _check(load().pkv_speculative_accept(*ptrs, counts, target, draft, _cuda("uniform", uniform, torch.float32, 2), B, K,
+                                         V, _PROB_DT[target_probs.dtype], _stream(tokens)))
 
 
 @_one_device

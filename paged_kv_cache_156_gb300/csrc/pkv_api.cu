@@ -783,6 +783,120 @@ pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void*
 
 namespace {
 
+pkv_status gather_call(void* k_out, void* v_out, const void* key_cache, const void* value_cache,
+                       const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                       const int32_t* row_starts, int num_seqs, int64_t num_rows, int64_t num_blocks, int block_size,
+                       int num_kv_heads, int head_dim, pkv_dtype dt, const float* k_scale, const float* v_scale,
+                       void* stream) {
+    if (!valid_dtype(dt)) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", static_cast<int>(dt));
+    if (num_seqs < 0 || num_rows < 0 || num_rows >= (int64_t(1) << 31))
+        return fail(PKV_ERR_INVALID, "num_seqs %d / num_rows %lld (at least 0, rows below 2^31)", num_seqs,
+                    static_cast<long long>(num_rows));
+    if (num_kv_heads <= 0 || head_dim <= 0 || head_dim % 8 != 0)
+        return fail(PKV_ERR_INVALID, "num_kv_heads %d / head_dim %d (head_dim must be a positive multiple of 8)",
+                    num_kv_heads, head_dim);
+    if (static_cast<int64_t>(num_kv_heads) * head_dim > (1 << 24))
+        return fail(PKV_ERR_INVALID, "num_kv_heads * head_dim above 2^24");
+    if (block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq < 0)
+        return fail(PKV_ERR_INVALID, "block_size %d / num_blocks %lld / max_blocks_per_seq %d", block_size,
+                    static_cast<long long>(num_blocks), max_blocks_per_seq);
+    if (num_seqs == 0 || num_rows == 0) return ok();
+    if (!k_out || !v_out || !key_cache || !value_cache || !block_tables || !seq_lens || !row_starts)
+        return fail(PKV_ERR_INVALID, "null pointer");
+    const unsigned pool_align = k_scale ? 7u : 15u;
+    if (!aligned16(k_out) || !aligned16(v_out) || (reinterpret_cast<uintptr_t>(key_cache) & pool_align) ||
+        (reinterpret_cast<uintptr_t>(value_cache) & pool_align) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+        (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(row_starts) & 3u) ||
+        (reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u))
+        return fail(PKV_ERR_INVALID, "outputs and 16-bit caches 16-byte aligned, E4M3 caches 8-byte, the rest 4-byte");
+    pkv::GatherArgs a{};
+    a.k_out = static_cast<uint4*>(k_out);
+    a.v_out = static_cast<uint4*>(v_out);
+    a.key_cache = key_cache;
+    a.value_cache = value_cache;
+    a.block_tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.row_starts = row_starts;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.num_rows = num_rows;
+    a.num_blocks = num_blocks;
+    a.num_seqs = num_seqs;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_size = block_size;
+    a.row_vecs = num_kv_heads * head_dim / 8;
+    a.head_vecs = head_dim / 8;
+    a.bf16 = dt == PKV_BF16;
+    a.err = error_word(current_device());
+    cudaError_t e = pkv::launch_gather(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "gather launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_paged_kv_gather(void* k_out, void* v_out, const void* key_cache, const void* value_cache,
+                               const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                               const int32_t* row_starts, int num_seqs, int64_t num_rows, int64_t num_blocks,
+                               int block_size, int num_kv_heads, int head_dim, pkv_dtype dt, void* stream) {
+    CallRange range_("pkv_paged_kv_gather");
+    return gather_call(k_out, v_out, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, row_starts,
+                       num_seqs, num_rows, num_blocks, block_size, num_kv_heads, head_dim, dt, nullptr, nullptr, stream);
+}
+
+pkv_status pkv_paged_kv_gather_fp8(void* k_out, void* v_out, const void* key_cache, const void* value_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* row_starts, int num_seqs, int64_t num_rows, int64_t num_blocks,
+                                   int block_size, int num_kv_heads, int head_dim, pkv_dtype dt, const float* k_scale,
+                                   const float* v_scale, void* stream) {
+    CallRange range_("pkv_paged_kv_gather_fp8");
+    if (!k_scale || !v_scale) return fail(PKV_ERR_INVALID, "E4M3 pools need k_scale and v_scale");
+    return gather_call(k_out, v_out, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, row_starts,
+                       num_seqs, num_rows, num_blocks, block_size, num_kv_heads, head_dim, dt, k_scale, v_scale, stream);
+}
+
+pkv_status pkv_speculative_accept(int64_t* tokens, int32_t* num_accepted, const int64_t* draft_tokens,
+                                  const int32_t* num_drafts, const void* target_probs, const void* draft_probs,
+                                  const float* uniform, int num_seqs, int max_drafts, int64_t vocab, pkv_dtype dt,
+                                  void* stream) {
+    CallRange range_("pkv_speculative_accept");
+    if (!valid_dtype(dt) && dt != PKV_F32) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", static_cast<int>(dt));
+    if (num_seqs < 0 || num_seqs > (1 << 24)) return fail(PKV_ERR_INVALID, "num_seqs %d outside [0, 2^24]", num_seqs);
+    if (max_drafts < 0 || max_drafts > 1024) return fail(PKV_ERR_INVALID, "max_drafts %d outside [0, 1024]", max_drafts);
+    if (vocab < 1 || vocab > PKV_ACCEPT_MAX_VOCAB)
+        return fail(PKV_ERR_INVALID, "vocab %lld outside [1, %d]", static_cast<long long>(vocab), PKV_ACCEPT_MAX_VOCAB);
+    if (num_seqs == 0) return ok();
+    if (!tokens || !num_accepted || !target_probs || !uniform || (max_drafts > 0 && !draft_tokens))
+        return fail(PKV_ERR_INVALID, "null pointer");
+    const unsigned el = dt == PKV_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(tokens) & 7u) || (reinterpret_cast<uintptr_t>(draft_tokens) & 7u) ||
+        (reinterpret_cast<uintptr_t>(num_accepted) & 3u) || (reinterpret_cast<uintptr_t>(num_drafts) & 3u) ||
+        (reinterpret_cast<uintptr_t>(uniform) & 3u) || (reinterpret_cast<uintptr_t>(target_probs) & el) ||
+        (reinterpret_cast<uintptr_t>(draft_probs) & el))
+        return fail(PKV_ERR_INVALID, "tokens must be 8-byte aligned, the rest to their elements");
+    pkv::AcceptArgs a{};
+    a.tokens = tokens;
+    a.num_accepted = num_accepted;
+    a.draft_tokens = draft_tokens;
+    a.num_drafts = num_drafts;
+    a.target_probs = target_probs;
+    a.draft_probs = max_drafts > 0 ? draft_probs : nullptr;
+    a.uniform = uniform;
+    a.vocab = vocab;
+    a.num_seqs = num_seqs;
+    a.max_drafts = max_drafts;
+    a.err = error_word(current_device());
+    cudaError_t e = pkv::launch_accept(a, dt == PKV_F16 ? 0 : dt == PKV_BF16 ? 1 : 2, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "accept launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
 // Shared by copy_blocks (one pool) and swap_blocks (two pools).
 pkv_status block_copies(void* const* src_key, void* const* src_value, void* const* dst_key, void* const* dst_value,
                         int num_layers, const int64_t* src_dst_pairs, int64_t num_pairs, int64_t src_num_blocks,

@@ -261,6 +261,45 @@ cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            int dtype, int head_dim, cudaStream_t s);
 
+// ---------------------------------------------------------------- cache read-back (csrc/pkv_gather.cu)
+struct GatherArgs {
+    uint4* k_out;            // [num_rows][row_vecs] 8 elements a vector
+    uint4* v_out;
+    const void* key_cache;   // [num_blocks * block_size][row_vecs] (16-bit elements, or 8 codes a vector)
+    const void* value_cache;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* row_starts;       // [num_seqs + 1]
+    const float* k_scale;    // [num_kv_heads] (E4M3 pools only, else nullptr)
+    const float* v_scale;
+    int64_t num_rows;
+    int64_t num_blocks;
+    int num_seqs;
+    int max_blocks_per_seq;
+    int block_size;
+    int row_vecs;            // num_kv_heads * head_dim / 8
+    int head_vecs;           // head_dim / 8
+    int bf16;                // the outputs' type over an E4M3 pool: 0 = fp16, 1 = bf16
+    unsigned* err;
+};
+cudaError_t launch_gather(const GatherArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- draft acceptance (csrc/pkv_accept.cu)
+struct AcceptArgs {
+    int64_t* tokens;                 // [num_seqs][max_drafts + 1]
+    int32_t* num_accepted;           // [num_seqs]
+    const int64_t* draft_tokens;     // [num_seqs][max_drafts]
+    const int32_t* num_drafts;       // [num_seqs], or nullptr: max_drafts each
+    const void* target_probs;        // [num_seqs][max_drafts + 1][vocab]
+    const void* draft_probs;         // [num_seqs][max_drafts][vocab], or nullptr
+    const float* uniform;            // [num_seqs][max_drafts + 1]
+    int64_t vocab;
+    int num_seqs;
+    int max_drafts;
+    unsigned* err;
+};
+cudaError_t launch_accept(const AcceptArgs& a, int dtype, cudaStream_t s);   // dtype 0: fp16, 1: bf16, 2: fp32
+
 // Record `msg` as the calling thread's pkv_last_error() message and return `st`.
 int set_error_message(int st, const char* msg);
 
