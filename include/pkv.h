@@ -479,7 +479,8 @@ PKV_API pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, con
  *                 word's bounds bit)
  *   block_tables  int32 [num_seqs][max_blocks_per_seq] (a position whose table
  *                 entry is out of range is not written and raises the bit)
- * Any block_size; head_dim a multiple of 8; num_rows below 2^31.
+ * Any block_size; head_dim a multiple of 8; num_kv_heads and head_dim up to 4096;
+ * num_rows below 2^31.
  *
  * pkv_paged_kv_gather_fp8: over uint8 E4M3 pools (P3 §6.2);
  * element = dt(e4m3_value(code) * scale[kv_head]), the product in float32,

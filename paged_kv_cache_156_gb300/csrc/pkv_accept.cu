@@ -16,11 +16,12 @@
 // the token is the first whose inclusive sum exceeds floor(u T).
 //
 // One cluster a sequence: its CTAs take a contiguous piece of the row each, a
-// warp a contiguous piece of that, held in registers, so the row is read once;
-// totals go round through distributed shared memory, and the warp that holds
-// the mark scans its registers.  Rows of more than kHeld weights a cluster are
-// summed in several rounds and the round that holds the mark is read again.
-// Bound by latency at a few sequences (some dependent loads: draft token, its
+// warp a contiguous piece of that, so the row is read once; totals go round
+// through distributed shared memory.  Every lane keeps its sum of each batch of
+// 512 weights in shared memory, so the warp that holds the mark finds the batch
+// from there and reads those 512 weights again.  (Weights held in registers
+// instead spilled at two CTAs an SM: 36 us for 64 sequences of 128000 tokens.)
+// Bound by latency at a few sequences (dependent loads: draft token, its
 // probabilities, the row), by HBM at many.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -29,6 +30,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "../../include/pkv.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -38,11 +40,10 @@ namespace pkv {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kIters = 8;                           // groups of 128 weights a warp holds
-constexpr int kHeld = kCluster * kWarps * kIters * 128;     // weights of a round
-constexpr float kUnit = 17592186044416.0f;          // 2^44
+constexpr int kBatch = 4;                           // groups of 128 weights whose loads are in flight together
+constexpr int kMaxBatches = (PKV_ACCEPT_MAX_VOCAB + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128);
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T x) {
@@ -51,15 +52,30 @@ __device__ __forceinline__ float to_f32(T x) {
     else return __bfloat162float(x);
 }
 
-// Four consecutive probabilities from element i of a row (0 past its end).
+// Four consecutive probabilities from element i of a row (0 past its end), `off` elements past a vector's
+// boundary (the row's base and so every fourth element are): the two aligned vectors that hold them, shifted
+// together, where both lie inside the row; element by element at its ends.
 template <typename T>
-__device__ __forceinline__ void load4(const T* row, int64_t i, int64_t vocab, bool vec, float (&x)[4]) {
-    if (vec && i + 4 <= vocab) {
+__device__ __forceinline__ void load4(const T* row, int i, int vocab, int off, float (&x)[4]) {
+    const int at = i - off;
+    if (off == 0 ? i + 4 <= vocab : at >= 0 && at + 8 <= vocab) {
         if constexpr (std::is_same<T, float>::value) {
-            const float4 v = __ldcs(reinterpret_cast<const float4*>(row + i));
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(row + at));
             x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            if (off != 0) {
+                const float4 n = __ldcs(reinterpret_cast<const float4*>(row + at) + 1);
+                x[0] = off == 1 ? v.y : off == 2 ? v.z : v.w;
+                x[1] = off == 1 ? v.z : off == 2 ? v.w : n.x;
+                x[2] = off == 1 ? v.w : off == 2 ? n.x : n.y;
+                x[3] = off == 1 ? n.x : off == 2 ? n.y : n.z;
+            }
         } else {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(row + i));
+            uint2 v = __ldcs(reinterpret_cast<const uint2*>(row + at));
+            if (off != 0) {
+                const uint2 n = __ldcs(reinterpret_cast<const uint2*>(row + at) + 1);
+                const uint32_t a = off >= 2 ? v.y : v.x, b = off >= 2 ? n.x : v.y, c = off >= 2 ? n.y : n.x;
+                v = (off & 1) ? make_uint2(__funnelshift_r(a, b, 16), __funnelshift_r(b, c, 16)) : make_uint2(a, b);
+            }
             const float2 lo = Mma<T>::unpack(v.x), hi = Mma<T>::unpack(v.y);
             x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
         }
@@ -69,8 +85,13 @@ __device__ __forceinline__ void load4(const T* row, int64_t i, int64_t vocab, bo
     }
 }
 
+// floor(min(w, 1) 2^44), 0 for a negative weight or NaN, from the bits: the significand, its leading one at bit
+// 63, shifted down by the exponent (the conversion to 64-bit integers runs at a fraction of the rate of these).
 __device__ __forceinline__ unsigned long long units(float w) {
-    return w > 0.0f ? static_cast<unsigned long long>(__float2ull_rz(fminf(w, 1.0f) * kUnit)) : 0ull;   // (NaN: none)
+    const uint32_t b = __float_as_uint(fminf(fmaxf(w, 0.0f), 1.0f));     // (max and min drop NaN)
+    unsigned long long r = static_cast<unsigned long long>(b << 8 | 0x80000000u) << 32;
+    asm("shr.b64 %0, %0, %1;" : "+l"(r) : "r"(146u - (b >> 23)));        // (64 and more give 0)
+    return r;
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
@@ -80,9 +101,10 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 }
 
 template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) accept_kernel(const AcceptArgs a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) accept_kernel(const AcceptArgs a) {
     __shared__ unsigned long long warp_total[kWarps];
-    __shared__ unsigned long long cta_total[2][kCluster];   // every CTA's total of a round (alternating rounds)
+    __shared__ unsigned long long cta_total[2][kCluster];   // every CTA's total, one for each pass
+    __shared__ unsigned long long batch_sum[kMaxBatches][kThreads];
     __shared__ int s_kept;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
@@ -92,7 +114,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
     grid_dependency_wait();
     launch_dependents();
     const int K = a.max_drafts;
-    const int64_t V = a.vocab;
+    const int V = static_cast<int>(a.vocab);
     const T* target = static_cast<const T*>(a.target_probs) + static_cast<int64_t>(b) * (K + 1) * V;
     const T* draft = a.draft_probs ? static_cast<const T*>(a.draft_probs) + static_cast<int64_t>(b) * K * V : nullptr;
     const int64_t* drafts = a.draft_tokens + static_cast<int64_t>(b) * K;
@@ -116,8 +138,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
                 const int64_t x = __ldcg(drafts + i);
                 if (x >= 0 && x < V) {
                     // (both factors have 24 bits: the fp64 product is exact)
-                    const double q = draft ? static_cast<double>(to_f32(draft[i * V + x])) : 1.0;
-                    keep = static_cast<double>(__ldcg(uniform + i)) * q < static_cast<double>(to_f32(target[i * V + x]));
+                    const double q = draft ? static_cast<double>(to_f32(draft[static_cast<int64_t>(i) * V + x])) : 1.0;
+                    keep = static_cast<double>(__ldcg(uniform + i)) * q < static_cast<double>(to_f32(target[static_cast<int64_t>(i) * V + x]));
                 } else if (rank == 0) {
                     raise_error(a.err, kErrBounds);
                 }
@@ -142,60 +164,69 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
     const T* qrow = refused && draft ? draft + static_cast<int64_t>(kept) * V : nullptr;
     const int64_t out_x = refused && !draft ? __ldcg(drafts + kept) : -1;      // the weight that leaves the row
     const float u = __ldcg(uniform + K);
-    constexpr int kVec = std::is_same<T, float>::value ? 16 : 8;
-    const bool vec = ((reinterpret_cast<uintptr_t>(prow) | (qrow ? reinterpret_cast<uintptr_t>(qrow) : 0)) & (kVec - 1)) == 0;
-    const int rounds = static_cast<int>((V + kHeld - 1) / kHeld);
-    // a warp's weights of a round: per groups of 128 from `first`
-    const int64_t per = ((min(V, static_cast<int64_t>(kHeld)) + kCluster * kWarps * 128 - 1) / (kCluster * kWarps * 128)) * 128;
-    const int iters = static_cast<int>(per / 128);
+    auto offset = [](const T* row) {                // elements past a boundary of four
+        return static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 3);
+    };
+    const int poff = offset(prow), qoff = qrow ? offset(qrow) : 0;
+    // a warp's piece of the row: whole batches
+    const int batches = static_cast<int>((V + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128));
+    const int first = (rank * kWarps + warp) * batches * kBatch * 128 + 4 * lane;
 
-    float w[kIters][4];
-    unsigned flips = 0;                             // which half of cta_total this exchange uses
-    auto load = [&](int round, bool residual) {     // this warp's weights and their total
-        const int64_t first = static_cast<int64_t>(round) * kHeld + (static_cast<int64_t>(rank) * kWarps + warp) * per + 4 * lane;
-        float p[kIters][4], q[kIters][4];
+    float w[kBatch][4];
+    auto load = [&](int batch, bool residual) {     // this lane's weights of a batch
+        const int i0 = first + batch * kBatch * 128;
+        float q[kBatch][4];
 #pragma unroll
-        for (int k = 0; k < kIters; ++k)
-            if (k < iters) load4(prow, first + 128 * k, V, vec, p[k]);
+        for (int k = 0; k < kBatch; ++k) {
+            load4(prow, i0 + 128 * k, V, poff, w[k]);
+            if (residual && qrow) load4(qrow, i0 + 128 * k, V, qoff, q[k]);
+        }
         if (residual && qrow) {
 #pragma unroll
-            for (int k = 0; k < kIters; ++k)
-                if (k < iters) load4(qrow, first + 128 * k, V, vec, q[k]);
-        }
-        unsigned long long sum = 0;
+            for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-        for (int k = 0; k < kIters; ++k) {
+                for (int e = 0; e < 4; ++e) w[k][e] -= q[k][e];
+        }
+        if (residual && out_x >= 0) {
+            const int gone = static_cast<int>(min(out_x, static_cast<int64_t>(V))) - i0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = k < iters ? p[k][e] : 0.0f;
-                if (residual && qrow && k < iters) x -= q[k][e];
-                if (residual && first + 128 * k + e == out_x) x = 0.0f;
-                w[k][e] = x;
-                sum += units(x);
-            }
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[k][e] = gone == 128 * k + e ? 0.0f : w[k][e];
         }
-        return warp_sum(sum);
-    };
-    auto exchange = [&](unsigned long long mine) {  // every CTA's total into cta_total[flips]; this CTA's warps' into warp_total
-        __syncthreads();                            // (warp_total is no longer read)
-        if (lane == 0) warp_total[warp] = mine;
-        __syncthreads();
-        if (warp == 0) {
-            const unsigned long long sum = warp_sum(lane < kWarps ? warp_total[lane] : 0ull);
-            if (lane < kCluster) *cluster.map_shared_rank(&cta_total[flips][rank], lane) = sum;
-        }
-        cluster.sync();
     };
 
     cluster.barrier_wait(std::move(started));
     for (int pass = 0; pass < 2; ++pass) {
         const bool residual = pass == 0;
-        unsigned long long total = 0, before_round = 0;
-        for (int round = 0; round < rounds; ++round) {
-            exchange(load(round, residual));
+        unsigned long long mine = 0;
+#pragma unroll 1
+        for (int batch = 0; batch < batches; ++batch) {
+            unsigned long long sum = 0;
+            if (first - 4 * lane + batch * kBatch * 128 < V) {
+                load(batch, residual);
 #pragma unroll
-            for (int c = 0; c < kCluster; ++c) total += cta_total[flips][c];
-            flips ^= 1u;
+                for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum += units(w[k][e]);
+            }
+            batch_sum[batch][t] = sum;
+            mine += sum;
+        }
+        mine = warp_sum(mine);
+        if (lane == 0) warp_total[warp] = mine;
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned long long sum = warp_sum(lane < kWarps ? warp_total[lane] : 0ull);
+            if (lane < kCluster) *cluster.map_shared_rank(&cta_total[pass][rank], lane) = sum;
+        }
+        cluster.sync();
+        unsigned long long total = 0, before = 0;   // of the row; of what stands before this warp's piece
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+            const unsigned long long x = cta_total[pass][c];
+            before += c < rank ? x : 0ull;
+            total += x;
         }
         if (total == 0) {
             if (pass == 0) continue;                // nothing left of the row: draw from the target's itself
@@ -204,47 +235,34 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
         }
         const double z = (u > 0.0f ? static_cast<double>(u) : 0.0) * static_cast<double>(total);
         const unsigned long long mark = min(__double2ull_rz(z), total - 1);
-        for (int round = 0; round < rounds; ++round) {
-            if (rounds > 1) {
-                exchange(load(round, residual));
-                flips ^= 1u;
-            }
-            // the totals before this warp's weights, in the row's order
-            unsigned long long before = before_round, all = 0;
+        for (int v = 0; v < warp; ++v) before += warp_total[v];
+        if (mark < before || mark >= before + mine) break;       // another warp's
+        int batch = 0;
+        for (; batch + 1 < batches; ++batch) {
+            const unsigned long long sum = warp_sum(batch_sum[batch][t]);
+            if (mark < before + sum) break;
+            before += sum;
+        }
+        load(batch, residual);
 #pragma unroll
-            for (int c = 0; c < kCluster; ++c) {
-                const unsigned long long x = cta_total[flips ^ 1u][c];
-                before += c < rank ? x : 0ull;
-                all += x;
-            }
-            for (int v = 0; v < warp; ++v) before += warp_total[v];
-            if (mark >= before && mark < before + warp_total[warp]) {
-                const int64_t first = static_cast<int64_t>(round) * kHeld + (static_cast<int64_t>(rank) * kWarps + warp) * per + 4 * lane;
-                unsigned long long at = before;
+        for (int k = 0; k < kBatch; ++k) {
+            unsigned long long c[4];
+            c[0] = units(w[k][0]);
+            c[1] = c[0] + units(w[k][1]);
+            c[2] = c[1] + units(w[k][2]);
+            c[3] = c[2] + units(w[k][3]);
+            unsigned long long inc = c[3];
 #pragma unroll
-                for (int k = 0; k < kIters; ++k) {
-                    if (k >= iters) break;
-                    unsigned long long c[4];
-                    c[0] = units(w[k][0]);
-                    c[1] = c[0] + units(w[k][1]);
-                    c[2] = c[1] + units(w[k][2]);
-                    c[3] = c[2] + units(w[k][3]);
-                    unsigned long long inc = c[3];
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
-                        if (lane >= o) inc += y;
-                    }
-                    const unsigned long long mine = at + inc - c[3];     // before this lane's four
-                    if (mark >= mine && mark < mine + c[3]) {
-                        const int e = mark < mine + c[0] ? 0 : mark < mine + c[1] ? 1 : mark < mine + c[2] ? 2 : 3;
-                        a.tokens[static_cast<int64_t>(b) * (K + 1) + kept] = first + 128 * k + e;
-                    }
-                    at += __shfl_sync(0xffffffffu, inc, 31);
-                }
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
             }
-            before_round += all;
-            if (mark < before_round) break;         // (the same in every thread of the cluster)
+            const unsigned long long at = before + inc - c[3];   // before this lane's four
+            if (mark >= at && mark < at + c[3]) {
+                const int e = mark < at + c[0] ? 0 : mark < at + c[1] ? 1 : mark < at + c[2] ? 2 : 3;
+                a.tokens[static_cast<int64_t>(b) * (K + 1) + kept] = first + (batch * kBatch + k) * 128 + e;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
         }
         break;
     }

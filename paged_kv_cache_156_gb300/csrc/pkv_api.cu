@@ -795,8 +795,8 @@ pkv_status gather_call(void* k_out, void* v_out, const void* key_cache, const vo
     if (num_kv_heads <= 0 || head_dim <= 0 || head_dim % 8 != 0)
         return fail(PKV_ERR_INVALID, "num_kv_heads %d / head_dim %d (head_dim must be a positive multiple of 8)",
                     num_kv_heads, head_dim);
-    if (static_cast<int64_t>(num_kv_heads) * head_dim > (1 << 24))
-        return fail(PKV_ERR_INVALID, "num_kv_heads * head_dim above 2^24");
+    if (num_kv_heads > 4096 || head_dim > 4096)
+        return fail(PKV_ERR_INVALID, "num_kv_heads %d / head_dim %d above 4096", num_kv_heads, head_dim);
     if (block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq < 0)
         return fail(PKV_ERR_INVALID, "block_size %d / num_blocks %lld / max_blocks_per_seq %d", block_size,
                     static_cast<long long>(num_blocks), max_blocks_per_seq);

@@ -8,13 +8,16 @@
 // process or a prefix store takes from the cache.
 //
 // HBM-bound: every byte is read once and written once.  The grid covers the
-// output's rows (the one size the host knows), kRows a CTA; the CTA finds the
-// sequence of its first row by counting the starts at or below it (no search
-// loop: one load a thread for up to 256 sequences), walks on from there, and
-// then moves its rows 16 bytes a lane, every load of a thread issued before its
-// stores.
+// output's rows (the one size the host knows), so many a CTA that each thread has
+// kUnroll loads of K and of V; the CTA finds the sequence of its first row by
+// counting the starts at or below it (no search loop: one load a thread for up to
+// 256 sequences), every thread walks on from there to a row of its own, and then
+// the rows are moved 16 bytes a load, a thread's loads before its stores.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -23,7 +26,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 8;                            // output rows a CTA
+constexpr int kMaxRows = kThreads;                  // output rows a CTA at most
 constexpr int kUnroll = 4;                          // 16-byte loads of K and of V in flight a thread
 
 template <typename T>
@@ -39,13 +42,23 @@ __device__ __forceinline__ uint4 expand8(uint2 c, float scale) {        // 8 cod
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// T: the output's type over an E4M3 pool (KV8); 16-bit rows are moved as they are.
-template <typename T, bool KV8>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
-    __shared__ int64_t src_row[kRows];              // the output row's row in the pools (-1: not written)
+// The neighbouring lane's first 8 codes for an even lane, its last 8 for an odd one.
+__device__ __forceinline__ uint2 swap_half(bool odd, const uint4& x) {
+    uint2 g = odd ? make_uint2(x.x, x.y) : make_uint2(x.z, x.w);
+    g.x = __shfl_xor_sync(0xffffffffu, g.x, 1);
+    g.y = __shfl_xor_sync(0xffffffffu, g.y, 1);
+    return g;
+}
+
+// T: the output's type over an E4M3 pool (KV8); 16-bit rows are moved as they are.  WIDE: 16 codes a load (head_dim
+// a multiple of 16, an even number of loads a row and 16-byte aligned pools), else 8.
+template <typename T, bool KV8, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 4) gather_kernel(const GatherArgs a) {
+    __shared__ int64_t src_row[kMaxRows];           // the output row's row in the pools (-1: not written)
     grid_dependency_wait();
     launch_dependents();
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+    const int rows = a.cta_rows;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
     const int t = threadIdx.x;
     // ---- the last sequence that starts at or before the first row (the starts do not decrease)
     int mine = 0;
@@ -54,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
     __shared__ int part[kThreads / 32];
     if ((t & 31) == 0) part[t >> 5] = mine;
     __syncthreads();
-    if (t < kRows) {
+    if (t < rows) {
         int s = -1;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) s += part[w];
@@ -73,6 +86,13 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
         }
         src_row[t] = src;
     }
+    // the heads' scales, once a CTA (from L2 for every vector they cost as much as the codes)
+    extern __shared__ float scales[];               // [K | V][heads]
+    const int heads = KV8 ? a.row_vecs / a.head_vecs : 0;
+    for (int i = t; i < heads; i += kThreads) {
+        scales[i] = __ldcg(a.k_scale + i);
+        scales[heads + i] = __ldcg(a.v_scale + i);
+    }
     // the batch's lengths and starts, checked by the first CTA
     if (blockIdx.x == 0)
         for (int i = t; i < a.num_seqs; i += kThreads) {
@@ -81,70 +101,91 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
         }
     __syncthreads();
 
-    const int rv = a.row_vecs;                      // output vectors of a row (8 elements each)
-    const int total = kRows * rv;
-    for (int i0 = t; i0 < total; i0 += kThreads * kUnroll) {
-        if constexpr (KV8) {
-            uint2 x[kUnroll], y[kUnroll];
+    // A thread's row and place advance by constants, without a division a vector.
+    using Vec = std::conditional_t<KV8 && !WIDE, uint2, uint4>;
+    constexpr int kOut = KV8 && WIDE ? 2 : 1;       // output vectors a load gives
+    const int rv = a.row_vecs / kOut;               // loads a row
+    const int step_r = kThreads / rv, step_c = kThreads - step_r * rv;
+    const int hv = KV8 ? a.head_vecs / kOut : 1;
+    const int trips = (rows * rv + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+    int r = t / rv, c = t - r * rv;
+    for (int trip = 0; trip < trips; ++trip) {
+        Vec x[kUnroll], y[kUnroll];
+        int rr[kUnroll], cc[kUnroll];
+        bool live[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + u * kThreads, r = i / rv;
-                const int64_t src = i < total ? src_row[r] : -1;
-                if (src >= 0) {
-                    x[u] = __ldcs(static_cast<const uint2*>(a.key_cache) + src * rv + (i - r * rv));
-                    y[u] = __ldcs(static_cast<const uint2*>(a.value_cache) + src * rv + (i - r * rv));
+        for (int u = 0; u < kUnroll; ++u) {
+            rr[u] = r;
+            cc[u] = c;
+            const int64_t src = r < rows ? src_row[r] : -1;
+            live[u] = src >= 0;
+            if (live[u]) {
+                x[u] = __ldcs(static_cast<const Vec*>(a.key_cache) + src * rv + c);
+                y[u] = __ldcs(static_cast<const Vec*>(a.value_cache) + src * rv + c);
+            }
+            r += step_r;
+            c += step_c;
+            if (c >= rv) {
+                c -= rv;
+                ++r;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if constexpr (KV8 && WIDE) {
+                // 16 codes are two output vectors: lane pairs swap halves, so that a pair's store fills a
+                // 32-byte sector (each lane's two vectors stored by itself filled half of one at a time and
+                // cost 15% more)
+                const bool odd = threadIdx.x & 1;
+                const uint2 kx = swap_half(odd, x[u]), vx = swap_half(odd, y[u]);
+                if (!live[u]) continue;
+                const int ce = cc[u] & ~1, h0 = ce / hv, h1 = (ce + 1) / hv;
+                const int64_t at = ((row0 + rr[u]) * rv + ce) * 2 + odd;
+                a.k_out[at] = expand8<T>(odd ? kx : make_uint2(x[u].x, x[u].y), scales[h0]);
+                a.v_out[at] = expand8<T>(odd ? vx : make_uint2(y[u].x, y[u].y), scales[heads + h0]);
+                a.k_out[at + 2] = expand8<T>(odd ? make_uint2(x[u].z, x[u].w) : kx, scales[h1]);
+                a.v_out[at + 2] = expand8<T>(odd ? make_uint2(y[u].z, y[u].w) : vx, scales[heads + h1]);
+            } else if (live[u]) {
+                const int64_t at = (row0 + rr[u]) * rv + cc[u];
+                if constexpr (KV8) {
+                    const int h = cc[u] / hv;
+                    a.k_out[at] = expand8<T>(x[u], scales[h]);
+                    a.v_out[at] = expand8<T>(y[u], scales[heads + h]);
+                } else {
+                    a.k_out[at] = x[u];
+                    a.v_out[at] = y[u];
                 }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + u * kThreads, r = i / rv;
-                if (i >= total || src_row[r] < 0) continue;
-                const int h = (i - r * rv) / a.head_vecs;
-                a.k_out[row0 * rv + i] = expand8<T>(x[u], __ldcg(a.k_scale + h));
-                a.v_out[row0 * rv + i] = expand8<T>(y[u], __ldcg(a.v_scale + h));
-            }
-        } else {
-            uint4 x[kUnroll], y[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + u * kThreads, r = i / rv;
-                const int64_t src = i < total ? src_row[r] : -1;
-                if (src >= 0) {
-                    x[u] = __ldcs(static_cast<const uint4*>(a.key_cache) + src * rv + (i - r * rv));
-                    y[u] = __ldcs(static_cast<const uint4*>(a.value_cache) + src * rv + (i - r * rv));
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + u * kThreads, r = i / rv;
-                if (i >= total || src_row[r] < 0) continue;
-                a.k_out[row0 * rv + i] = x[u];
-                a.v_out[row0 * rv + i] = y[u];
             }
         }
     }
 }
 
-template <typename T, bool KV8>
-cudaError_t launch(const GatherArgs& a, cudaStream_t s) {
+template <typename T, bool KV8, bool WIDE>
+cudaError_t launch(GatherArgs a, cudaStream_t s) {
+    const int loads = a.row_vecs / (KV8 && WIDE ? 2 : 1);                // a row
+    a.cta_rows = std::min(kMaxRows, std::max(4, kThreads * kUnroll / loads));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.num_rows + kRows - 1) / kRows));
+    cfg.gridDim = dim3(static_cast<unsigned>((a.num_rows + a.cta_rows - 1) / a.cta_rows));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = KV8 ? 2 * sizeof(float) * static_cast<size_t>(a.row_vecs / a.head_vecs) : 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gather_kernel<T, KV8>, a);
+    return cudaLaunchKernelEx(&cfg, gather_kernel<T, KV8, WIDE>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_gather(const GatherArgs& a, cudaStream_t s) {
     if (a.num_rows <= 0 || a.num_seqs <= 0) return cudaSuccess;
-    if (!a.k_scale) return launch<__half, false>(a, s);
-    return a.bf16 ? launch<__nv_bfloat16, true>(a, s) : launch<__half, true>(a, s);
+    if (!a.k_scale) return launch<__half, false, true>(a, s);
+    const bool wide = a.head_vecs % 2 == 0 && a.row_vecs % 4 == 0 &&
+                      ((reinterpret_cast<uintptr_t>(a.key_cache) | reinterpret_cast<uintptr_t>(a.value_cache)) & 15u) == 0;
+    if (a.bf16) return wide ? launch<__nv_bfloat16, true, true>(a, s) : launch<__nv_bfloat16, true, false>(a, s);
+    return wide ? launch<__half, true, true>(a, s) : launch<__half, true, false>(a, s);
 }
 
 }  // namespace pkv

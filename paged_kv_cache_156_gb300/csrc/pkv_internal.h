@@ -279,6 +279,7 @@ struct GatherArgs {
     int block_size;
     int row_vecs;            // num_kv_heads * head_dim / 8
     int head_vecs;           // head_dim / 8
+    int cta_rows;            // output rows a CTA (set by the launch)
     int bf16;                // the outputs' type over an E4M3 pool: 0 = fp16, 1 = bf16
     unsigned* err;
 };
