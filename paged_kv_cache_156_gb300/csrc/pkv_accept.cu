@@ -85,13 +85,18 @@ __device__ __forceinline__ void load4(const T* row, int i, int vocab, int off, f
     }
 }
 
-// floor(min(w, 1) 2^44), 0 for a negative weight or NaN, from the bits: the significand, its leading one at bit
-// 63, shifted down by the exponent (the conversion to 64-bit integers runs at a fraction of the rate of these).
-__device__ __forceinline__ unsigned long long units(float w) {
-    const uint32_t b = __float_as_uint(fminf(fmaxf(w, 0.0f), 1.0f));     // (max and min drop NaN)
-    unsigned long long r = static_cast<unsigned long long>(b << 8 | 0x80000000u) << 32;
-    asm("shr.b64 %0, %0, %1;" : "+l"(r) : "r"(146u - (b >> 23)));        // (64 and more give 0)
-    return r;
+// Whole units of a weight in [0, 1] (clipped as it is formed, NaN to 0), floor(w 2^44), as two 22-bit halves added
+// to hi and lo: w + 2 rounded towards zero holds floor(w 2^22) in its significand's last bits, what is left of w
+// (exact) plus 2^-21 the next 22.  Seven single-rate instructions a weight with its clipped difference; a shift by
+// the exponent took twice that, the conversion to 64-bit integers runs at a sixteenth of the rate.
+__device__ __forceinline__ void add_units(float w, uint32_t& hi, uint32_t& lo) {
+    const float y = __fadd_rz(w, 2.0f);
+    const float rest = __fsub_rn(w, __fsub_rn(y, 2.0f));
+    hi += __float_as_uint(y) - 0x40000000u;
+    lo += __float_as_uint(__fadd_rz(rest, 0x1p-21f)) - 0x35000000u;
+}
+__device__ __forceinline__ unsigned long long join(uint32_t hi, uint32_t lo) {      // (of up to 512 weights)
+    return (static_cast<unsigned long long>(hi) << 22) + lo;
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
@@ -181,12 +186,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             load4(prow, i0 + 128 * k, V, poff, w[k]);
             if (residual && qrow) load4(qrow, i0 + 128 * k, V, qoff, q[k]);
         }
-        if (residual && qrow) {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
+        for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[k][e] -= q[k][e];
-        }
+            for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(residual && qrow ? w[k][e] - q[k][e] : w[k][e]);
         if (residual && out_x >= 0) {
             const int gone = static_cast<int>(min(out_x, static_cast<int64_t>(V))) - i0;
 #pragma unroll
@@ -202,14 +205,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
         unsigned long long mine = 0;
 #pragma unroll 1
         for (int batch = 0; batch < batches; ++batch) {
-            unsigned long long sum = 0;
+            uint32_t hi = 0, lo = 0;
             if (first - 4 * lane + batch * kBatch * 128 < V) {
                 load(batch, residual);
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sum += units(w[k][e]);
+                    for (int e = 0; e < 4; ++e) add_units(w[k][e], hi, lo);
             }
+            const unsigned long long sum = join(hi, lo);
             batch_sum[batch][t] = sum;
             mine += sum;
         }
@@ -247,10 +251,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             unsigned long long c[4];
-            c[0] = units(w[k][0]);
-            c[1] = c[0] + units(w[k][1]);
-            c[2] = c[1] + units(w[k][2]);
-            c[3] = c[2] + units(w[k][3]);
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                add_units(w[k][e], hi, lo);
+                c[e] = join(hi, lo);
+            }
             unsigned long long inc = c[3];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
