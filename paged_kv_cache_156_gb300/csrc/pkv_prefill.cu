@@ -240,8 +240,9 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* sr
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(keep ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
+    return r;
 }
 // 4 x 4 transposition over a quad: lane q's register i becomes lane i's register q.
 __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4]) {
@@ -436,11 +437,13 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             }
         } else if (KV8 && (warp == G::kLoadV || warp == G::kClean || warp == G::kClean + 2)) {
             // ======================================================== codes to f16, V cleaned on the way
-            // A lane takes 16 codes (one 128-byte row over 8 lanes) and writes two 16-byte pieces; the lanes
-            // of a row's second half write theirs in the other order, so that no two meet in a bank.
+            // A lane takes 16 codes, 32 bytes of f16 in one column plane.  A load or store instruction covers
+            // eight rows by four lanes a row, and every eight lanes two rows whose numbers differ in bits 0
+            // and 2 (q and q ^ 5): the swizzles then put the eight pieces into different banks both times.  A
+            // lane's row in a group of eight, and so its swizzle, never changes: addresses advance by 1 KB.
             const int cw = (warp - G::kLoadV) / 2;
             int* mine = bad + cw * D;
-            const int ch = lane & 7, sub = lane >> 3;
+            const int l3 = lane & 3, rl = (lane >> 3) ^ ((lane >> 2) & 1 ? 5 : 0);
             Ring<ST> c;
             Ring<G::kCodes> q;
             Item it;
@@ -456,19 +459,27 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const uint32_t src = smem_u32(smem + G::kCode + q.slot * G::kCodeTile), dst = smem_u32(ring + c.slot * G::kTile);
-#pragma unroll 2
-                    for (int g = cw; g < kStep / 4; g += G::kConverters) {
-                        const int row = 4 * g + sub;
-                        uint32_t x[4];
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(dec::swz(src, row, ch)));
-                        if (4 * g + 3 >= nv && row >= nv) x[0] = x[1] = x[2] = x[3] = 0u;      // slots past the end
-                        if (look && 4 * g + 3 >= lo) {
+#pragma unroll 1
+                    for (int g0 = cw; g0 < kStep / 8; g0 += 2 * G::kConverters) {      // two groups of eight rows at a time
+                        uint32_t x[4][4];                    // [group, plane]
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int row = 8 * (g0 + (u >> 1) * G::kConverters) + rl;
+                            x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0u;                        // slots past the end
+                            if (row < nv)
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(x[u][0]), "=r"(x[u][1]), "=r"(x[u][2]), "=r"(x[u][3])
+                                             : "r"(dec::swz(src, row, 4 * (u & 1) + l3)));
+                        }
+                        if (look && 8 * (g0 + G::kConverters) + 7 >= lo) {
                             uint32_t hit = 0;                // (a code of seven ones is NaN)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) hit |= ((x[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                            if (row < lo) hit = 0;
+                            for (int u = 0; u < 4; ++u) {
+                                uint32_t any = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) any |= ((x[u][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                if (any && 8 * (g0 + (u >> 1) * G::kConverters) + rl >= lo) hit |= 1u << u;
+                            }
                             if (__any_sync(0xffffffffu, hit != 0)) {                           // rare
                                 if (bad_tag[cw] != r) {
                                     const unsigned long long t0 = globaltimer_ns();
@@ -479,27 +490,35 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                                     __syncwarp();
                                 }
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    for (int b = 0; b < 4 && hit != 0; ++b) {
-                                        if ((x[e] >> (8 * b) & 0x7fu) != 0x7fu) continue;
-                                        atomicMin(&mine[16 * ch + 4 * e + b], tok0 + row);
-                                        x[e] &= ~(0xffu << (8 * b));
-                                    }
+                                for (int u = 0; u < 4; ++u) {
+                                    if (!(hit >> u & 1u)) continue;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+#pragma unroll 1
+                                        for (int b = 0; b < 4; ++b) {
+                                            if ((x[u][e] >> (8 * b) & 0x7fu) != 0x7fu) continue;
+                                            atomicMin(&mine[64 * (u & 1) + 16 * l3 + 4 * e + b],
+                                                      tok0 + 8 * (g0 + (u >> 1) * G::kConverters) + rl);
+                                            x[u][e] &= ~(0xffu << (8 * b));
+                                        }
                                 }
                             }
                         }
-                        uint32_t h[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = e4m3x2_to_f16x2(x[e >> 1] >> (16 * (e & 1)));
-                        const uint32_t plane = dst + (ch >> 2) * G::kPlane;
-                        const int c0 = 2 * (ch & 3) + (ch >> 2), c1 = c0 ^ 1;
-                        const bool back = (ch >> 2) != 0;    // (the piece with the later elements first)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dec::swz(plane, row, c0)),
-                                     "r"(back ? h[4] : h[0]), "r"(back ? h[5] : h[1]), "r"(back ? h[6] : h[2]), "r"(back ? h[7] : h[3])
-                                     : "memory");
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dec::swz(plane, row, c1)),
-                                     "r"(back ? h[0] : h[4]), "r"(back ? h[1] : h[5]), "r"(back ? h[2] : h[6]), "r"(back ? h[3] : h[7])
-                                     : "memory");
+                        for (int u = 0; u < 4; ++u) {
+                            const int row = 8 * (g0 + (u >> 1) * G::kConverters) + rl;
+                            if (row >= kStep) break;
+                            const uint32_t plane = dst + (u & 1) * G::kPlane;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) h[e] = e4m3x2_to_f16x2(x[u][2 * half + (e >> 1)] >> (16 * (e & 1)));
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dec::swz(plane, row, 2 * l3 + half)),
+                                             "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                             : "memory");
+                            }
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
