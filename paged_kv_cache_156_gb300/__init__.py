@@ -168,6 +168,20 @@ def _one_device(fn):
     the tensors' device, and dereference every pointer there."""
     @functools.wraps(fn)
     def call(*args, **kwargs):
+        # the usual call: plain tensors of the current device
+        dev = None
+        for v in (*args, *kwargs.values()):
+            if type(v) is torch.Tensor:
+                d = v.get_device()
+                if d >= 0 and d != dev:
+                    if dev is not None:
+                        break
+                    dev = d
+            elif isinstance(v, (list, tuple, torch.Tensor)):
+                break
+        else:
+            if dev is None or dev == torch.cuda.current_device():
+                return fn(*args, **kwargs)
         devs = _cuda_devices(list(args) + list(kwargs.values()))
         if len(devs) > 1:
             raise ValueError(f"{fn.__name__}: tensors on more than one device: {sorted(str(d) for d in devs)}")
@@ -179,7 +193,7 @@ def _one_device(fn):
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _cuda(name, t, dtype=None, ndim=None):
@@ -191,7 +205,7 @@ def _cuda(name, t, dtype=None, ndim=None):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _pool(name, c, dtypes=(torch.float16, torch.bfloat16)):
@@ -306,7 +320,7 @@ def _scales(name, t, Hkv):
     _cuda(name, t, torch.float32, 1)
     if t.shape[0] != Hkv:
         raise ValueError(f"{name} must have num_kv_heads = {Hkv} entries")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 @_one_device

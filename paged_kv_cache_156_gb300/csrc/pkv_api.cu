@@ -652,6 +652,7 @@ pkv_status prefill_args(pkv::PrefillArgs& a, pkv::PrefillWorkspace& lay, const i
     a.part_rows = lay.part_rows;
     a.slots = sms;
     a.may_split = pkv::prefill_may_split(num_tokens, max_seq_len, num_heads, num_kv_heads, sms);
+    a.direct = pkv::prefill_direct(num_seqs, num_tokens, max_seq_len, num_heads, num_kv_heads, sms);
     return ok();
 }
 
@@ -720,7 +721,7 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = planned ? cudaSuccess : pkv::launch_prefill_plan(a, s);
+    cudaError_t e = planned || a.direct ? cudaSuccess : pkv::launch_prefill_plan(a, s);
     if (e == cudaSuccess) e = pkv::launch_prefill(a, tmq, tmk, tmv, dt == PKV_F16 ? 0 : 1, head_dim, s);
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
     return ok();
@@ -748,6 +749,7 @@ pkv_status pkv_prefill_plan(const int32_t* seq_lens, const int32_t* query_starts
                                  num_kv_heads, head_dim, workspace, workspace_bytes);
     if (st != PKV_OK || num_seqs == 0 || num_tokens == 0) return st;
     a.err = error_word(current_device());
+    if (a.direct) return ok();                           // (the run reads no plan)
     cudaError_t e = pkv::launch_prefill_plan(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "prefill plan launch: %s", cudaGetErrorString(e));
     return ok();

@@ -237,6 +237,7 @@ struct PrefillArgs {
     int part_rows;                   // rows of a partial slot: min(256, num_tokens * group), a multiple of 32
     int slots;                       // CTAs the grid may hold at once
     int may_split;                   // 0: the plan splits no tile (no merge kernel follows)
+    int direct;                      // 1: no plan: a CTA finds its item by itself (at most one each)
     int q_tma;                       // 1: a Q tile is one TMA box a column plane (the group divides 128)
     int negate_q;                    // scale < 0
     float scale_log2;                // |scale| * log2(e)
@@ -257,6 +258,8 @@ PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int 
 // Whether the plan may split a tile of such a batch: long enough sequences, and not so many tiles that
 // every SM has several anyway.
 bool prefill_may_split(int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots);
+// A call so small that every item has a CTA of its own and none is split: no plan is made or read.
+bool prefill_direct(int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots);
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            int dtype, int head_dim, cudaStream_t s);

@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "pkv_decode_common.cuh"
+#include "pkv_prefill_common.cuh"
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
@@ -139,6 +140,30 @@ __device__ __forceinline__ Entry fetch_entry(const PrefillArgs& a, int total, in
         n.kvh = static_cast<int>(w) - e * a.num_kv_heads;
         n.x = __ldcg(a.items + 2 * e);
         n.y = __ldcg(a.items + 2 * e + 1);
+    }
+    return n;
+}
+// The same without a plan: this CTA's item is tile blockIdx.x / KV heads of the batch, counted by a warp over the
+// sequences.
+__device__ __forceinline__ Entry find_entry(const PrefillArgs& a) {
+    Entry n{};
+    const int lane = threadIdx.x & 31;
+    const int e = static_cast<int>(blockIdx.x) / a.num_kv_heads;
+    int before = 0;
+    for (int s0 = 0; s0 < a.num_seqs; s0 += 32) {
+        pf::Seq q{0, 0, 0};
+        if (s0 + lane < a.num_seqs) q = pf::load_seq(a, s0 + lane, blockIdx.x == 0);
+        const int mine = pf::tiles_of(q, a.group), upto = before + pf::warp_scan(mine);
+        const unsigned m = __ballot_sync(0xffffffffu, upto > e);
+        if (!n.live && m) {
+            const int k = __ffs(m) - 1;
+            n.live = true;
+            n.kvh = static_cast<int>(blockIdx.x) - e * a.num_kv_heads;
+            n.x = make_int4(s0 + k, e - __shfl_sync(0xffffffffu, upto - mine, k), 0, 1 << 23);
+            n.y = make_int4(__shfl_sync(0xffffffffu, q.start, k), __shfl_sync(0xffffffffu, q.n, k),
+                            __shfl_sync(0xffffffffu, q.len, k), 0);
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
     }
     return n;
 }
@@ -724,9 +749,15 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
         } else if (warp == G::kPlan) {
             // ======================================================== items, decoded a few ahead
             // (the first entry is read beside the count of items, not after it: entries past the count are stale)
-            Entry next = fetch_entry(a, a.capacity * a.num_kv_heads, 0);
-            const int total = min(max(__ldcg(a.header), 0), a.capacity) * a.num_kv_heads;
-            next.live = static_cast<int>(blockIdx.x) < total;
+            Entry next{};
+            int total = 0;
+            if (a.direct) {
+                next = find_entry(a);
+            } else {
+                next = fetch_entry(a, a.capacity * a.num_kv_heads, 0);
+                total = min(max(__ldcg(a.header), 0), a.capacity) * a.num_kv_heads;
+                next.live = static_cast<int>(blockIdx.x) < total;
+            }
             bool ok = !*abort_flag, more = true;
             for (int r = 0; ok && more; ++r) {
                 const int k = r % G::kItems;
@@ -1165,7 +1196,8 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtenso
     if (regs.load(std::memory_order_relaxed) * G::kThreads < 256 * G::kRegsSoftmax + 256 * G::kRegsOther)
         return cudaErrorLaunchOutOfResources;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.slots, static_cast<int64_t>(a.capacity) * a.num_kv_heads)));
+    cfg.gridDim = dim3(static_cast<unsigned>(
+        std::min<int64_t>(a.slots, static_cast<int64_t>(a.direct ? a.capacity - a.part_cap : a.capacity) * a.num_kv_heads)));
     cfg.blockDim = dim3(G::kThreads);
     cfg.dynamicSmemBytes = G::kBytes;
     cfg.stream = s;

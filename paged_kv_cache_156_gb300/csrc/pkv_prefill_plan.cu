@@ -24,8 +24,7 @@
 
 #include <algorithm>
 
-#include "pkv_device.cuh"
-#include "pkv_internal.h"
+#include "pkv_prefill_common.cuh"
 
 namespace pkv {
 namespace {
@@ -40,25 +39,9 @@ constexpr int kSplitCost = 3;        // and of a part's partial output and its s
 constexpr int kMinPart = 2;          // steps of a part at least
 constexpr int kBuckets = 128;
 
-struct Seq {
-    int start, n, len;
-};
-
-__device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int s, bool report) {
-    Seq q{__ldcg(a.query_starts + s), 0, __ldcg(a.seq_lens + s)};
-    const int end = __ldcg(a.query_starts + s + 1);
-    if (q.len > a.max_seq_len) {
-        if (report) raise_error(a.err, kErrBounds);
-        q.len = a.max_seq_len;
-    }
-    q.len = max(q.len, 0);
-    if (q.start < 0 || end < q.start || end > a.num_tokens) {
-        if (report) raise_error(a.err, kErrBounds);
-    } else {
-        q.n = end - q.start;
-    }
-    return q;
-}
+using pf::load_seq;
+using pf::Seq;
+using pf::warp_scan;
 
 // Steps the last row of a tile sees.
 __device__ __forceinline__ int tile_steps(const Seq& q, int group, int tile) {
@@ -66,16 +49,6 @@ __device__ __forceinline__ int tile_steps(const Seq& q, int group, int tile) {
     const int last = min(rows, (tile + 1) * kPrefillRows) - 1;
     const int lim = min(q.len, max(0, q.len - q.n + last / group + 1));
     return (lim + kPrefillStep - 1) / kPrefillStep;
-}
-
-__device__ __forceinline__ int warp_scan(int v) {            // inclusive
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    return v;
 }
 
 constexpr int kCached = 2048;        // tiles whose steps stay in shared memory between the phases
@@ -102,7 +75,7 @@ __device__ void load_chunk(const PrefillArgs& a, Shared& sh, int base, bool repo
     sh.start[t] = q.start;
     sh.n[t] = q.n;
     sh.len[t] = q.len;
-    const int mine = static_cast<int>((static_cast<long long>(q.n) * a.group + kPrefillRows - 1) / kPrefillRows);
+    const int mine = pf::tiles_of(q, a.group);
     const int inc = warp_scan(mine);
     if (lane == 31) sh.scan[warp] = inc;
     __syncthreads();
@@ -292,6 +265,12 @@ PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int 
 bool prefill_may_split(int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots) {
     const int64_t tiles = num_tokens * (num_heads / num_kv_heads) / kPrefillRows;       // at least
     return max_seq_len > kMinPart * kPrefillStep && tiles * num_kv_heads < 8ll * slots;
+}
+
+bool prefill_direct(int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots) {
+    const int64_t rows = num_tokens * (num_heads / num_kv_heads);
+    return num_seqs <= 128 && (rows / kPrefillRows + std::min<int64_t>(num_seqs, rows)) * num_kv_heads <= slots &&
+           !prefill_may_split(num_tokens, max_seq_len, num_heads, num_kv_heads, slots);
 }
 
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
