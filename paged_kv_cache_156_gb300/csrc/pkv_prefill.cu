@@ -76,13 +76,16 @@ struct PfGeo {
     static constexpr size_t kBars = kCode + size_t(kCodes) * kCodeTile;
     static constexpr int kItems = 4;                        // items decoded ahead
     static constexpr int kItemReaders = 15;                 // warps that read each
-    static constexpr int kNumBars = 3 * kStages + 17 + 2 * kItems + 2 * kCodes;
+    static constexpr int kNumBars = 3 * kStages + 21 + 2 * kItems + 2 * kCodes;
     static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, epilogue count, tags
     static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // first positions of non-finite V elements: [2 warps][+inf, -inf][D], or [3 warps][NaN][D]
     static constexpr size_t kList = kBad + size_t(4) * D * 4;    // [kItems] decoded items
     static constexpr size_t kBytes = kList + kItems * 64;
     static_assert(!KV8 || D == 128, "E4M3 pools: a row of codes is one 128-byte plane");
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+    // P's columns: its own at head_dim 64, where they are left over; S's at 128
+    static constexpr bool kOwnP = D == 64;
+    static constexpr uint32_t kColP = kOwnP ? 384 : kColS, kStrideP = kOwnP ? 64 : 128;
     // registers a thread: 512 threads start with 128; the softmax warpgroups take 192, the others keep 64
     static constexpr int kRegsSoftmax = 192, kRegsOther = 64;
     static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "the split fits the launch's registers");
@@ -343,7 +346,9 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
     uint64_t* turn = q_full + 12;                   // [2] the tile may issue its next round (the other's MMA warp)
     uint64_t* q_raw = q_full + 14;                  // [2] the tile before its conversion to f16 (kConvertQ)
     uint64_t* fin = q_full + 16;                    // every product issued is done (both MMA warps' commits)
-    uint64_t* item_full = q_full + 17;              // [kItems] an item is decoded (plan warp)
+    uint64_t* s_read = q_full + 17;                 // [2] kOwnP: a step's S in registers (softmax threads)
+    uint64_t* o_step = q_full + 19;                 // [2] kOwnP: a step's O product done (MMA commit)
+    uint64_t* item_full = q_full + 21;              // [kItems] an item is decoded (plan warp)
     uint64_t* item_empty = item_full + G::kItems;   // [kItems] every reader has read it
     uint64_t* code_full = item_empty + G::kItems;   // [kCodes] a tile of codes landed (TMA bytes)
     uint64_t* code_empty = code_full + G::kCodes;   // [kCodes] it is expanded (converter warps)
@@ -370,6 +375,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             mbar_init(&p_full[2 * i + 1], kSub);
             mbar_init(&o_full[i], 1);
             mbar_init(&turn[i], 1);
+            mbar_init(&s_read[i], kSub);
+            mbar_init(&o_step[i], 1);
         }
         for (int i = 0; i < G::kItems; ++i) {
             mbar_init(&item_full[i], 1);
@@ -622,10 +629,11 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             const uint64_t dq = tc::smem_desc_sw128(smem_u32(smem) + i * G::kTile, 16, 1024);
             const uint64_t dk = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);            // ring slot 0 as K
             const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring), G::kPlane, 1024);     // and as V
-            const uint32_t ts = __shfl_sync(0xffffffffu, tmem, 0) + G::kColS + i * 128, to = ts + G::kColO;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t ts = tm + G::kColS + i * 128, to = tm + G::kColO + i * D, tp = tm + G::kColP + i * G::kStrideP;
             const bool leader = elect_one();
             Ring<ST> c;                                      // the next tile of the ring
-            unsigned np = 0, nq = 0, nturn = i == 0;   // parities (tile 0 goes first: its turn's phase before the first)
+            unsigned np = 0, nq = 0, nr = 0, nturn = i == 0;   // parities (tile 0 goes first: its turn's phase before the first)
             Item it;
             bool ok = !*abort_flag;
             auto wait = [&](uint64_t* bar, unsigned parity) { return wait_bar(bar, parity, abort_flag); };
@@ -647,11 +655,37 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                     const bool more_k = j + 1 < n;
                     if (ok && more_k) ok = wait(&full[c.slot], c.phase);
                     if (!ok) break;
-                    // the tiles take turns, a round's O product and S product at a time: left to themselves
-                    // they fall into step, both on the tensor cores, then both in their softmax
-                    ok = wait(&turn[i], nturn);
-                    nturn ^= 1u;
-                    if (!ok) break;
+                    auto issue_s = [&]() {                   // (leader) S of step j + 1
+                        const uint64_t d = dk + static_cast<uint64_t>(c.slot * (G::kTile >> 4));
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint64_t off = ((ks >> 2) * G::kPlane + (ks & 3) * 32) >> 4;
+                            tc::mma_ss(ts, dq + off, d + off, kIdS, ks > 0);
+                        }
+                        tc::commit(&s_full[i]);
+                        if (j + 2 == ni) tc::commit(&q_empty[i]);
+                    };
+                    if constexpr (G::kOwnP) {
+                        // S of the next step as soon as this one's is in registers: it runs under the softmax
+                        if (j + 1 < ni) {
+                            ok = j < 0 ? wait(&q_full[i], nq) : wait(&s_read[i], nr);
+                            if (!ok) break;
+                            if (j < 0) nq ^= 1u;
+                            else nr ^= 1u;
+                            tc::fence_after_sync();
+                            if (leader) issue_s();
+                        }
+                        // (the item's last S is read too before the next item's first replaces it: by the softmax
+                        // threads that wrote the P this waits for)
+                        if (j >= 0 && j == ni - 1) nr ^= 1u;
+                        if (leader && more_k) tc::commit(&empty[c.slot]);
+                    } else {
+                        // the tiles take turns, a round's O product and S product at a time: left to themselves
+                        // they fall into step, both on the tensor cores, then both in their softmax
+                        ok = wait(&turn[i], nturn);
+                        nturn ^= 1u;
+                        if (!ok) break;
+                    }
                     if (j >= 0 && j < ni) {
                         const int left = it.end_of(i) - (it.step0 + j) * kStep;   // (16 a product, none wholly past the end)
                         const uint64_t d = dv + static_cast<uint64_t>(v.slot * (G::kTile >> 4));
@@ -663,38 +697,37 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                                 if (left >= kStep - 15) {
 #pragma unroll
                                     for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                        tc::mma_ts(to, ts + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                                        tc::mma_ts(to, tp + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
                                 } else {
 #pragma unroll 1
                                     for (int kk = 4 * half; kk < 4 * half + 4 && kk * 16 < left; ++kk)
-                                        tc::mma_ts(to, ts + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                                        tc::mma_ts(to, tp + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
                                 }
                             }
                         }
                         np ^= 1u;
                         if (!ok) break;
+                        if (G::kOwnP && leader) tc::commit(&o_step[i]);
                     }
-                    if (j < 0 && ni > 0) {
-                        ok = wait(&q_full[i], nq);
-                        nq ^= 1u;
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                    }
-                    if (leader) {
-                        if (j + 1 < ni) {
-                            const uint64_t d = dk + static_cast<uint64_t>(c.slot * (G::kTile >> 4));
-#pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks) {
-                                const uint64_t off = ((ks >> 2) * G::kPlane + (ks & 3) * 32) >> 4;
-                                tc::mma_ss(ts, dq + off, d + off, kIdS, ks > 0);
-                            }
-                            tc::commit(&s_full[i]);
-                            if (j + 2 == ni) tc::commit(&q_empty[i]);
+                    if constexpr (G::kOwnP) {
+                        if (leader && j >= 0) {
+                            if (j == ni - 1) tc::commit(&o_full[i]);
+                            tc::commit(&empty[v.slot]);
                         }
-                        mbar_arrive(&turn[1 - i]);
-                        if (j >= 0 && j == ni - 1) tc::commit(&o_full[i]);
-                        if (j >= 0) tc::commit(&empty[v.slot]);
-                        if (more_k) tc::commit(&empty[c.slot]);
+                    } else {
+                        if (j < 0 && ni > 0) {
+                            ok = wait(&q_full[i], nq);
+                            nq ^= 1u;
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                        }
+                        if (leader) {
+                            if (j + 1 < ni) issue_s();
+                            mbar_arrive(&turn[1 - i]);
+                            if (j >= 0 && j == ni - 1) tc::commit(&o_full[i]);
+                            if (j >= 0) tc::commit(&empty[v.slot]);
+                            if (more_k) tc::commit(&empty[c.slot]);
+                        }
                     }
                     if (more_k) c.next();
                 }
@@ -883,9 +916,9 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
         const int wg = warp >> 2;
         const int t = threadIdx.x & 127;
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t ts = tl + G::kColS + wg * 128, to = tl + G::kColO + wg * 128;
+        const uint32_t ts = tl + G::kColS + wg * 128, to = tl + G::kColO + wg * D, tp = tl + G::kColP + wg * G::kStrideP;
         OT* out = static_cast<OT*>(a.out);
-        unsigned ns = 0, no = 0, nraw = 0;
+        unsigned ns = 0, no = 0, nraw = 0, nstep = 0;
         Item it;
         bool ok = !*abort_flag;
 #pragma unroll 1
@@ -937,6 +970,10 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc::ld32(x[c], ts + 32 * c);
                 tc::wait_ld();
+                if constexpr (G::kOwnP) {
+                    tc::fence_before_sync();
+                    mbar_arrive(&s_read[wg]);
+                }
                 const int vis = seen - (it.step0 + j) * kStep;
                 if (__any_sync(0xffffffffu, vis < kStep)) {
 #pragma unroll
@@ -959,8 +996,18 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                     if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - top);
                     m_ref = top;
                 }
+                if constexpr (G::kOwnP) {
+                    // the last step's O product reads P's columns and writes O
+                    if (j > 0) {
+                        ok = wait_bar(&o_step[wg], nstep & 1, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        ++nstep;
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                    }
+                }
                 if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-                    // (S of this step was issued after the last O product: that is done)
+                    // (where P takes S's place, S of this step was issued after the last O product: that is done)
                     l *= alpha;
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 16) {
@@ -988,7 +1035,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                         else sum0 = add2(sum0, pack64(p0, p1));
                         w[e] = Mma<T>::pack(p0, p1);
                     }
-                    tc::st32(ts + 32 * h, w);
+                    tc::st32(tp + 32 * h, w);
                     tc::wait_st();
                     tc::fence_before_sync();
                     mbar_arrive(&p_full[2 * wg + h]);
@@ -1003,6 +1050,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             const int64_t slot = static_cast<int64_t>(it.kvh) * a.part_cap + (it.split >> 16) + ((it.split >> 8) & 255);
             float4* prow = a.part_o + slot * (D / 4) * a.part_rows + myrow;      // [column / 4][row]
             if (n > 0) {
+                if (G::kOwnP) ++nstep;                       // (the last step's, of which this is the completion)
                 ok = wait_bar(&o_full[wg], no & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 ++no;

@@ -31,7 +31,7 @@ __device__ __forceinline__ int tiles_of(const Seq& q, int group) { return (q.n *
 
 __device__ __forceinline__ int warp_scan(int v) {            // inclusive
     const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;

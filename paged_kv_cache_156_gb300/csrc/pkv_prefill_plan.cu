@@ -37,7 +37,7 @@ static_assert(kPrefillMaxParts == 152, "the last candidate");
 constexpr int kItemCost = 2;         // steps' worth of an item's query load and epilogue
 constexpr int kSplitCost = 3;        // and of a part's partial output and its share of the merge
 constexpr int kMinPart = 2;          // steps of a part at least
-constexpr int kBuckets = 128;
+constexpr int kBuckets = 32;         // (one a lane of the scan)
 
 using pf::load_seq;
 using pf::Seq;
@@ -65,8 +65,11 @@ struct Shared {
     int part_len, max_item, next_slot, next_merge;
 };
 
+// (The kernel runs every instruction about once, so it is bound by fetching them: what is used twice is a function,
+// and no loop is unrolled.  Inlined and unrolled it was 45 KB and took 7 us.)
+
 // Loads a chunk of sequences and their tile offsets.
-__device__ void load_chunk(const PrefillArgs& a, Shared& sh, int base, bool report) {
+__device__ __noinline__ void load_chunk(const PrefillArgs& a, Shared& sh, int base, bool report) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int s = base + t;
     Seq q{0, 0, 0};
@@ -89,13 +92,21 @@ __device__ void load_chunk(const PrefillArgs& a, Shared& sh, int base, bool repo
 // The chunk's sequence (0 .. 1023) that holds a tile.
 __device__ __forceinline__ int find_seq(const Shared& sh, int tile) {
     int lo = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = kThreads / 2; w > 0; w >>= 1)
         if (sh.first[lo + w] <= tile) lo += w;
     return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArgs a) {
+// Tile i of the current chunk: its sequence and steps.
+__device__ __noinline__ int tile_of(const PrefillArgs& a, const Shared& sh, int i, int* k) {
+    *k = find_seq(sh, i);
+    return tile_steps(Seq{sh.start[*k], sh.n[*k], sh.len[*k]}, a.group, i - sh.first[*k]);
+}
+
+__device__ __noinline__ int parts_of(int steps, int P) { return max(1, (steps + P - 1) / P); }
+
+__global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __grid_constant__ PrefillArgs a) {
     __shared__ Shared sh;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     grid_dependency_wait();
@@ -103,27 +114,19 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     if (t == 0) sh.next_slot = sh.next_merge = 0;
     if (t < kBuckets) sh.bucket[t] = 0;
     const bool one_chunk = a.num_seqs <= kThreads;
-    // tile i of the current chunk: its sequence and steps
-    auto tile_of = [&](int i, bool cached, int& k) {
-        if (cached) {
-            k = sh.seq[i];
-            return sh.steps[i];
-        }
-        k = find_seq(sh, i);
-        return tile_steps(Seq{sh.start[k], sh.n[k], sh.len[k]}, a.group, i - sh.first[k]);
-    };
-
     // ---- tiles, their steps' sum and maximum
     int mx = 0;
     long long tiles_all = 0;
     unsigned long long sum = 0;
+#pragma unroll 1
     for (int base = 0; base < a.num_seqs; base += kThreads) {
         load_chunk(a, sh, base, true);
         const int tiles = sh.first[kThreads];
         const bool keep = one_chunk && tiles <= kCached;
+#pragma unroll 1
         for (int i = t; i < tiles; i += kThreads) {
             int k;
-            const int st = tile_of(i, false, k);
+            const int st = tile_of(a, sh, i, &k);
             if (keep) {
                 sh.steps[i] = st;
                 sh.seq[i] = k;
@@ -143,70 +146,85 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     }
     __syncthreads();
     const int maxs = __reduce_max_sync(0xffffffffu, sh.wmax[lane]);
+    unsigned long long steps = sh.wsum[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
 
     // ---- the part length: a warp a candidate counts every tile's parts at it.  (The host rules splitting out
     // by the same count of tiles; a batch that the plan would have to reload is not split either.)
+    // Nor is one whose longest tile is well below what every CTA has to do anyway: cutting it shortens nothing.
     const long long nh = a.num_kv_heads;
-    const bool may_split = a.may_split && cached && maxs > kMinPart && tiles_all * nh < 8ll * a.slots;
-    if (may_split && warp < kCand) {
-        const int P = max(kMinPart, (maxs + kParts[warp] - 1) / kParts[warp]);
-        int all = 0, split = 0;
-        for (int i = lane; i < tiles_all; i += 32) {
-            const int parts = max(1, (sh.steps[i] + P - 1) / P);
-            all += parts;
-            split += parts > 1 ? parts : 0;
+    const float each = (static_cast<float>(steps) + kItemCost * static_cast<float>(tiles_all)) * nh / a.slots;
+    const bool may_split = a.may_split && cached && maxs > kMinPart && tiles_all * nh < 8ll * a.slots &&
+                           maxs + kItemCost > 0.6f * each;
+    int P = max(1, maxs), top = P;                           // the part length, the longest item
+    if (may_split) {
+        if (warp < kCand) {
+            const int Pw = max(kMinPart, (maxs + kParts[warp] - 1) / kParts[warp]);
+            int all = 0, split = 0;
+#pragma unroll 1
+            for (int i = lane; i < tiles_all; i += 32) {
+                const int parts = parts_of(sh.steps[i], Pw);
+                all += parts;
+                split += parts > 1 ? parts : 0;
+            }
+            all = __reduce_add_sync(0xffffffffu, all);
+            split = __reduce_add_sync(0xffffffffu, split);
+            if (lane == 0) {
+                sh.items[warp] = all;
+                sh.parts[warp] = split;
+            }
         }
-        all = __reduce_add_sync(0xffffffffu, all);
-        split = __reduce_add_sync(0xffffffffu, split);
-        if (lane == 0) {
-            sh.items[warp] = all;
-            sh.parts[warp] = split;
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {
-        long long best = 1ll << 62;
-        if (may_split && lane < kCand) {
-            unsigned long long steps = 0;
-            for (int w = 0; w < kWarps; ++w) steps += sh.wsum[w];
-            const int P = max(kMinPart, (maxs + kParts[lane] - 1) / kParts[lane]);
-            const long long items = sh.items[lane], parts = sh.parts[lane];
-            const bool fits = parts <= a.part_cap && tiles_all + parts <= a.capacity &&
-                              (maxs + P - 1) / P <= kPrefillMaxParts;
-            const long long top = min(P, maxs) + kItemCost + (parts > 0 ? kSplitCost : 0);
-            const long long load = (static_cast<long long>(steps) + kItemCost * items + kSplitCost * parts) * nh;
-            // in sixteenths of a step, the candidate's index breaking ties towards fewer parts
-            const long long est = items * nh <= a.slots ? 16 * top : max(16 * top, 16 * load / a.slots + 8 * top);
-            if (fits) best = est * 32 + lane;
-        }
+        __syncthreads();
+        if (warp == 0) {
+            unsigned long long best = ~0ull;
+            if (lane < kCand) {
+                const int P = max(kMinPart, (maxs + kParts[lane] - 1) / kParts[lane]);
+                const long long items = sh.items[lane], parts = sh.parts[lane];
+                const bool fits = parts <= a.part_cap && tiles_all + parts <= a.capacity &&
+                                  (maxs + P - 1) / P <= kPrefillMaxParts;
+                const float top = static_cast<float>(min(P, maxs) + kItemCost + (parts > 0 ? kSplitCost : 0));
+                const float load = (static_cast<float>(steps) + kItemCost * static_cast<float>(items) +
+                                    kSplitCost * static_cast<float>(parts)) * nh / a.slots;
+                const float est = items * nh <= a.slots ? top : fmaxf(top, load + 0.5f * top);
+                // (positive floats order as their bits; the candidate's index breaks ties towards fewer parts)
+                if (fits) best = static_cast<unsigned long long>(__float_as_uint(est)) << 32 | lane;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-        if (lane == 0) {
-            const int k = best == (1ll << 62) ? 1 : kParts[best & 31];
-            const int P = k == 1 ? max(1, maxs) : max(kMinPart, (maxs + k - 1) / k);
-            sh.part_len = P;
-            sh.max_item = min(P, max(1, maxs));
+            for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+            if (lane == 0) {
+                const int k = best == ~0ull ? 1 : kParts[best & 31];
+                const int P = k == 1 ? max(1, maxs) : max(kMinPart, (maxs + k - 1) / k);
+                sh.part_len = P;
+                sh.max_item = min(P, max(1, maxs));
+            }
         }
+        __syncthreads();
+        P = sh.part_len;
+        top = sh.max_item;
     }
-    __syncthreads();
-    const int P = sh.part_len, top = sh.max_item;
 
     // ---- items by length: count, offsets, write
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
         for (int base = 0; base < a.num_seqs; base += kThreads) {
             if (!one_chunk) load_chunk(a, sh, base, false);
             const int tiles = sh.first[kThreads];
-            for (int i = t; i < tiles; i += kThreads) {
+#pragma unroll 1
+        for (int i = t; i < tiles; i += kThreads) {
                 int k;
-                const int st = tile_of(i, cached, k);
+                const int st = cached ? sh.steps[i] : tile_of(a, sh, i, &k);
+                if (cached) k = sh.seq[i];
                 const int tile = i - sh.first[k];
-                const int parts = max(1, (st + P - 1) / P);
+                const int parts = parts_of(st, P);
                 const int len = (st + parts - 1) / parts;           // equal parts
                 int slot = 0;
                 if (pass == 1 && parts > 1) {
                     slot = atomicAdd(&sh.next_slot, parts);
                     a.merges[atomicAdd(&sh.next_merge, 1)] = make_int4(prefill_split(parts, 0, slot), tile, sh.start[k], sh.n[k]);
                 }
+#pragma unroll 1
                 for (int p = 0; p < parts; ++p) {
                     const int s0 = min(st, p * len), s1 = min(st, s0 + len);
                     const int b = min(kBuckets - 1, (top - (s1 - s0)) * kBuckets / (top + 1));
@@ -226,14 +244,9 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
         __syncthreads();
         if (pass == 0) {
             if (warp == 0) {
-                int carry = 0;
-                for (int b0 = 0; b0 < kBuckets; b0 += 32) {
-                    const int v = sh.bucket[b0 + lane];
-                    const int inc = warp_scan(v);
-                    sh.at[b0 + lane] = carry + inc - v;
-                    carry += __shfl_sync(0xffffffffu, inc, 31);
-                }
-                if (lane == 0) a.header[0] = min(carry, a.capacity);
+                const int v = sh.bucket[lane], inc = warp_scan(v);
+                sh.at[lane] = inc - v;
+                if (lane == 31) a.header[0] = min(inc, a.capacity);
             }
         } else if (t == 0) {
             a.header[1] = sh.next_merge;
