@@ -966,31 +966,38 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 ++ns;
                 if (!ok) break;
                 tc::fence_after_sync();
-                uint32_t x[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc::ld32(x[c], ts + 32 * c);
-                tc::wait_ld();
-                if constexpr (G::kOwnP) {
-                    tc::fence_before_sync();
-                    mbar_arrive(&s_read[wg]);
-                }
+                // Two passes over S, a rolled loop of two halves each, S read from TMEM again for the second: half
+                // the code of one pass with S in registers, and the code of the loops is what the schedulers'
+                // instruction caches must hold beside the MMA warps'.
                 const int vis = seen - (it.step0 + j) * kStep;
-                if (__any_sync(0xffffffffu, vis < kStep)) {
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t x[2][32];
+                    tc::ld32(x[0], ts + 64 * h);
+                    tc::ld32(x[1], ts + 64 * h + 32);
+                    tc::wait_ld();
+                    if (__any_sync(0xffffffffu, vis < 64 * h + 64)) {            // masked scores go back as -inf
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e >= vis) x[c][e] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (64 * h + 32 * c + e >= vis) x[c][e] = 0xff800000u;
+                            tc::st32(ts + 64 * h + 32 * c, x[c]);
+                        }
+                        tc::wait_st();
+                    }
+                    float mx[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        mx[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
+#pragma unroll
+                        for (int e = 3; e < 31; e += 2) mx[c] = max3(mx[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                        mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
+                    }
+                    top = max3(top, mx[0], mx[1]);
                 }
-                float mx[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mx[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
-#pragma unroll
-                    for (int e = 3; e < 31; e += 2) mx[c] = max3(mx[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-                    mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
-                }
-                const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sl2;
+                top *= sl2;
                 float alpha = 1.0f;
                 if (top > m_ref + 8.0f) {
                     if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - top);
@@ -1023,12 +1030,21 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 const float off = m_ref == -INFINITY ? -INFINITY : -m_ref;
                 const uint64_t offx2 = pack64(off, off);
                 uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
+                    uint32_t x[2][32], w[32];
+                    tc::ld32(x[0], ts + 64 * h);
+                    tc::ld32(x[1], ts + 64 * h + 32);
+                    tc::wait_ld();
+                    if constexpr (G::kOwnP) {
+                        if (h == 1) {
+                            tc::fence_before_sync();
+                            mbar_arrive(&s_read[wg]);
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const uint32_t* y = &x[2 * h + (e >> 4)][2 * (e & 15)];
+                        const uint32_t* y = &x[e >> 4][2 * (e & 15)];
                         const float2 z = unpack64(fma2(pack64(__uint_as_float(y[0]), __uint_as_float(y[1])), sl2x2, offx2));
                         const float p0 = fast_exp2(z.x), p1 = fast_exp2(z.y);
                         if (e & 1) sum1 = add2(sum1, pack64(p0, p1));
