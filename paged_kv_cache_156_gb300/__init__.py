@@ -523,14 +523,14 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
         max_seq_len = int(seq_lens.max().item()) if B else 0
     if workspace is None:
         workspace = alloc_prefill_workspace(B, T, Hq, Hkv, d, q.device)
-    args = [*ptrs, block_tables.shape[1], *lens, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB, float(scale), _DT[q.dtype]]
-    rest = [_cuda("workspace", workspace), workspace.numel() * workspace.element_size(), PLANNED if planned else 0,
-            _stream(q)]
+    scales = [_scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv)] if kv8 else []
+    args = [*ptrs, block_tables.shape[1], *lens, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB, float(scale), _DT[q.dtype],
+            *scales, _cuda("workspace", workspace), workspace.numel() * workspace.element_size(),
+            PLANNED if planned else 0, _stream(q)]
     if kv8:
-        _check(load().pkv_paged_attention_prefill_fp8(*args, _scales("k_scale", k_scale, Hkv),
-                                                      _scales("v_scale", v_scale, Hkv), *rest))
+        _check(load().pkv_paged_attention_prefill_fp8(*args))
     else:
-        _check(load().pkv_paged_attention_prefill(*args, *rest))
+        _check(load().pkv_paged_attention_prefill(*args))
 
 
 @_one_device
