@@ -721,7 +721,8 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = planned || a.direct ? cudaSuccess : pkv::launch_prefill_plan(a, s);
+    a.local = !planned && !a.direct && pkv::prefill_local(num_seqs, num_tokens, num_heads, num_kv_heads, a.slots, lay);
+    cudaError_t e = planned || a.direct || a.local ? cudaSuccess : pkv::launch_prefill_plan(a, s);
     if (e == cudaSuccess) e = pkv::launch_prefill(a, tmq, tmk, tmv, dt == PKV_F16 ? 0 : 1, head_dim, s);
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
     return ok();

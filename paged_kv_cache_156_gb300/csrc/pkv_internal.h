@@ -209,6 +209,10 @@ constexpr int kPrefillRows = 256;
 constexpr int kPrefillSub = 128;                // rows of one of an item's two tiles (the MMA's M)
 constexpr int kPrefillStep = 128;
 constexpr int kPrefillMaxParts = 152;           // parts one tile's positions are split into at most
+constexpr int kPrefillMinPart = 2;              // steps of a part at least
+// The prefill kernel plans by itself up to this many sequences and tiles a KV head, and items (parts and all)
+constexpr int kPrefillLocal = 512;
+constexpr int kPrefillLocalItems = 1024;
 
 struct PrefillArgs {
     void* out;                       // [num_tokens][num_heads][D]
@@ -238,6 +242,7 @@ struct PrefillArgs {
     int slots;                       // CTAs the grid may hold at once
     int may_split;                   // 0: the plan splits no tile (no merge kernel follows)
     int direct;                      // 1: no plan: a CTA finds its item by itself (at most one each)
+    int local;                       // 1: every CTA plans for itself (the same plan as the plan kernel's)
     int q_tma;                       // 1: a Q tile is one TMA box a column plane (the group divides 128)
     int negate_q;                    // scale < 0
     float scale_log2;                // |scale| * log2(e)
@@ -260,6 +265,9 @@ PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int 
 bool prefill_may_split(int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots);
 // A call so small that every item has a CTA of its own and none is split: no plan is made or read.
 bool prefill_direct(int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots);
+// A batch small enough for every CTA to plan it by itself, in its own shared memory, instead of a plan kernel.
+bool prefill_local(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads, int slots,
+                   const PrefillWorkspace& w);
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            int dtype, int head_dim, cudaStream_t s);

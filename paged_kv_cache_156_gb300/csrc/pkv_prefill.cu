@@ -322,12 +322,120 @@ __device__ __forceinline__ void copy_q(const PrefillArgs& a, const Item& it, int
     __syncwarp();
 }
 
+// ---------------------------------------------------------------- planning by the CTA itself
+struct LocalPlan {
+    int start[kPrefillLocal], n[kPrefillLocal], len[kPrefillLocal];      // sequences
+    int first[kPrefillLocal + 1];                                        // their first tiles
+    int steps[kPrefillLocal], seq[kPrefillLocal], slot[kPrefillLocal];   // tiles
+    alignas(16) int key[kPrefillLocalItems];                             // items: length and order
+    int ref[kPrefillLocalItems];                                         // tile, part
+    int order[kPrefillLocalItems];                                       // by rank
+    int scan[16], wmax[16], wsum[16];
+    pf::Choice choice;
+};
+
+// Exclusive scan of v over the block; *total: its sum.
+__device__ __forceinline__ int block_scan(int v, int* scan, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int inc = pf::warp_scan(v);
+    __syncthreads();
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    const int w = pf::warp_scan(lane < 16 ? scan[lane] : 0);
+    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    *total = __shfl_sync(0xffffffffu, w, 15);
+    return inc - v + (warp > 0 ? before : 0);
+}
+
+// The plan kernel's plan (pkv_prefill_plan.cu), made by a CTA of 512 threads in its own shared memory and so ordered
+// without atomics, the same in every CTA: an item's rank is the number of longer ones and of equally long ones
+// before it.  Returns the number of items a KV head.  CTA 0 reports bad bounds and lists the split tiles.
+__device__ __forceinline__ int local_plan(const PrefillArgs& a, LocalPlan& lp) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const bool report = blockIdx.x == 0;
+    pf::Seq q{0, 0, 0};
+    if (t < a.num_seqs) q = pf::load_seq(a, t, report);
+    lp.start[t] = q.start;
+    lp.n[t] = q.n;
+    lp.len[t] = q.len;
+    int tiles;
+    lp.first[t] = block_scan(pf::tiles_of(q, a.group), lp.scan, &tiles);
+    if (t == 0) lp.first[kPrefillLocal] = tiles;
+    tiles = min(tiles, kPrefillLocal);                       // (more only where the starts decrease: reported)
+    __syncthreads();
+    int st = 0, k = 0;
+    if (t < tiles) {
+#pragma unroll 1
+        for (int w = kPrefillLocal / 2; w > 0; w >>= 1)
+            if (lp.first[k + w] <= t) k += w;
+        st = pf::tile_steps(pf::Seq{lp.start[k], lp.n[k], lp.len[k]}, a.group, t - lp.first[k]);
+    }
+    lp.steps[t] = st;
+    lp.seq[t] = k;
+    const int wm = __reduce_max_sync(0xffffffffu, st), ws = __reduce_add_sync(0xffffffffu, st);
+    if (lane == 0) {
+        lp.wmax[warp] = wm;
+        lp.wsum[warp] = ws;
+    }
+    __syncthreads();
+    const int maxs = __reduce_max_sync(0xffffffffu, lane < 16 ? lp.wmax[lane] : 0);
+    unsigned long long sum = 0;
+    for (int w = 0; w < 16; ++w) sum += lp.wsum[w];
+    const int P = pf::choose_part<16>(a, lp.choice, lp.steps, tiles, maxs, static_cast<float>(sum));
+    // items, partial slots and split tiles before this tile, in one scan (11, 11 and 10 bits)
+    const int parts = t < tiles ? pf::parts_of(st, P) : 0;
+    int total;
+    const int at = block_scan(parts | (parts > 1 ? parts << 11 | 1 << 22 : 0), lp.scan, &total);
+    const int item0 = at & 2047, slot = at >> 11 & 2047, merge = static_cast<unsigned>(at) >> 22;
+    const int items = total & 2047;
+    lp.slot[t] = slot;
+    const int len = parts > 0 ? (st + parts - 1) / parts : 0;
+    for (int p = 0; p < parts; ++p) {
+        const int s0 = min(st, p * len);
+        lp.key[item0 + p] = (min(st, s0 + len) - s0) << 10 | (kPrefillLocalItems - 1 - item0 - p);
+        lp.ref[item0 + p] = t << 8 | p;
+    }
+    if (report) {
+        if (parts > 1) a.merges[merge] = make_int4(prefill_split(parts, 0, slot), t - lp.first[k], lp.start[k], lp.n[k]);
+        if (t == 0) a.header[1] = static_cast<unsigned>(total) >> 22;
+    }
+    if (t < 3 && items + t < kPrefillLocalItems) lp.key[items + t] = -1;      // (the last four are read whole)
+    __syncthreads();
+#pragma unroll 1
+    for (int i = t; i < items; i += 512) {
+        const int key = lp.key[i];
+        int rank = 0;
+        const int4* all = reinterpret_cast<const int4*>(lp.key);
+#pragma unroll 2
+        for (int j = 0; 4 * j < items; ++j) {
+            const int4 o = all[j];
+            rank += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+        }
+        lp.order[rank] = i;
+    }
+    lp.wsum[warp] = P;                                       // (for the entries)
+    __syncthreads();
+    return items;
+}
+
+// The entry of rank e of a local plan.
+__device__ __forceinline__ Entry local_entry(const LocalPlan& lp, int e, int kvh) {
+    const int P = lp.wsum[0], ref = lp.ref[lp.order[e]], t = ref >> 8, p = ref & 255, k = lp.seq[t], st = lp.steps[t];
+    const int parts = pf::parts_of(st, P), len = (st + parts - 1) / parts, s0 = min(st, p * len);
+    Entry n;
+    n.x = make_int4(k, t - lp.first[k], s0, min(st, s0 + len));
+    n.y = make_int4(lp.start[k], lp.n[k], lp.len[k], parts > 1 ? prefill_split(parts, p, lp.slot[t]) : 0);
+    n.kvh = kvh;
+    n.live = true;
+    return n;
+}
+
 // T: the products' type; KV8: E4M3 pools (codes expanded to f16, every one exact there); OT: q's and out's.
 template <typename T, int D, bool KV8, typename OT>
 __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
                                                                         const __grid_constant__ CUtensorMap tmk,
                                                                         const __grid_constant__ CUtensorMap tmv,
-                                                                        const PrefillArgs a) {
+                                                                        const __grid_constant__ PrefillArgs a) {
     using G = PfGeo<D, KV8>;
     constexpr int ST = G::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -401,6 +509,20 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();
+    // ---- without a plan kernel: the CTA plans here, over the still idle tiles, and lane r of the plan warp takes
+    // round r's entry
+    Entry mine{};
+    if (a.local) {
+        LocalPlan& lp = *reinterpret_cast<LocalPlan*>(smem);
+        static_assert(sizeof(LocalPlan) <= G::kBars, "the scratch lies in the tiles");
+        const int total = local_plan(a, lp) * a.num_kv_heads;
+        if (warp == G::kPlan) {
+            const int g = gridDim.x, b = blockIdx.x, w = lane * g + ((lane & 1) ? g - 1 - b : b);
+            if (w < total) mine = local_entry(lp, w / a.num_kv_heads, w % a.num_kv_heads);
+        }
+        fence_proxy_async_smem();                   // the scratch before the tiles' copies
+        __syncthreads();
+    }
     Item* list = reinterpret_cast<Item*>(smem + G::kList);
     // The round's item for one warp; false: none is left, or a wait gave up.
     auto get_item = [&](int r, Item& it, bool& ok) {
@@ -784,8 +906,20 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             // (the first entry is read beside the count of items, not after it: entries past the count are stale)
             Entry next{};
             int total = 0;
+            auto round_entry = [&](int r) {                  // (local plan)
+                Entry n;
+                n.x = make_int4(__shfl_sync(0xffffffffu, mine.x.x, r), __shfl_sync(0xffffffffu, mine.x.y, r),
+                                __shfl_sync(0xffffffffu, mine.x.z, r), __shfl_sync(0xffffffffu, mine.x.w, r));
+                n.y = make_int4(__shfl_sync(0xffffffffu, mine.y.x, r), __shfl_sync(0xffffffffu, mine.y.y, r),
+                                __shfl_sync(0xffffffffu, mine.y.z, r), __shfl_sync(0xffffffffu, mine.y.w, r));
+                n.kvh = __shfl_sync(0xffffffffu, mine.kvh, r);
+                n.live = __shfl_sync(0xffffffffu, static_cast<int>(mine.live), r) != 0;
+                return n;
+            };
             if (a.direct) {
                 next = find_entry(a);
+            } else if (a.local) {
+                next = round_entry(0);
             } else {
                 next = fetch_entry(a, a.capacity * a.num_kv_heads, 0);
                 total = min(max(__ldcg(a.header), 0), a.capacity) * a.num_kv_heads;
@@ -798,7 +932,9 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 more = next.live;
                 if (more) {
                     read_item(a, next, it);
-                    next = fetch_entry(a, total, r + 1);
+                    if (!a.local) next = fetch_entry(a, total, r + 1);
+                    else if (r < 31) next = round_entry(r + 1);
+                    else next.live = false;
                 } else {
                     it.rows = -1;
                 }

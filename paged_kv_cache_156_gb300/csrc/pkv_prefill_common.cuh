@@ -1,4 +1,5 @@
-// What the prefill plan and the prefill kernel share: a sequence's bounds, and its tiles.
+// What the prefill plan and the prefill kernel share: a sequence's bounds, its tiles, and whether and how far tiles are
+// split.
 #pragma once
 
 #include "pkv_device.cuh"
@@ -29,6 +30,14 @@ __device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int s, bool report
 
 __device__ __forceinline__ int tiles_of(const Seq& q, int group) { return (q.n * group + kPrefillRows - 1) / kPrefillRows; }
 
+// Steps the last row of a tile sees.
+__device__ __forceinline__ int tile_steps(const Seq& q, int group, int tile) {
+    const int rows = q.n * group;
+    const int last = min(rows, (tile + 1) * kPrefillRows) - 1;
+    const int lim = min(q.len, max(0, q.len - q.n + last / group + 1));
+    return (lim + kPrefillStep - 1) / kPrefillStep;
+}
+
 __device__ __forceinline__ int warp_scan(int v) {            // inclusive
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -37,6 +46,74 @@ __device__ __forceinline__ int warp_scan(int v) {            // inclusive
         if (lane >= o) v += u;
     }
     return v;
+}
+
+__device__ __forceinline__ int parts_of(int steps, int P) { return max(1, (steps + P - 1) / P); }
+
+constexpr int kCand = 24;
+// Parts that candidate c cuts the longest tile into: 1 .. 10, then ever wider apart up to kPrefillMaxParts.
+__device__ __forceinline__ int cand_parts(int c) {
+    return c < 10 ? c + 1 : c < kCand - 1 ? 10 + ((c - 9) * (c - 9) * 29 + 20) / 40 : kPrefillMaxParts;
+}
+constexpr int kItemCost = 2;         // steps' worth of an item's query load and epilogue
+constexpr int kSplitCost = 3;        // and of a part's partial output and its share of the merge
+
+struct Choice {
+    int items[kCand], parts[kCand];  // per candidate: all items; parts of split tiles
+    int part_len;
+};
+
+// The part length P of a batch whose tiles' steps are in `steps`, by a block of WARPS warps: the longest tile's
+// length (no split), or the candidate with the smallest estimated end,
+//
+//     (steps + kItemCost * items + kSplitCost * parts) * KV heads / SMs
+//         + half the largest item             when the items outnumber the SMs,
+//     the largest item                        otherwise
+//
+// (the first line is the average load plus the expected overhang of a longest-first schedule).  Tiles are not split
+// when there are many for every SM, nor when the longest is well below what every CTA has to do anyway.
+template <int WARPS>
+__device__ __forceinline__ int choose_part(const PrefillArgs& a, Choice& ch, const int* steps, int tiles, int maxs, float sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float nh = static_cast<float>(a.num_kv_heads), slots = static_cast<float>(a.slots);
+    const float each = (sum + kItemCost * static_cast<float>(tiles)) * nh / slots;
+    if (!a.may_split || maxs <= kPrefillMinPart || tiles * nh >= 8.0f * slots || maxs + kItemCost <= 0.6f * each)
+        return max(1, maxs);
+#pragma unroll 1
+    for (int c = warp; c < kCand; c += WARPS) {
+        const int k = cand_parts(c), P = max(kPrefillMinPart, (maxs + k - 1) / k);
+        int all = 0, split = 0;
+#pragma unroll 1
+        for (int i = lane; i < tiles; i += 32) {
+            const int parts = parts_of(steps[i], P);
+            all += parts;
+            split += parts > 1 ? parts : 0;
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        split = __reduce_add_sync(0xffffffffu, split);
+        if (lane == 0) {
+            ch.items[c] = all;
+            ch.parts[c] = split;
+        }
+    }
+    __syncthreads();
+    // (every warp chooses for itself)
+    unsigned best = 0xffffffffu;
+    int P = max(1, maxs);
+    if (lane < kCand) {
+        const int k = cand_parts(lane);
+        if (lane > 0) P = max(kPrefillMinPart, (maxs + k - 1) / k);
+        const int items = ch.items[lane], parts = ch.parts[lane];
+        const float top = static_cast<float>(min(P, maxs) + kItemCost + (parts > 0 ? kSplitCost : 0));
+        const float load = (sum + kItemCost * static_cast<float>(items) + kSplitCost * static_cast<float>(parts)) * nh / slots;
+        const float est = items * nh <= slots ? top : fmaxf(top, load + 0.5f * top);
+        // (positive floats order as their bits)
+        if (parts <= a.part_cap && tiles + parts <= a.capacity && (maxs + P - 1) / P <= kPrefillMaxParts) best = __float_as_uint(est);
+    }
+    const unsigned least = __reduce_min_sync(0xffffffffu, best);
+    const unsigned m = __ballot_sync(0xffffffffu, best == least && lane < kCand);
+    const int win = least == 0xffffffffu ? 0 : __ffs(m) - 1;              // ties: fewer parts
+    return least == 0xffffffffu ? max(1, maxs) : __shfl_sync(0xffffffffu, P, win);
 }
 
 }  // namespace pf

@@ -6,17 +6,14 @@
 // its last row sees.  Tiles are listed longest first, so that the persistent
 // CTAs, which take items round robin, end at about the same time.  When a few
 // long tiles would leave SMs idle (a handful of rows over a long cache), every
-// tile is cut into parts of P steps whose partial softmax states the last part
-// to finish merges.  P is the candidate with the smallest estimated end:
+// tile is cut into parts whose partial softmax states a merge kernel joins
+// (pf::choose_part).  The order of equally long items, and which partial slot a
+// tile gets, vary from run to run; no result depends on either, since the merge
+// sums parts in part order.
 //
-//     (steps + kItemCost * items + kSplitCost * parts) * KV heads / SMs
-//         + half the largest item             when the items outnumber the SMs,
-//     the largest item                        otherwise
-//
-// (the first line is the average load plus the expected overhang of a
-// longest-first schedule).  The order of equally long items, and which partial
-// slot a tile gets, vary from run to run; no result depends on either, since
-// the merge sums parts in part order.
+// A single call over a batch of moderate size does not run this kernel: every
+// CTA of the prefill kernel makes the same plan by itself.  This one serves the
+// calls that share a plan (a step's layers) and the largest batches.
 //
 // One CTA: a few bytes per sequence, latency-bound.
 #include <cuda_runtime.h>
@@ -31,25 +28,13 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCand = 24;
-__constant__ const int kParts[kCand] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 19, 21, 25, 30, 38, 50, 64, 76, 100, 128, 152};
-static_assert(kPrefillMaxParts == 152, "the last candidate");
-constexpr int kItemCost = 2;         // steps' worth of an item's query load and epilogue
-constexpr int kSplitCost = 3;        // and of a part's partial output and its share of the merge
-constexpr int kMinPart = 2;          // steps of a part at least
 constexpr int kBuckets = 32;         // (one a lane of the scan)
 
 using pf::load_seq;
+using pf::parts_of;
 using pf::Seq;
+using pf::tile_steps;
 using pf::warp_scan;
-
-// Steps the last row of a tile sees.
-__device__ __forceinline__ int tile_steps(const Seq& q, int group, int tile) {
-    const int rows = q.n * group;
-    const int last = min(rows, (tile + 1) * kPrefillRows) - 1;
-    const int lim = min(q.len, max(0, q.len - q.n + last / group + 1));
-    return (lim + kPrefillStep - 1) / kPrefillStep;
-}
 
 constexpr int kCached = 2048;        // tiles whose steps stay in shared memory between the phases
 
@@ -60,9 +45,9 @@ struct Shared {
     int steps[kCached], seq[kCached];
     int wmax[kWarps];
     unsigned long long wsum[kWarps];
-    long long items[kCand], parts[kCand];                    // per candidate: all items; parts of split tiles
+    pf::Choice choice;
     int bucket[kBuckets], at[kBuckets];
-    int part_len, max_item, next_slot, next_merge;
+    int next_slot, next_merge;
 };
 
 // (The kernel runs every instruction about once, so it is bound by fetching them: what is used twice is a function,
@@ -103,8 +88,6 @@ __device__ __noinline__ int tile_of(const PrefillArgs& a, const Shared& sh, int 
     *k = find_seq(sh, i);
     return tile_steps(Seq{sh.start[*k], sh.n[*k], sh.len[*k]}, a.group, i - sh.first[*k]);
 }
-
-__device__ __noinline__ int parts_of(int steps, int P) { return max(1, (steps + P - 1) / P); }
 
 __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __grid_constant__ PrefillArgs a) {
     __shared__ Shared sh;
@@ -150,59 +133,10 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __grid_con
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
 
-    // ---- the part length: a warp a candidate counts every tile's parts at it.  (The host rules splitting out
-    // by the same count of tiles; a batch that the plan would have to reload is not split either.)
-    // Nor is one whose longest tile is well below what every CTA has to do anyway: cutting it shortens nothing.
-    const long long nh = a.num_kv_heads;
-    const float each = (static_cast<float>(steps) + kItemCost * static_cast<float>(tiles_all)) * nh / a.slots;
-    const bool may_split = a.may_split && cached && maxs > kMinPart && tiles_all * nh < 8ll * a.slots &&
-                           maxs + kItemCost > 0.6f * each;
-    int P = max(1, maxs), top = P;                           // the part length, the longest item
-    if (may_split) {
-        if (warp < kCand) {
-            const int Pw = max(kMinPart, (maxs + kParts[warp] - 1) / kParts[warp]);
-            int all = 0, split = 0;
-#pragma unroll 1
-            for (int i = lane; i < tiles_all; i += 32) {
-                const int parts = parts_of(sh.steps[i], Pw);
-                all += parts;
-                split += parts > 1 ? parts : 0;
-            }
-            all = __reduce_add_sync(0xffffffffu, all);
-            split = __reduce_add_sync(0xffffffffu, split);
-            if (lane == 0) {
-                sh.items[warp] = all;
-                sh.parts[warp] = split;
-            }
-        }
-        __syncthreads();
-        if (warp == 0) {
-            unsigned long long best = ~0ull;
-            if (lane < kCand) {
-                const int P = max(kMinPart, (maxs + kParts[lane] - 1) / kParts[lane]);
-                const long long items = sh.items[lane], parts = sh.parts[lane];
-                const bool fits = parts <= a.part_cap && tiles_all + parts <= a.capacity &&
-                                  (maxs + P - 1) / P <= kPrefillMaxParts;
-                const float top = static_cast<float>(min(P, maxs) + kItemCost + (parts > 0 ? kSplitCost : 0));
-                const float load = (static_cast<float>(steps) + kItemCost * static_cast<float>(items) +
-                                    kSplitCost * static_cast<float>(parts)) * nh / a.slots;
-                const float est = items * nh <= a.slots ? top : fmaxf(top, load + 0.5f * top);
-                // (positive floats order as their bits; the candidate's index breaks ties towards fewer parts)
-                if (fits) best = static_cast<unsigned long long>(__float_as_uint(est)) << 32 | lane;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-            if (lane == 0) {
-                const int k = best == ~0ull ? 1 : kParts[best & 31];
-                const int P = k == 1 ? max(1, maxs) : max(kMinPart, (maxs + k - 1) / k);
-                sh.part_len = P;
-                sh.max_item = min(P, max(1, maxs));
-            }
-        }
-        __syncthreads();
-        P = sh.part_len;
-        top = sh.max_item;
-    }
+    // ---- the part length (a batch that the plan would have to reload is not split)
+    const int P = cached ? pf::choose_part<kWarps>(a, sh.choice, sh.steps, static_cast<int>(tiles_all), maxs, static_cast<float>(steps))
+                         : max(1, maxs);
+    const int top = min(P, max(1, maxs));                    // the longest item
 
     // ---- items by length: count, offsets, write
 #pragma unroll 1
@@ -277,13 +211,22 @@ PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int 
 
 bool prefill_may_split(int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots) {
     const int64_t tiles = num_tokens * (num_heads / num_kv_heads) / kPrefillRows;       // at least
-    return max_seq_len > kMinPart * kPrefillStep && tiles * num_kv_heads < 8ll * slots;
+    return max_seq_len > kPrefillMinPart * kPrefillStep && tiles * num_kv_heads < 8ll * slots;
 }
 
 bool prefill_direct(int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots) {
     const int64_t rows = num_tokens * (num_heads / num_kv_heads);
     return num_seqs <= 128 && (rows / kPrefillRows + std::min<int64_t>(num_seqs, rows)) * num_kv_heads <= slots &&
            !prefill_may_split(num_tokens, max_seq_len, num_heads, num_kv_heads, slots);
+}
+
+bool prefill_local(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads, int slots,
+                   const PrefillWorkspace& w) {
+    const int64_t rows = num_tokens * (num_heads / num_kv_heads);
+    const int64_t tiles = rows / kPrefillRows + std::min<int64_t>(num_seqs, rows);        // at most
+    // (an item a lane of the plan warp, 32 rounds)
+    return num_seqs <= kPrefillLocal && tiles <= kPrefillLocal && tiles + w.part_cap <= kPrefillLocalItems &&
+           (tiles + w.part_cap) * num_kv_heads <= 32ll * slots;
 }
 
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
