@@ -406,7 +406,7 @@ __device__ __forceinline__ int local_plan(const PrefillArgs& a, LocalPlan& lp) {
         const int key = lp.key[i];
         int rank = 0;
         const int4* all = reinterpret_cast<const int4*>(lp.key);
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; 4 * j < items; ++j) {
             const int4 o = all[j];
             rank += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
@@ -1303,7 +1303,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 //     m = max_p m_p,  out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
 // summed in part order.  A kernel of its own, since the merge of a 256-row tile is a megabyte of reads:
 // by the last CTA to finish it took 70 us of a 177 us call (33 tokens x 64 heads over 65549 positions).
-constexpr int kMergeThreads = 128, kMergeRows = 32;
+constexpr int kMergeThreads = 256, kMergeRows = 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const PrefillArgs a) {
     constexpr int kQuads = D / 4 / (kMergeThreads / 32);      // 4-column pieces a thread merges
@@ -1349,14 +1349,16 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
         float4 acc[kQuads];
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
+#pragma unroll 4
         for (int p = 0; p < nparts; ++p) {
             const float2 x = has ? __ldcg(ml + static_cast<int64_t>(p) * a.part_rows) : make_float2(-INFINITY, 0.0f);
-            if (x.x == -INFINITY && x.y == 0.0f) continue;    // (a part the row sees nothing of: its O was not written)
-            const float w = fast_exp2(x.x - m);
+            // (a part the row sees nothing of: its O was not written)
+            const bool none = x.x == -INFINITY && x.y == 0.0f;
+            const float w = none ? 0.0f : fast_exp2(x.x - m);
 #pragma unroll
             for (int k = 0; k < kQuads; ++k) {
-                const float4 v = __ldcg(po + (static_cast<int64_t>(p) * (D / 4) + warp + k * (kMergeThreads / 32)) * a.part_rows);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (!none) v = __ldcg(po + (static_cast<int64_t>(p) * (D / 4) + warp + k * (kMergeThreads / 32)) * a.part_rows);
                 acc[k].x += w * v.x;
                 acc[k].y += w * v.y;
                 acc[k].z += w * v.z;
