@@ -1386,17 +1386,20 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtenso
     using G = PfGeo<D, KV8>;
     static_assert(G::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
     auto kern = prefill_kernel<T, D, KV8, OT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kBytes));
+    // once a device: the shared memory, and that the warpgroups' register split fits what a block is launched with
+    // (or it would wait for ever)
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    // the warpgroups' register split must fit what a block is launched with, or it would wait for ever
-    static std::atomic<int> regs{0};
-    if (regs.load(std::memory_order_relaxed) == 0) {
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
         cudaFuncAttributes fa{};
         if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-        regs.store(fa.numRegs, std::memory_order_relaxed);
+        if (fa.numRegs * G::kThreads < 256 * G::kRegsSoftmax + 256 * G::kRegsOther) return cudaErrorLaunchOutOfResources;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kBytes));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
-    if (regs.load(std::memory_order_relaxed) * G::kThreads < 256 * G::kRegsSoftmax + 256 * G::kRegsOther)
-        return cudaErrorLaunchOutOfResources;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(
         std::min<int64_t>(a.slots, static_cast<int64_t>(a.direct ? a.capacity - a.part_cap : a.capacity) * a.num_kv_heads)));
