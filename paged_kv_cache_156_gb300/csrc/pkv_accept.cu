@@ -43,7 +43,7 @@ constexpr int kCluster = 8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;                           // groups of 128 weights whose loads are in flight together
-constexpr int kMaxBatches = (PKV_ACCEPT_MAX_VOCAB + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128);
+constexpr int kMaxBatches = (PKV_ACCEPT_MAX_VOCAB + 3 + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128);
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T x) {
@@ -52,38 +52,42 @@ __device__ __forceinline__ float to_f32(T x) {
     else return __bfloat162float(x);
 }
 
-// Four consecutive probabilities from element i of a row (0 past its end), `off` elements past a vector's
-// boundary (the row's base and so every fourth element are): the two aligned vectors that hold them, shifted
-// together, where both lie inside the row; element by element at its ends.
+// Four probabilities, as one vector load brings them.
 template <typename T>
-__device__ __forceinline__ void load4(const T* row, int i, int vocab, int off, float (&x)[4]) {
-    const int at = i - off;
-    if (off == 0 ? i + 4 <= vocab : at >= 0 && at + 8 <= vocab) {
-        if constexpr (std::is_same<T, float>::value) {
-            const float4 v = __ldcs(reinterpret_cast<const float4*>(row + at));
-            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-            if (off != 0) {
-                const float4 n = __ldcs(reinterpret_cast<const float4*>(row + at) + 1);
-                x[0] = off == 1 ? v.y : off == 2 ? v.z : v.w;
-                x[1] = off == 1 ? v.z : off == 2 ? v.w : n.x;
-                x[2] = off == 1 ? v.w : off == 2 ? n.x : n.y;
-                x[3] = off == 1 ? n.x : off == 2 ? n.y : n.z;
-            }
-        } else {
-            uint2 v = __ldcs(reinterpret_cast<const uint2*>(row + at));
-            if (off != 0) {
-                const uint2 n = __ldcs(reinterpret_cast<const uint2*>(row + at) + 1);
-                const uint32_t a = off >= 2 ? v.y : v.x, b = off >= 2 ? n.x : v.y, c = off >= 2 ? n.y : n.x;
-                v = (off & 1) ? make_uint2(__funnelshift_r(a, b, 16), __funnelshift_r(b, c, 16)) : make_uint2(a, b);
-            }
-            const float2 lo = Mma<T>::unpack(v.x), hi = Mma<T>::unpack(v.y);
-            x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = i + e < vocab ? to_f32(row[i + e]) : 0.0f;
+struct Four {
+    static constexpr int kWords = 2;
+    static __device__ __forceinline__ void unpack(const uint32_t (&v)[2], float (&x)[4]) {
+        const float2 lo = Mma<T>::unpack(v[0]), hi = Mma<T>::unpack(v[1]);
+        x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
     }
-}
+    // elements d to d + 3 of v and the vector after it, n (d: 1 to 3)
+    static __device__ __forceinline__ void shift(uint32_t (&v)[2], const uint32_t (&n)[2], int d) {
+        const uint32_t a = d >= 2 ? v[1] : v[0], b = d >= 2 ? n[0] : v[1], c = d >= 2 ? n[1] : n[0];
+        v[0] = (d & 1) ? __funnelshift_r(a, b, 16) : a;
+        v[1] = (d & 1) ? __funnelshift_r(b, c, 16) : b;
+    }
+    static __device__ __forceinline__ void load(uint32_t (&v)[2], const T* p) {
+        const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p));
+        v[0] = r.x; v[1] = r.y;
+    }
+};
+template <>
+struct Four<float> {
+    static constexpr int kWords = 4;
+    static __device__ __forceinline__ void unpack(const uint32_t (&v)[4], float (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(v[e]);
+    }
+    static __device__ __forceinline__ void shift(uint32_t (&v)[4], const uint32_t (&n)[4], int d) {
+        const uint32_t x[7] = {v[0], v[1], v[2], v[3], n[0], n[1], n[2]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = d == 1 ? x[e + 1] : d == 2 ? x[e + 2] : x[e + 3];
+    }
+    static __device__ __forceinline__ void load(uint32_t (&v)[4], const float* p) {
+        const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
+        v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+    }
+};
 
 // Whole units of a weight in [0, 1] (clipped as it is formed, NaN to 0), floor(w 2^44), as two 22-bit halves added
 // to hi and lo: w + 2 rounded towards zero holds floor(w 2^22) in its significand's last bits, what is left of w
@@ -169,29 +173,67 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
     const T* qrow = refused && draft ? draft + static_cast<int64_t>(kept) * V : nullptr;
     const int64_t out_x = refused && !draft ? __ldcg(drafts + kept) : -1;      // the weight that leaves the row
     const float u = __ldcg(uniform + K);
+    // The row is cut at the target row's boundaries of four: its first vector may hold elements before it.  The
+    // draft's row may stand otherwise there (by qoff): a lane then joins its vector with the next lane's.
     auto offset = [](const T* row) {                // elements past a boundary of four
         return static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 3);
     };
-    const int poff = offset(prow), qoff = qrow ? offset(qrow) : 0;
+    const int poff = offset(prow), qoff = qrow ? (offset(qrow) - poff) & 3 : 0;
     // a warp's piece of the row: whole batches
-    const int batches = static_cast<int>((V + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128));
-    const int first = (rank * kWarps + warp) * batches * kBatch * 128 + 4 * lane;
+    const int batches = (V + poff + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128);
+    const int first = (rank * kWarps + warp) * batches * kBatch * 128 - poff;
 
     float w[kBatch][4];
     auto load = [&](int batch, bool residual) {     // this lane's weights of a batch
-        const int i0 = first + batch * kBatch * 128;
-        float q[kBatch][4];
+        constexpr int W = Four<T>::kWords;
+        const int i0 = first + batch * kBatch * 128;             // (warp-uniform, as the branches below)
+        const int i = i0 + 4 * lane;
+        const bool sub = residual && qrow != nullptr;
+        if (i0 >= qoff && i0 + kBatch * 128 + (qoff ? 4 : 0) <= V) {
+            // every load before the first use: a branch between them would wait for each in turn
+            uint32_t p[kBatch][W], q[kBatch][W];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            load4(prow, i0 + 128 * k, V, poff, w[k]);
-            if (residual && qrow) load4(qrow, i0 + 128 * k, V, qoff, q[k]);
+            for (int k = 0; k < kBatch; ++k) Four<T>::load(p[k], prow + i + 128 * k);
+            if (sub) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) Four<T>::load(q[k], qrow + i + 128 * k - qoff);
+                if (qoff != 0) {
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        uint32_t last[W] = {}, next[W];
+                        if (lane == 31) Four<T>::load(last, qrow + i + 128 * k - qoff + 4);
+#pragma unroll
+                        for (int e = 0; e < W; ++e) {
+                            next[e] = __shfl_down_sync(0xffffffffu, q[k][e], 1);
+                            if (lane == 31) next[e] = last[e];
+                        }
+                        Four<T>::shift(q[k], next, qoff);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                float y[4];
+                Four<T>::unpack(p[k], w[k]);
+                if (sub) Four<T>::unpack(q[k], y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(sub ? w[k][e] - y[e] : w[k][e]);
+            }
+        } else {                                    // a batch at the row's ends
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = i + 128 * k + e;
+                    w[k][e] = 0.0f;
+                    if (at >= 0 && at < V) {
+                        const float x = to_f32(prow[at]);
+                        w[k][e] = __saturatef(sub ? x - to_f32(qrow[at]) : x);
+                    }
+                }
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(residual && qrow ? w[k][e] - q[k][e] : w[k][e]);
         if (residual && out_x >= 0) {
-            const int gone = static_cast<int>(min(out_x, static_cast<int64_t>(V))) - i0;
+            const int gone = static_cast<int>(min(out_x, static_cast<int64_t>(V))) - i;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
 #pragma unroll
@@ -206,7 +248,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
 #pragma unroll 1
         for (int batch = 0; batch < batches; ++batch) {
             uint32_t hi = 0, lo = 0;
-            if (first - 4 * lane + batch * kBatch * 128 < V) {
+            if (first + batch * kBatch * 128 < V) {
                 load(batch, residual);
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k)
@@ -241,34 +283,56 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
         const unsigned long long mark = min(__double2ull_rz(z), total - 1);
         for (int v = 0; v < warp; ++v) before += warp_total[v];
         if (mark < before || mark >= before + mine) break;       // another warp's
+        // the batch that holds the mark: four batches' sums at a time, side by side
         int batch = 0;
-        for (; batch + 1 < batches; ++batch) {
-            const unsigned long long sum = warp_sum(batch_sum[batch][t]);
-            if (mark < before + sum) break;
-            before += sum;
-        }
-        load(batch, residual);
+        for (int b0 = 0; b0 < batches; b0 += 4) {
+            unsigned long long sum[4];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            unsigned long long c[4];
-            uint32_t hi = 0, lo = 0;
+            for (int e = 0; e < 4; ++e) sum[e] = b0 + e < batches ? batch_sum[b0 + e][t] : 0ull;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = warp_sum(sum[e]);
+            bool here = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                add_units(w[k][e], hi, lo);
-                c[e] = join(hi, lo);
+                if (here) continue;
+                batch = b0 + e;
+                here = mark < before + sum[e];
+                if (!here) before += sum[e];
             }
-            unsigned long long inc = c[3];
+            if (here) break;
+        }
+        load(batch, residual);
+        unsigned long long own[kBatch], inc[kBatch];              // a lane's four weights, and up to and with them
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
+        for (int k = 0; k < kBatch; ++k) {
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) add_units(w[k][e], hi, lo);
+            own[k] = inc[k] = join(hi, lo);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, inc[k], o);
+                if (lane >= o) inc[k] += y;
             }
-            const unsigned long long at = before + inc - c[3];   // before this lane's four
-            if (mark >= at && mark < at + c[3]) {
-                const int e = mark < at + c[0] ? 0 : mark < at + c[1] ? 1 : mark < at + c[2] ? 2 : 3;
-                a.tokens[static_cast<int64_t>(b) * (K + 1) + kept] = first + (batch * kBatch + k) * 128 + e;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            unsigned long long at = before + inc[k] - own[k];     // before this lane's four
+            if (mark >= at && mark < at + own[k]) {
+                int e = 0;
+#pragma unroll
+                for (int f = 0; f < 3; ++f) {
+                    uint32_t hi = 0, lo = 0;
+                    add_units(w[k][f], hi, lo);
+                    at += join(hi, lo);
+                    e += mark >= at;
+                }
+                a.tokens[static_cast<int64_t>(b) * (K + 1) + kept] = first + (batch * kBatch + k) * 128 + 4 * lane + e;
             }
-            before += __shfl_sync(0xffffffffu, inc, 31);
+            before += __shfl_sync(0xffffffffu, inc[k], 31);
         }
         break;
     }
