@@ -1306,33 +1306,38 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
     }
 }
 
-// The split tiles' parts merged: 32 rows a CTA, a row a lane, its columns over the warps.
+// The split tiles' parts merged: 32 rows by 64 columns a CTA, a row a lane, its columns over the warps.
 //     m = max_p m_p,  out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
 // summed in part order.  A kernel of its own, since the merge of a 256-row tile is a megabyte of reads:
 // by the last CTA to finish it took 70 us of a 177 us call (33 tokens x 64 heads over 65549 positions).
-constexpr int kMergeThreads = 256, kMergeRows = 32;
+// Bound by latency: the next call waits for the last of these CTAs.  So the parts' weights are found first, a part a
+// warp, and kept in shared memory; then every load of the partial outputs is independent of the others, 16 in flight
+// a lane.
+constexpr int kMergeThreads = 256, kMergeRows = 32, kMergeCols = 64;
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const PrefillArgs a) {
-    constexpr int kQuads = D / 4 / (kMergeThreads / 32);      // 4-column pieces a thread merges
-    __shared__ uint2 tile[kMergeRows][D / 4 + 1];
+    constexpr int kWarps = kMergeThreads / 32;
+    constexpr int kQuads = kMergeCols / 4 / kWarps;           // 4-column pieces a thread merges
+    __shared__ uint2 tile[kMergeRows][kMergeCols / 4 + 1];
     __shared__ int rows_at[kMergeRows];
+    __shared__ float2 weight[kPrefillMaxParts][kMergeRows];   // (reference, sum), then (2^(m_p - m), times the sum); below 0: nothing seen
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     launch_dependents();
-    const int groups = a.part_rows / kMergeRows;
-    const long long units = static_cast<long long>(min(__ldcg(a.header + 1), a.part_cap / 2)) * a.num_kv_heads * groups;
+    const int groups = a.part_rows / kMergeRows, pieces = groups * (D / kMergeCols);
+    const long long units = static_cast<long long>(min(__ldcg(a.header + 1), a.part_cap / 2)) * a.num_kv_heads * pieces;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const int g = static_cast<int>(u % groups);
-        const int kvh = static_cast<int>((u / groups) % a.num_kv_heads);
-        const int4 e = __ldcg(a.merges + u / groups / a.num_kv_heads);
+        const int piece = static_cast<int>(u % pieces), g = piece / (D / kMergeCols), cols = piece % (D / kMergeCols);
+        const int kvh = static_cast<int>((u / pieces) % a.num_kv_heads);
+        const int4 e = __ldcg(a.merges + u / pieces / a.num_kv_heads);
         const int nparts = e.x & 255, base = e.x >> 16;
         Item it;
         it.tile = e.y;
         it.qs = e.z;
         it.n = e.w;
         it.kvh = kvh;
-        if (nparts < 1 || base < 0 || base + nparts > a.part_cap || it.tile < 0 || it.qs < 0 || it.n <= 0 ||
-            it.qs + static_cast<long long>(it.n) > a.num_tokens) {
+        if (nparts < 1 || nparts > kPrefillMaxParts || base < 0 || base + nparts > a.part_cap || it.tile < 0 || it.qs < 0 ||
+            it.n <= 0 || it.qs + static_cast<long long>(it.n) > a.num_tokens) {
             if (threadIdx.x == 0) raise_error(a.err, kErrBounds);
             continue;
         }
@@ -1342,30 +1347,37 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
         const int row = g * kMergeRows + lane;
         const int64_t slot = static_cast<int64_t>(kvh) * a.part_cap + base;
         const float2* ml = a.part_ml + slot * a.part_rows + row;
-        const float4* po = a.part_o + slot * (D / 4) * a.part_rows + row;
-        float m = -INFINITY, den = 0.0f;
-        if (has) {
+        const float4* po = a.part_o + (slot * (D / 4) + cols * (kMergeCols / 4) + warp) * a.part_rows + row;
+#pragma unroll 4
+        for (int p = warp; p < nparts; p += kWarps)
+            weight[p][lane] = has ? __ldcg(ml + static_cast<int64_t>(p) * a.part_rows) : make_float2(-INFINITY, 0.0f);
+        if (warp == 0) rows_at[lane] = has ? static_cast<int>(qo_row(a, it, row)) : -1;
+        __syncthreads();
+        float m = -INFINITY;
 #pragma unroll 8
-            for (int p = 0; p < nparts; ++p) m = fmaxf(m, __ldcg(ml + static_cast<int64_t>(p) * a.part_rows).x);
-#pragma unroll 8
-            for (int p = 0; p < nparts; ++p) {
-                const float2 x = __ldcg(ml + static_cast<int64_t>(p) * a.part_rows);
-                den += x.x == -INFINITY && x.y == 0.0f ? 0.0f : fast_exp2(x.x - m) * x.y;
-            }
+        for (int p = 0; p < nparts; ++p) m = fmaxf(m, weight[p][lane].x);
+        __syncthreads();
+        for (int p = warp; p < nparts; p += kWarps) {
+            const float2 x = weight[p][lane];
+            // (a part the row sees nothing of: its O was not written)
+            const float w = x.x == -INFINITY && x.y == 0.0f ? -1.0f : fast_exp2(x.x - m);
+            weight[p][lane] = make_float2(w, w < 0.0f ? 0.0f : w * x.y);
         }
+        __syncthreads();
+        float den = 0.0f;
         float4 acc[kQuads];
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
         for (int p = 0; p < nparts; ++p) {
-            const float2 x = has ? __ldcg(ml + static_cast<int64_t>(p) * a.part_rows) : make_float2(-INFINITY, 0.0f);
-            // (a part the row sees nothing of: its O was not written)
-            const bool none = x.x == -INFINITY && x.y == 0.0f;
-            const float w = none ? 0.0f : fast_exp2(x.x - m);
+            const float2 x = weight[p][lane];
+            const bool none = x.x < 0.0f;
+            den += x.y;
 #pragma unroll
             for (int k = 0; k < kQuads; ++k) {
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (!none) v = __ldcg(po + (static_cast<int64_t>(p) * (D / 4) + warp + k * (kMergeThreads / 32)) * a.part_rows);
+                if (!none) v = __ldcg(po + (static_cast<int64_t>(p) * (D / 4) + k * kWarps) * a.part_rows);
+                const float w = none ? 0.0f : x.x;
                 acc[k].x += w * v.x;
                 acc[k].y += w * v.y;
                 acc[k].z += w * v.z;
@@ -1375,13 +1387,13 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
         const float inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
 #pragma unroll
         for (int k = 0; k < kQuads; ++k)
-            tile[lane][warp + k * (kMergeThreads / 32)] =
+            tile[lane][warp + k * kWarps] =
                 make_uint2(Mma<T>::pack(acc[k].x * inv, acc[k].y * inv), Mma<T>::pack(acc[k].z * inv, acc[k].w * inv));
-        if (warp == 0) rows_at[lane] = has ? static_cast<int>(qo_row(a, it, row)) : -1;
         __syncthreads();
-        for (int i = threadIdx.x; i < kMergeRows * (D / 4); i += kMergeThreads) {
-            const int r = i / (D / 4), c = i % (D / 4);
-            if (rows_at[r] >= 0) reinterpret_cast<uint2*>(static_cast<T*>(a.out) + static_cast<int64_t>(rows_at[r]) * D)[c] = tile[r][c];
+        for (int i = threadIdx.x; i < kMergeRows * (kMergeCols / 4); i += kMergeThreads) {
+            const int r = i / (kMergeCols / 4), c = i % (kMergeCols / 4);
+            if (rows_at[r] >= 0)
+                reinterpret_cast<uint2*>(static_cast<T*>(a.out) + static_cast<int64_t>(rows_at[r]) * D + cols * kMergeCols)[c] = tile[r][c];
         }
         __syncthreads();
     }
