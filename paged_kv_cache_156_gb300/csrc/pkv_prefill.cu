@@ -392,7 +392,7 @@ __device__ __forceinline__ int local_plan(const PrefillArgs& a, LocalPlan& lp) {
     const int len = parts > 0 ? (st + parts - 1) / parts : 0;
     for (int p = 0; p < parts; ++p) {
         const int s0 = min(st, p * len);
-        lp.key[item0 + p] = (min(st, s0 + len) - s0) << 10 | (kPrefillLocalItems - 1 - item0 - p);
+        lp.key[item0 + p] = min(min(st, s0 + len) - s0, (1 << 21) - 1) << 10 | (kPrefillLocalItems - 1 - item0 - p);
         lp.ref[item0 + p] = t << 8 | p;
     }
     if (report) {

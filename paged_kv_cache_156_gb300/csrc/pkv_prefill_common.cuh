@@ -50,17 +50,17 @@ __device__ __forceinline__ int warp_scan(int v) {            // inclusive
 
 __device__ __forceinline__ int parts_of(int steps, int P) { return max(1, (steps + P - 1) / P); }
 
-constexpr int kCand = 24;
-// Parts that candidate c cuts the longest tile into: 1 .. 10, then ever wider apart up to kPrefillMaxParts.
+constexpr int kCand = 32;            // (a lane each)
+// Parts that candidate c cuts the longest tile into: 1 .. 20, then ever wider apart up to kPrefillMaxParts.
 __device__ __forceinline__ int cand_parts(int c) {
-    return c < 10 ? c + 1 : c < kCand - 1 ? 10 + ((c - 9) * (c - 9) * 29 + 20) / 40 : kPrefillMaxParts;
+    return c < 20 ? c + 1 : 20 + ((c - 19) * (c - 19) * (kPrefillMaxParts - 20) + 72) / 144;
 }
+static_assert((kCand - 20) * (kCand - 20) == 144, "the last candidate: kPrefillMaxParts");
 constexpr int kItemCost = 2;         // steps' worth of an item's query load and epilogue
 constexpr int kSplitCost = 3;        // and of a part's partial output and its share of the merge
 
 struct Choice {
     int items[kCand], parts[kCand];  // per candidate: all items; parts of split tiles
-    int part_len;
 };
 
 // The part length P of a batch whose tiles' steps are in `steps`, by a block of WARPS warps: the longest tile's
@@ -100,7 +100,7 @@ __device__ __forceinline__ int choose_part(const PrefillArgs& a, Choice& ch, con
     // (every warp chooses for itself)
     unsigned best = 0xffffffffu;
     int P = max(1, maxs);
-    if (lane < kCand) {
+    {
         const int k = cand_parts(lane);
         if (lane > 0) P = max(kPrefillMinPart, (maxs + k - 1) / k);
         const int items = ch.items[lane], parts = ch.parts[lane];
@@ -111,7 +111,7 @@ __device__ __forceinline__ int choose_part(const PrefillArgs& a, Choice& ch, con
         if (parts <= a.part_cap && tiles + parts <= a.capacity && (maxs + P - 1) / P <= kPrefillMaxParts) best = __float_as_uint(est);
     }
     const unsigned least = __reduce_min_sync(0xffffffffu, best);
-    const unsigned m = __ballot_sync(0xffffffffu, best == least && lane < kCand);
+    const unsigned m = __ballot_sync(0xffffffffu, best == least);
     const int win = least == 0xffffffffu ? 0 : __ffs(m) - 1;              // ties: fewer parts
     return least == 0xffffffffu ? max(1, maxs) : __shfl_sync(0xffffffffu, P, win);
 }
