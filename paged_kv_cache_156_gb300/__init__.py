@@ -28,6 +28,7 @@ _POOL_DT = {torch.float16: 0, torch.bfloat16: 1, torch.uint8: 2}   # uint8 pools
 PLAN_MAX_SEQS = 1024        # PKV_PLAN_MAX_SEQS: batches up to this size run through the plan kernel
 PLANNED = 1                 # PKV_PLANNED: run over the plan an earlier call wrote
 _PROB_DT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 3}   # PKV_F32: probabilities only
+_HALF_DTS, _POOL_DTS, _PROB_DTS = tuple(_DT), tuple(_POOL_DT), tuple(_PROB_DT)
 ACCEPT_MAX_VOCAB = 524288   # PKV_ACCEPT_MAX_VOCAB
 INPUTS_READY = 2            # PKV_INPUTS_READY: nothing pending writes the pools, tables, lengths or plan
 
@@ -152,6 +153,14 @@ def _check(status: int):
         raise PkvError(status, load().pkv_last_error().decode(errors="replace"))
 
 
+_Tensor = torch.Tensor
+_NESTED = (list, tuple, torch.Tensor)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _cuda_devices(values):
     """The CUDA devices of the tensors among ``values`` (tensors, or lists / tuples of them)."""
     devs = set()
@@ -170,17 +179,18 @@ def _one_device(fn):
     def call(*args, **kwargs):
         # the usual call: plain tensors of the current device
         dev = None
-        for v in (*args, *kwargs.values()):
-            if type(v) is torch.Tensor:
+        for v in (*args, *kwargs.values()) if kwargs else args:
+            if type(v) is _Tensor:
                 d = v.get_device()
-                if d >= 0 and d != dev:
+                if d != dev and d >= 0:
                     if dev is not None:
                         break
                     dev = d
-            elif isinstance(v, (list, tuple, torch.Tensor)):
+            elif v is not None and isinstance(v, _NESTED):
                 break
         else:
-            if dev is None or dev == torch.cuda.current_device():
+            # (a CUDA tensor exists: the runtime is up, and the raw call answers in a tenth of the public one's time)
+            if dev is None or dev == _current_device():
                 return fn(*args, **kwargs)
         devs = _cuda_devices(list(args) + list(kwargs.values()))
         if len(devs) > 1:
@@ -198,11 +208,11 @@ def _stream(t: torch.Tensor):
 
 
 def _cuda(name, t, dtype=None, ndim=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype is not dtype and (type(dtype) is not tuple or t.dtype not in dtype):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
@@ -500,38 +510,42 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
     see ``alloc_prefill_workspace`` (allocated here when omitted); ``planned``: run over the list ``prefill_plan``
     put there for this batch.  ``max_seq_len`` is read from the device if omitted, which synchronises.  uint8 pools hold
     E4M3 codes and take k_scale / v_scale (float32 [Hkv]) as paged_attention_decode_fp8 does."""
-    kv8 = key_cache.dtype == torch.uint8
-    NB, bs, Hkv, d = _pool("key_cache", key_cache, tuple(_POOL_DT))
-    if value_cache.shape != key_cache.shape or value_cache.dtype != key_cache.dtype:
+    dt = key_cache.dtype
+    kv8 = dt is torch.uint8
+    if not kv8 and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale / v_scale belong to E4M3 (uint8) pools")
+    kc = _cuda("key_cache", key_cache, _POOL_DTS, 4)
+    NB, bs, Hkv, d = key_cache.shape
+    if value_cache.shape != key_cache.shape or value_cache.dtype is not dt:
         raise ValueError("value_cache must match key_cache")
+    qp = _cuda("q", q, _HALF_DTS if kv8 else dt)
     if q.dim() != 3:
         raise ValueError("q must be [num_tokens, num_heads, head_dim]")
     T, Hq, dq = q.shape
-    if dq != d or tuple(out.shape) != (T, Hq, d):
+    if dq != d or out.shape != q.shape:
         raise ValueError("q and out must be [num_tokens, num_heads, head_dim]")
+    op, vc, bt = _cuda("out", out, q.dtype), _cuda("value_cache", value_cache), _cuda("block_tables", block_tables, torch.int32, 2)
+    sl, qs = _cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("query_starts", query_starts, torch.int32, 1)
     B = seq_lens.shape[0]
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    qdt = (torch.float16, torch.bfloat16) if kv8 else key_cache.dtype
-    ptrs = [_cuda("out", out, qdt), _cuda("q", q, out.dtype), _cuda("key_cache", key_cache),
-            _cuda("value_cache", value_cache), _cuda("block_tables", block_tables, torch.int32, 2)]
-    lens = [_cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("query_starts", query_starts, torch.int32, 1)]
-    if block_tables.shape[0] != B or query_starts.shape[0] != B + 1:
+    NT, W = block_tables.shape
+    if NT != B or query_starts.shape[0] != B + 1:
         raise ValueError("block_tables must have num_seqs rows and query_starts num_seqs + 1 entries")
-    if planned and workspace is None:
-        raise ValueError("planned=True needs the workspace that prefill_plan wrote")
+    if workspace is None:
+        if planned:
+            raise ValueError("planned=True needs the workspace that prefill_plan wrote")
+        workspace = alloc_prefill_workspace(B, T, Hq, Hkv, d, q.device)
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
-    if workspace is None:
-        workspace = alloc_prefill_workspace(B, T, Hq, Hkv, d, q.device)
-    scales = [_scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv)] if kv8 else []
-    args = [*ptrs, block_tables.shape[1], *lens, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB, float(scale), _DT[q.dtype],
-            *scales, _cuda("workspace", workspace), workspace.numel() * workspace.element_size(),
-            PLANNED if planned else 0, _stream(q)]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    wp, flags = _cuda("workspace", workspace), PLANNED if planned else 0
     if kv8:
-        _check(load().pkv_paged_attention_prefill_fp8(*args))
+        ks, vs = _scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv)
+        _check(load().pkv_paged_attention_prefill_fp8(op, qp, kc, vc, bt, W, sl, qs, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB,
+                                                      scale, _DT[q.dtype], ks, vs, wp, workspace.nbytes, flags, _stream(q)))
     else:
-        _check(load().pkv_paged_attention_prefill(*args))
+        _check(load().pkv_paged_attention_prefill(op, qp, kc, vc, bt, W, sl, qs, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB,
+                                                  scale, _DT[dt], wp, workspace.nbytes, flags, _stream(q)))
 
 
 @_one_device
@@ -540,26 +554,31 @@ def paged_kv_gather(k_out, v_out, key_cache, value_cache, block_tables, seq_lens
     """Rows row_starts[s] + t of k_out, v_out ([R, Hkv, d]) = position t < seq_lens[s] of sequence s (row_starts
     int32 [B + 1]; other rows are left as they are).  uint8 pools hold E4M3 codes and take k_scale / v_scale
     (float32 [Hkv]): the rows are then code value * scale, rounded to the outputs' fp16 / bf16."""
-    kv8 = key_cache.dtype == torch.uint8
-    NB, bs, Hkv, d = _pool("key_cache", key_cache, tuple(_POOL_DT))
-    if value_cache.shape != key_cache.shape or value_cache.dtype != key_cache.dtype:
+    dt = key_cache.dtype
+    kv8 = dt is torch.uint8
+    if not kv8 and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale / v_scale belong to E4M3 (uint8) pools")
+    kc = _cuda("key_cache", key_cache, _POOL_DTS, 4)
+    NB, bs, Hkv, d = key_cache.shape
+    if value_cache.shape != key_cache.shape or value_cache.dtype is not dt:
         raise ValueError("value_cache must match key_cache")
-    odt = (torch.float16, torch.bfloat16) if kv8 else key_cache.dtype
-    ptrs = [_cuda("k_out", k_out, odt, 3), _cuda("v_out", v_out, k_out.dtype, 3), _cuda("key_cache", key_cache),
-            _cuda("value_cache", value_cache), _cuda("block_tables", block_tables, torch.int32, 2)]
-    R = k_out.shape[0]
-    if tuple(k_out.shape) != (R, Hkv, d) or tuple(v_out.shape) != (R, Hkv, d):
+    ko = _cuda("k_out", k_out, _HALF_DTS if kv8 else dt, 3)
+    vo, vc = _cuda("v_out", v_out, k_out.dtype, 3), _cuda("value_cache", value_cache)
+    bt = _cuda("block_tables", block_tables, torch.int32, 2)
+    R, Hr, dr = k_out.shape
+    if Hr != Hkv or dr != d or v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out must be [rows, num_kv_heads, head_dim]")
-    lens = [_cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("row_starts", row_starts, torch.int32, 1)]
+    sl, rs = _cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("row_starts", row_starts, torch.int32, 1)
     B = seq_lens.shape[0]
-    if block_tables.shape[0] != B or row_starts.shape[0] != B + 1:
+    NT, W = block_tables.shape
+    if NT != B or row_starts.shape[0] != B + 1:
         raise ValueError("block_tables must have num_seqs rows and row_starts num_seqs + 1 entries")
-    args = [*ptrs, block_tables.shape[1], *lens, B, R, NB, bs, Hkv, d, _DT[k_out.dtype]]
     if kv8:
-        _check(load().pkv_paged_kv_gather_fp8(*args, _scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv),
+        _check(load().pkv_paged_kv_gather_fp8(ko, vo, kc, vc, bt, W, sl, rs, B, R, NB, bs, Hkv, d, _DT[k_out.dtype],
+                                              _scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv),
                                               _stream(key_cache)))
     else:
-        _check(load().pkv_paged_kv_gather(*args, _stream(key_cache)))
+        _check(load().pkv_paged_kv_gather(ko, vo, kc, vc, bt, W, sl, rs, B, R, NB, bs, Hkv, d, _DT[dt], _stream(key_cache)))
 
 
 @_one_device
@@ -573,12 +592,12 @@ def speculative_accept(tokens, num_accepted, draft_tokens, target_probs, uniform
     receives the accepted drafts, the drawn token, then -1; num_accepted int32 [B] the count of drafts kept."""
     ptrs = [_cuda("tokens", tokens, torch.int64, 2), _cuda("num_accepted", num_accepted, torch.int32, 1),
             _cuda("draft_tokens", draft_tokens, torch.int64, 2)]
-    target = _cuda("target_probs", target_probs, tuple(_PROB_DT), 3)
+    target = _cuda("target_probs", target_probs, _PROB_DTS, 3)
     B, K = draft_tokens.shape
     V = target_probs.shape[2]
-    if tuple(target_probs.shape) != (B, K + 1, V) or tuple(tokens.shape) != (B, K + 1) or num_accepted.shape[0] != B:
+    if target_probs.shape != (B, K + 1, V) or tokens.shape != (B, K + 1) or num_accepted.shape[0] != B:
         raise ValueError("target_probs must be [B, K + 1, V], tokens [B, K + 1] and num_accepted [B]")
-    if tuple(uniform.shape) != (B, K + 1):
+    if uniform.shape != tokens.shape:
         raise ValueError("uniform must be [B, K + 1]")
     counts = draft = None
     if num_drafts is not None:
@@ -587,7 +606,7 @@ def speculative_accept(tokens, num_accepted, draft_tokens, target_probs, uniform
             raise ValueError("num_drafts must be [B]")
     if draft_probs is not None:
         draft = _cuda("draft_probs", draft_probs, target_probs.dtype, 3)
-        if tuple(draft_probs.shape) != (B, K, V):
+        if draft_probs.shape != (B, K, V):
             raise ValueError("draft_probs must be [B, K, V]")
     _check(load().pkv_speculative_accept(*ptrs, counts, target, draft, _cuda("uniform", uniform, torch.float32, 2), B, K,
                                          V, _PROB_DT[target_probs.dtype], _stream(tokens)))

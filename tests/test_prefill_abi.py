@@ -204,3 +204,14 @@ def test_binding_checks_shapes_and_types(no_device):
                dict(num_drafts=i64(2)), dict(uniform=h(2, 4))):
         with pytest.raises(ValueError):
             accept(**kw)
+
+
+def test_scales_are_refused_over_16_bit_pools(no_device):
+    h = lambda *s: on(torch.zeros(*s, dtype=torch.float16))
+    i32 = lambda *s: on(torch.zeros(*s, dtype=torch.int32))
+    pool, scale = h(4, 16, 2, 64), on(torch.ones(2))
+    for kw in (dict(k_scale=scale), dict(v_scale=scale), dict(k_scale=scale, v_scale=scale)):
+        with pytest.raises(ValueError, match="E4M3"):
+            pkv.paged_attention_prefill(h(3, 4, 64), h(3, 4, 64), pool, pool, i32(1, 2), i32(1), i32(2), max_seq_len=3, **kw)
+        with pytest.raises(ValueError, match="E4M3"):
+            pkv.paged_kv_gather(h(3, 2, 64), h(3, 2, 64), pool, pool, i32(1, 2), i32(1), i32(2), **kw)
