@@ -336,7 +336,7 @@ PKV_API pkv_status pkv_paged_attention_verify(void* out, const void* q, const vo
  * paged cache: prompts, chunks of a prompt over what is already cached, and
  * running sequences that add one token, in one ragged batch.
  *
- * P3 §四 (chunked prefill beside decode); P1 §4.2.2 (a prompt's K/V fill its
+ * P3 (chunked prefill beside decode); P1 §4.2.2 (a prompt's K/V fill its
  * blocks).  Sequence s has n_s = query_starts[s+1] - query_starts[s] new
  * tokens, whose K and V are already in its blocks as its last n_s positions
  * (pkv_paged_kv_append first).  New token i attends over positions

@@ -1070,7 +1070,11 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             const int n = it.steps_of(wg);
             const int seen = min(lim, it.end_of(wg));           // (dummy rows too stop at the tile's end)
             float m_ref = -INFINITY, l = 0.0f;
-            const float sl2 = KV8 ? a.scale_log2 * __ldcg(a.k_scale + it.kvh) : a.scale_log2;
+            float sl2 = a.scale_log2;
+            if (KV8) {
+                sl2 *= __ldcg(a.k_scale + it.kvh);
+                if (sl2 == 0.0f) sl2 = 1e-38f;               // (a masked score, -inf, stays -inf)
+            }
             const uint64_t sl2x2 = pack64(sl2, sl2);
             if constexpr (kConvertQ) {
                 if (n > 0) {                                 // the tile's bf16 queries to f16, in place

@@ -250,3 +250,25 @@ def test_the_tokens_follow_the_target():
         n = int((first == j).sum())
         mean, sd = B * float(p1[j]), math.sqrt(B * float(p1[j]) * (1 - float(p1[j])))
         assert abs(n - mean) < 5 * sd, (j, n, mean)
+
+
+def test_offsets_past_32_bits():
+    """Probabilities past the first 2^31: the last sequence keeps all its drafts but the last, or all of them."""
+    B, K, V = 64, 64, pkv.ACCEPT_MAX_VOCAB
+    target = torch.zeros(B, K + 1, V, dtype=torch.float16, device="cuda")
+    assert target.numel() > 2 ** 31
+    drafts = torch.full((B, K), 5, dtype=torch.int64)
+    drafts[-1] = V - 1 - torch.arange(K)
+    target[-1, torch.arange(K), drafts[-1].cuda()] = 1.0
+    target[-1, K, V - 3] = 1.0
+    uniform = torch.full((B, K + 1), 0.5, device="cuda")
+    for kept in (K, K - 1):
+        if kept < K:
+            target[-1, K - 1, V - K] = 0.0
+            target[-1, K - 1, V - 1] = 0.25
+        tokens = torch.full((B, K + 1), 7, dtype=torch.int64, device="cuda")
+        accepted = torch.full((B,), 7, dtype=torch.int32, device="cuda")
+        pkv.speculative_accept(tokens, accepted, drafts.cuda(), target, uniform)
+        assert int(accepted[-1]) == kept and tokens[-1, :kept].cpu().equal(drafts[-1, :kept])
+        assert int(tokens[-1, kept]) == (V - 3 if kept == K else V - 1)
+        assert (accepted[:-1] == 0).all() and (tokens[:-1] == -1).all()

@@ -135,3 +135,28 @@ def test_quantized_append_gather_and_prefill_in_a_row():
     slack = 2.0 ** -11 + 2 * 2.0 ** -11 * 0.09 * 60
     amax = float(c.v_scale.max() * 448)
     check(out16, ref, bound + slack * amax, "over the rows read back")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_offsets_past_32_bits(e4m3):
+    """Blocks past the pool's first 2^31 elements, rows past the outputs' first 2^31."""
+    b = batch([70, 0, 200], kv_heads=8, dim=128, block=32, dtype="f16", seed=21, e4m3=e4m3)
+    NB = 2 ** 31 // (32 * 8 * 128) + b.kc.shape[0]
+    rows = 2 ** 31 // (8 * 128) + 1 + 300
+    first = rows - 290
+    starts = [0, 75, 75, 280]
+    want = expected(b, starts, 290, torch.float16)
+    c = b.to("cuda")
+    far = []
+    for pool in (c.kc, c.vc):
+        x = torch.empty(NB, 32, 8, 128, dtype=pool.dtype, device="cuda")
+        x[NB - pool.shape[0]:] = pool
+        far.append(x)
+    k = torch.full((rows, 8, 128), math.nan, dtype=torch.float16, device="cuda")
+    v = torch.full_like(k, math.nan)
+    ids = torch.where(c.tables < b.kc.shape[0], c.tables + (NB - b.kc.shape[0]), NB + 7).int()
+    pkv.paged_kv_gather(k, v, far[0], far[1], ids, c.lens, torch.tensor(starts, dtype=torch.int32, device="cuda") + first,
+                        k_scale=c.k_scale, v_scale=c.v_scale)
+    torch.cuda.synchronize()
+    same((k[first:].cpu(), v[first:].cpu()), want)
+    assert torch.isnan(k[first - 300:first]).all()

@@ -381,3 +381,72 @@ def test_e4m3_scales_and_planned():
     out = run(c, workspace=ws, planned=True)
     torch.cuda.synchronize()
     check(out, ref, bound)
+
+
+def test_e4m3_zero_scales():
+    """A KV head whose K scale is zero weighs every visible position alike; a zero V scale gives zeros."""
+    b = build([40, 1, 260], [40, 700, 300], 8, 4, 128, 16, "f16", seed=11, e4m3=True)
+    b.k_scale[1] = 0.0
+    b.v_scale[2] = 0.0
+    ref, bound = reference(b, torch.float16)
+    out = run(b.to("cuda"))
+    torch.cuda.synchronize()
+    check(out, ref, bound)
+
+
+def test_planned_batch_that_needs_no_plan():
+    """A batch small enough to run without a plan gives the same through prefill_plan and planned."""
+    b = build([1, 17, 5, 2], [1, 17, 33, 50], 4, 4, 64, 16, "f16", seed=12)
+    ref, bound = reference(b)
+    c = b.to("cuda")
+    ws = pkv.alloc_prefill_workspace(4, 25, 4, 4, 64)
+    ws.fill_(0xA5)
+    pkv.prefill_plan(ws, c.lens, c.starts, 25, 4, 4, 64, c.max_len)
+    out = run(c, workspace=ws, planned=True)
+    torch.cuda.synchronize()
+    check(out, ref, bound)
+    assert torch.equal(out.view(torch.int16), run(c).view(torch.int16))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, give what they give one after the other."""
+    bs = [build([300, 1, 40], [900, 3000, 40], 8, 2, 128, 16, "bf16", seed=13).to("cuda"),
+          build([33, 1], [6000, 1200], 8, 2, 64, 8, "f16", seed=14).to("cuda")]
+    want = [run(b) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    spaces = [pkv.alloc_prefill_workspace(len(b.lens), b.q.shape[0], 8, 2, b.q.shape[2]) for b in bs]
+    outs = [[torch.full_like(b.q, math.nan) for _ in range(8)] for b in bs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for b, s, ws, out in zip(bs, streams, spaces, outs):
+            with torch.cuda.stream(s):
+                pkv.paged_attention_prefill(out[i], b.q, b.kc, b.vc, b.tables, b.lens, b.starts, b.scale,
+                                            max_seq_len=b.max_len, workspace=ws)
+    torch.cuda.synchronize()
+    for w, out in zip(want, outs):
+        for o in out:
+            assert torch.equal(o.view(torch.int16), w.view(torch.int16))
+
+
+@pytest.mark.parametrize("group", [4, 3])
+def test_offsets_past_32_bits(group):
+    """Blocks past the pool's first 2^31 elements, query rows past q's and out's first 2^31."""
+    b = build([30, 1, 300], [100, 900, 300], 8 * group, 8, 128, 32, "bf16", seed=15)
+    ref, bound = reference(b)
+    NB = 2 ** 31 // (32 * 8 * 128) + b.kc.shape[0]
+    T = 2 ** 31 // (8 * group * 128) + 1 + b.q.shape[0]
+    c = b.to("cuda")
+    far = []
+    for pool in (c.kc, c.vc):
+        x = torch.empty(NB, 32, 8, 128, dtype=torch.bfloat16, device="cuda")
+        x[NB - pool.shape[0]:] = pool
+        far.append(x)
+    q = torch.empty(T, 8 * group, 128, dtype=torch.bfloat16, device="cuda")
+    q[T - c.q.shape[0]:] = c.q
+    out = torch.full_like(q, math.nan)
+    ids = torch.where(c.tables < b.kc.shape[0], c.tables + (NB - b.kc.shape[0]), NB + 7).int()
+    pkv.paged_attention_prefill(out, q, far[0], far[1], ids, c.lens, c.starts + (T - c.q.shape[0]), c.scale,
+                                max_seq_len=c.max_len)
+    torch.cuda.synchronize()
+    check(out[T - c.q.shape[0]:], ref, bound)
+    assert torch.isnan(out[T - c.q.shape[0] - 300:T - c.q.shape[0]]).all()
