@@ -272,3 +272,23 @@ def test_offsets_past_32_bits():
         assert int(accepted[-1]) == kept and tokens[-1, :kept].cpu().equal(drafts[-1, :kept])
         assert int(tokens[-1, kept]) == (V - 3 if kept == K else V - 1)
         assert (accepted[:-1] == 0).all() and (tokens[:-1] == -1).all()
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", pkv.ACCEPT_MAX_VOCAB), ("bf16", pkv.ACCEPT_MAX_VOCAB), ("f32", 40001), ("f16", 40002)])
+@pytest.mark.parametrize("poff,qoff", [(0, 1), (1, 0), (2, 3), (3, 3)])
+def test_the_two_rows_stand_differently(dtype, V, poff, qoff):
+    """Target and draft rows at every distance from a boundary of four elements, up to the largest vocabulary."""
+    x, p, q, u = inputs(1, 1, V, dtype, seed=30 + poff, noise=1.0)
+    rows = []
+    for t, off in ((p, poff), (q, qoff)):
+        flat = torch.full((t.numel() + 8,), math.nan, dtype=t.dtype, device="cuda")
+        rows.append(flat[off:off + t.numel()].view(t.shape))
+        rows[-1].copy_(t)
+    u[:, 0] = 1.0                                       # (refused wherever p <= q)
+    for last in (0.0, 0.5, 0.9999999):
+        u[:, -1] = last
+        tokens = torch.empty(1, 2, dtype=torch.int64, device="cuda")
+        accepted = torch.empty(1, dtype=torch.int32, device="cuda")
+        pkv.speculative_accept(tokens, accepted, x.cuda(), rows[0], u.cuda(), draft_probs=rows[1])
+        want = ref(x.numpy(), p.float().numpy(), q.float().numpy(), u.numpy(), None)
+        assert np.array_equal(tokens.cpu().numpy(), want[0]) and np.array_equal(accepted.cpu().numpy(), want[1])
