@@ -647,6 +647,8 @@ pkv_status prefill_args(pkv::PrefillArgs& a, pkv::PrefillWorkspace& lay, const i
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
     a.group = group;
+    a.by_group = pkv::fast_div(group);
+    a.by_kv_heads = pkv::fast_div(num_kv_heads);
     a.capacity = lay.capacity;
     a.part_cap = lay.part_cap;
     a.part_rows = lay.part_rows;
@@ -707,6 +709,7 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.block_tables = block_tables;
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.block_size = block_size;
+    a.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     a.num_blocks = num_blocks;
     a.err = error_word(current_device());
     // (a zero scale becomes one that no finite score survives, so that a masked score, -inf, stays -inf)

@@ -214,6 +214,18 @@ constexpr int kPrefillMinPart = 2;              // steps of a part at least
 constexpr int kPrefillLocal = 512;
 constexpr int kPrefillLocalItems = 1024;
 
+// Division by a number the host knows: q = (hi(mul * n) + n) >> shift, exact for 0 <= n < 2^31 (Granlund and
+// Montgomery's round-up method).
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+};
+inline FastDiv fast_div(int d) {
+    int s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    return {static_cast<uint32_t>((((uint64_t(1) << s) - static_cast<uint64_t>(d)) << 32) / static_cast<uint64_t>(d) + 1), s};
+}
+
 struct PrefillArgs {
     void* out;                       // [num_tokens][num_heads][D]
     const void* q;
@@ -235,7 +247,9 @@ struct PrefillArgs {
     int num_heads;
     int num_kv_heads;
     int group;                       // num_heads / num_kv_heads
+    FastDiv by_group, by_kv_heads;
     int block_size;
+    int block_shift;                 // log2(block_size)
     int capacity;                    // entries of `items`
     int part_cap;                    // partial slots per KV head
     int part_rows;                   // rows of a partial slot: min(256, num_tokens * group), a multiple of 32

@@ -154,7 +154,7 @@ __device__ __forceinline__ Entry fetch_entry(const PrefillArgs& a, int total, in
     Entry n{};
     n.live = w < total;
     if (n.live) {
-        const int e = static_cast<int>(w) / a.num_kv_heads;
+        const int e = pf::div(static_cast<int>(w), a.by_kv_heads);
         n.kvh = static_cast<int>(w) - e * a.num_kv_heads;
         n.x = __ldcg(a.items + 2 * e);
         n.y = __ldcg(a.items + 2 * e + 1);
@@ -166,7 +166,7 @@ __device__ __forceinline__ Entry fetch_entry(const PrefillArgs& a, int total, in
 __device__ __forceinline__ Entry find_entry(const PrefillArgs& a) {
     Entry n{};
     const int lane = threadIdx.x & 31;
-    const int e = static_cast<int>(blockIdx.x) / a.num_kv_heads;
+    const int e = pf::div(static_cast<int>(blockIdx.x), a.by_kv_heads);
     int before = 0;
     for (int s0 = 0; s0 < a.num_seqs; s0 += 32) {
         pf::Seq q{0, 0, 0};
@@ -211,12 +211,12 @@ __device__ __forceinline__ void read_item(const PrefillArgs& a, const Entry& n, 
     const int row0 = it.tile * kPrefillRows;
     it.rows = min(kPrefillRows, it.n * a.group - row0);
     const int past = it.L - it.n;
-    it.lim0 = max(0, past + row0 / a.group + 1);
+    it.lim0 = max(0, past + pf::div(row0, a.by_group) + 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = min(kSub, it.rows - i * kSub);
         if (r > 0) {
-            const int lim = past + (row0 + i * kSub + r - 1) / a.group + 1;      // the tile's last row's
+            const int lim = past + pf::div(row0 + i * kSub + r - 1, a.by_group) + 1;      // the tile's last row's
             it.end[i] = max(0, min(step1 < (1 << 23) ? step1 * kStep : it.L, min(lim, it.L)));
             it.nst[i] = max(0, (it.end[i] + kStep - 1) / kStep - it.step0);
         }
@@ -306,7 +306,7 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4]) {
 // Element offset / D of row r of the item's tile in q / out.
 __device__ __forceinline__ int64_t qo_row(const PrefillArgs& a, const Item& it, int r) {
     const int rr = it.tile * kPrefillRows + r;
-    const int tok = rr / a.group;
+    const int tok = pf::div(rr, a.by_group);
     return (static_cast<int64_t>(it.qs) + tok) * a.num_heads + it.kvh * a.group + (rr - tok * a.group);
 }
 
@@ -383,7 +383,7 @@ __device__ __forceinline__ int local_plan(const PrefillArgs& a, LocalPlan& lp) {
 #pragma unroll 1
         for (int w = kPrefillLocal / 2; w > 0; w >>= 1)
             if (lp.first[k + w] <= t) k += w;
-        st = pf::tile_steps(pf::Seq{lp.start[k], lp.n[k], lp.len[k]}, a.group, t - lp.first[k]);
+        st = pf::tile_steps(a, pf::Seq{lp.start[k], lp.n[k], lp.len[k]}, t - lp.first[k]);
     }
     lp.steps[t] = st;
     lp.seq[t] = k;
@@ -404,7 +404,7 @@ __device__ __forceinline__ int local_plan(const PrefillArgs& a, LocalPlan& lp) {
     const int item0 = at & 2047, slot = at >> 11 & 2047, merge = static_cast<unsigned>(at) >> 22;
     const int items = total & 2047;
     lp.slot[t] = slot;
-    const int len = parts > 0 ? (st + parts - 1) / parts : 0;
+    const int len = pf::part_len(st, parts);
     for (int p = 0; p < parts; ++p) {
         const int s0 = min(st, p * len);
         lp.key[item0 + p] = min(min(st, s0 + len) - s0, (1 << 21) - 1) << 10 | (kPrefillLocalItems - 1 - item0 - p);
@@ -436,7 +436,7 @@ __device__ __forceinline__ int local_plan(const PrefillArgs& a, LocalPlan& lp) {
 // The entry of rank e of a local plan.
 __device__ __forceinline__ Entry local_entry(const LocalPlan& lp, int e, int kvh) {
     const int P = lp.wsum[0], ref = lp.ref[lp.order[e]], t = ref >> 8, p = ref & 255, k = lp.seq[t], st = lp.steps[t];
-    const int parts = pf::parts_of(st, P), len = (st + parts - 1) / parts, s0 = min(st, p * len);
+    const int parts = pf::parts_of(st, P), len = pf::part_len(st, parts), s0 = min(st, p * len);
     Entry n;
     n.x = make_int4(k, t - lp.first[k], s0, min(st, s0 + len));
     n.y = make_int4(lp.start[k], lp.n[k], lp.len[k], parts > 1 ? prefill_split(parts, p, lp.slot[t]) : 0);
@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
         const int total = local_plan(a, lp) * a.num_kv_heads;
         if (warp == G::kPlan) {
             const int g = gridDim.x, b = blockIdx.x, w = lane * g + ((lane & 1) ? g - 1 - b : b);
-            if (w < total) mine = local_entry(lp, w / a.num_kv_heads, w % a.num_kv_heads);
+            const int e = pf::div(w, a.by_kv_heads);
+            if (w < total) mine = local_entry(lp, e, w - e * a.num_kv_heads);
         }
         fence_proxy_async_smem();                   // the scratch before the tiles' copies
         __syncthreads();
@@ -572,14 +573,14 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
                 auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
                     const int pos = (it.step0 + j) * kStep + lane * bs;
-                    return lane * bs < kStep && j < n && pos < stop ? __ldcg(trow + pos / bs) : -1;
+                    return lane * bs < kStep && j < n && pos < stop ? __ldcg(trow + (pos >> a.block_shift)) : -1;
                 };
                 int nxt = id_of(0);
                 for (int j = 0; j < n && ok; ++j) {
                     int id = nxt;
                     nxt = id_of(j + 1);
                     const int tok0 = (it.step0 + j) * kStep;
-                    const int nb = (min(stop, tok0 + kStep) - tok0 + bs - 1) / bs;
+                    const int nb = (min(stop, tok0 + kStep) - tok0 + bs - 1) >> a.block_shift;
                     if (lane < nb && (id < 0 || static_cast<int64_t>(id) >= a.num_blocks)) {
                         raise_error(a.err, kErrBounds);
                         id = -1;
@@ -719,14 +720,14 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
                 auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
                     const int pos = (it.step0 + j) * kStep + lane * bs;
-                    return lane * bs < kStep && j < n && pos < stop ? __ldcg(trow + pos / bs) : -1;
+                    return lane * bs < kStep && j < n && pos < stop ? __ldcg(trow + (pos >> a.block_shift)) : -1;
                 };
                 int nxt = id_of(0);
                 for (int j = 0; j < n; ++j) {
                     int id = nxt;
                     nxt = id_of(j + 1);
                     const int tok0 = (it.step0 + j) * kStep;
-                    const int nb = (min(stop, tok0 + kStep) - tok0 + bs - 1) / bs;
+                    const int nb = (min(stop, tok0 + kStep) - tok0 + bs - 1) >> a.block_shift;
                     if (lane < nb && (id < 0 || static_cast<int64_t>(id) >= a.num_blocks)) {
                         raise_error(a.err, kErrBounds);
                         id = -1;                             // outside the tensor map: TMA fills zeros
@@ -1078,7 +1079,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
         for (int r = 0; ok && get_item(r, it, ok); ++r) {
             const int myrow = wg * kSub + t;                 // row of the item
             const bool has = myrow < it.rows;
-            const int rr = it.tile * kPrefillRows + myrow, tok = rr / a.group;
+            const int rr = it.tile * kPrefillRows + myrow, tok = pf::div(rr, a.by_group);
             const int at = has ? (it.qs + tok) * a.num_heads + it.kvh * a.group + (rr - tok * a.group) : -1;   // row of out
             // positions this row sees (rows past the end: all, their weights go nowhere)
             const int lim = has ? max(0, min(it.L, it.L - it.n + tok + 1)) : 0x7fffffff;

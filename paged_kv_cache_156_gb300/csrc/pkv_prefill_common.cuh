@@ -30,11 +30,17 @@ __device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int s, bool report
 
 __device__ __forceinline__ int tiles_of(const Seq& q, int group) { return (q.n * group + kPrefillRows - 1) / kPrefillRows; }
 
+// (An integer division by a number the compiler does not know is some thirty instructions, and the planning code runs
+// each of its own about once: it is bound by fetching them.)
+__device__ __forceinline__ int div(int n, FastDiv d) {       // 0 <= n < 2^31
+    return static_cast<int>((__umulhi(d.mul, static_cast<unsigned>(n)) + static_cast<unsigned>(n)) >> d.shift);
+}
+
 // Steps the last row of a tile sees.
-__device__ __forceinline__ int tile_steps(const Seq& q, int group, int tile) {
-    const int rows = q.n * group;
+__device__ __forceinline__ int tile_steps(const PrefillArgs& a, const Seq& q, int tile) {
+    const int rows = q.n * a.group;
     const int last = min(rows, (tile + 1) * kPrefillRows) - 1;
-    const int lim = min(q.len, max(0, q.len - q.n + last / group + 1));
+    const int lim = min(q.len, max(0, q.len - q.n + div(last, a.by_group) + 1));
     return (lim + kPrefillStep - 1) / kPrefillStep;
 }
 
@@ -48,7 +54,17 @@ __device__ __forceinline__ int warp_scan(int v) {            // inclusive
     return v;
 }
 
-__device__ __forceinline__ int parts_of(int steps, int P) { return max(1, (steps + P - 1) / P); }
+// ceil(steps / P), at least 1, where that is a small number (a tile has up to kPrefillMaxParts parts): the quotient in
+// single precision is then off by one at most, which the remainder shows.
+__device__ __forceinline__ int parts_of(int steps, int P) {
+    const int n = steps + P - 1;
+    int q = __float2int_rz(__fdividef(static_cast<float>(n), static_cast<float>(P)));
+    const int r = n - q * P;
+    q += (r >= P) - (r < 0);
+    return max(1, q);
+}
+// Steps of each of a tile's parts.
+__device__ __forceinline__ int part_len(int steps, int parts) { return parts > 1 ? (steps + parts - 1) / parts : steps; }
 
 constexpr int kCand = 32;            // (a lane each)
 // Parts that candidate c cuts the longest tile into: 1 .. 20, then ever wider apart up to kPrefillMaxParts.

@@ -86,7 +86,7 @@ __device__ __forceinline__ int find_seq(const Shared& sh, int tile) {
 // Tile i of the current chunk: its sequence and steps.
 __device__ __noinline__ int tile_of(const PrefillArgs& a, const Shared& sh, int i, int* k) {
     *k = find_seq(sh, i);
-    return tile_steps(Seq{sh.start[*k], sh.n[*k], sh.len[*k]}, a.group, i - sh.first[*k]);
+    return tile_steps(a, Seq{sh.start[*k], sh.n[*k], sh.len[*k]}, i - sh.first[*k]);
 }
 
 __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __grid_constant__ PrefillArgs a) {
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __grid_con
                 if (cached) k = sh.seq[i];
                 const int tile = i - sh.first[k];
                 const int parts = parts_of(st, P);
-                const int len = (st + parts - 1) / parts;           // equal parts
+                const int len = pf::part_len(st, parts);            // equal parts
                 int slot = 0;
                 if (pass == 1 && parts > 1) {
                     slot = atomicAdd(&sh.next_slot, parts);
