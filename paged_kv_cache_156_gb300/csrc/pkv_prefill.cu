@@ -51,7 +51,7 @@
 // position per column is noted; the epilogue then gives inf or NaN to exactly
 // the rows that see them.
 //
-// E4M3 pools.  Warp 8 streams tiles of codes, and three warps (10, 12, 14) expand
+// E4M3 pools.  Warp 8 streams tiles of codes, and three warps (10, 12, 13: one a scheduler) expand
 // them into the ring as f16, where every code is exact, and clean V on the way;
 // K's scale multiplies the scores, V's the output.  The products run in f16: a
 // bf16 query tile is converted in place by its softmax warps.  A step takes 1.8 us
@@ -77,7 +77,7 @@ constexpr int kSub = kPrefillSub;
 template <int D, bool KV8 = false>
 struct PfGeo {
     static constexpr int kThreads = 512;
-    static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12, kLoadQ = 13, kPlan = 15;   // (9 and 11: MMAs; 12 and 14: cleaning)
+    static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12, kLoadQ = KV8 ? 14 : 13, kPlan = 15;   // (9 and 11: MMAs; 12 and 14: cleaning; E4M3: 10, 12 and 13 expand)
     static constexpr int kHalves = D * 2 / 128;             // 128-byte column planes of a tile
     static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
     static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
@@ -85,7 +85,7 @@ struct PfGeo {
     static constexpr int kStages = KV8 ? 4 : D == 128 ? 5 : 10;
     static constexpr int kCodes = KV8 ? 2 : 0;              // staged tiles of codes (128 rows of D bytes)
     static constexpr int kCodeTile = 128 * D;
-    static constexpr int kConverters = 3;                   // warps 10, 12 and 14
+    static constexpr int kConverters = 3;                   // warps 10, 12 and 13: on two of the schedulers (10, 12, 14) 120 us, on three 117 (8 chunks of 256 to 512)
     static constexpr size_t kRing = 2 * size_t(kTile);      // after the two Q tiles
     static constexpr size_t kCode = kRing + size_t(kStages) * kTile;
     static constexpr size_t kBars = kCode + size_t(kCodes) * kCodeTile;
@@ -605,13 +605,13 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 const unsigned long long t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
             }
-        } else if (KV8 && (warp == G::kLoadV || warp == G::kClean || warp == G::kClean + 2)) {
+        } else if (KV8 && (warp == G::kLoadV || warp == G::kClean || warp == G::kClean + 1)) {
             // ======================================================== codes to f16, V cleaned on the way
             // A lane takes 16 codes, 32 bytes of f16 in one column plane.  A load or store instruction covers
             // eight rows by four lanes a row, and every eight lanes two rows whose numbers differ in bits 0
             // and 2 (q and q ^ 5): the swizzles then put the eight pieces into different banks both times.  A
             // lane's row in a group of eight, and so its swizzle, never changes: addresses advance by 1 KB.
-            const int cw = (warp - G::kLoadV) / 2;
+            const int cw = warp == G::kLoadV ? 0 : warp - G::kClean + 1;
             int* mine = bad + cw * D;
             const int l3 = lane & 3, rl = (lane >> 3) ^ ((lane >> 2) & 1 ? 5 : 0);
             Ring<ST> c;
