@@ -416,13 +416,15 @@ __device__ __forceinline__ int local_plan(const PrefillArgs& a, LocalPlan& lp) {
     }
     if (t < 3 && items + t < kPrefillLocalItems) lp.key[items + t] = -1;      // (the last four are read whole)
     __syncthreads();
+    const bool alone = items * a.num_kv_heads <= static_cast<int>(gridDim.x);       // an item a CTA at most: in any order
+    const int n = alone ? 0 : items;
 #pragma unroll 1
     for (int i = t; i < items; i += 512) {
         const int key = lp.key[i];
-        int rank = 0;
+        int rank = alone ? i : 0;
         const int4* all = reinterpret_cast<const int4*>(lp.key);
 #pragma unroll 4
-        for (int j = 0; 4 * j < items; ++j) {
+        for (int j = 0; 4 * j < n; ++j) {
             const int4 o = all[j];
             rank += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
         }
