@@ -724,6 +724,7 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (planned) a.direct = 0;
     a.local = !planned && !a.direct && pkv::prefill_local(num_seqs, num_tokens, num_heads, num_kv_heads, a.slots, lay);
     cudaError_t e = planned || a.direct || a.local ? cudaSuccess : pkv::launch_prefill_plan(a, s);
     if (e == cudaSuccess) e = pkv::launch_prefill(a, tmq, tmk, tmv, dt == PKV_F16 ? 0 : 1, head_dim, s);
@@ -753,7 +754,6 @@ pkv_status pkv_prefill_plan(const int32_t* seq_lens, const int32_t* query_starts
                                  num_kv_heads, head_dim, workspace, workspace_bytes);
     if (st != PKV_OK || num_seqs == 0 || num_tokens == 0) return st;
     a.err = error_word(current_device());
-    if (a.direct) return ok();                           // (the run reads no plan)
     cudaError_t e = pkv::launch_prefill_plan(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "prefill plan launch: %s", cudaGetErrorString(e));
     return ok();

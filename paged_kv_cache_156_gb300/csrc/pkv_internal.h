@@ -210,6 +210,10 @@ constexpr int kPrefillSub = 128;                // rows of one of an item's two 
 constexpr int kPrefillStep = 128;
 constexpr int kPrefillMaxParts = 152;           // parts one tile's positions are split into at most
 constexpr int kPrefillMinPart = 2;              // steps of a part at least
+// No tile is split in a batch of sequences of up to so many steps: what the parts save the planning and the merge cost.
+// Tiles of 4 to 16 rows, one to four sequences: 6 steps 13.3 us whole, 13.7 to 17.6 split; 8 steps 15.8 and 14.0 to 16.8;
+// 10 steps 18.4 and 14.2 to 17.6.
+constexpr int kPrefillNoSplit = 8;
 // The prefill kernel plans by itself up to this many sequences and tiles a KV head, and items (parts and all)
 constexpr int kPrefillLocal = 512;
 constexpr int kPrefillLocalItems = 1024;

@@ -211,7 +211,7 @@ PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int 
 
 bool prefill_may_split(int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots) {
     const int64_t tiles = num_tokens * (num_heads / num_kv_heads) / kPrefillRows;       // at least
-    return max_seq_len > kPrefillMinPart * kPrefillStep && tiles * num_kv_heads < 8ll * slots;
+    return max_seq_len > kPrefillNoSplit * kPrefillStep && tiles * num_kv_heads < 8ll * slots;
 }
 
 bool prefill_direct(int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int slots) {
