@@ -27,15 +27,15 @@
 // turns (99 to 97 us over 24 ragged prompts of 5 to 2000 tokens, 12 heads over 4).
 //
 // What bounds it.  A step of two tiles is 2048 tensor cycles at head_dim 128 and
-// takes 2700 to 2900: a tile's S, softmax, P V and next S are a serial chain, under
+// takes 2650 to 2850: a tile's S, softmax, P V and next S are a serial chain, under
 // which only the other tile's products run.  One prompt of 8192 tokens, 64 heads
-// over 8: 690 us, 1590 TFLOP/s; of 16384: 1677 TFLOP/s, 87% of the rate measured
-// for a large bf16 matrix product.  Small batches pay some 10 us of start-up (plan
-// 3 to 4, first S 5, second 1.7: dependent latencies), and the items' ends spread
-// by a tenth of a call.  Tiles of up to 128 rows compute half as much over the same
-// K and V: where all CTAs run such, a step takes 1.41 us, the HBM rate.  At
-// head_dim 64 the exponentials, as many for half the products, come first: 970
-// TFLOP/s over 16384 tokens.
+// over 8: 683 us, 1610 TFLOP/s; of 16384: 1670 TFLOP/s, 87% of the rate measured
+// for a large bf16 matrix product.  Start-up takes 7 us without a plan, 9 with one
+// (plan 3 to 4, first S 5, second 1.6: latencies and instruction fetch), and the
+// items' ends spread by a tenth of a call.  Tiles of up to 128 rows compute half as
+// much over the same K and V: where all CTAs run such, a step takes 1.41 us, the HBM
+// rate.  At head_dim 64 the exponentials, as many for half the products, come first:
+// 990 TFLOP/s over 16384 tokens, 16 heads over 4.
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (they also write the output),
 // 13 loads Q tiles, 8 and 10 stream the K and V blocks (TMA, one
@@ -54,8 +54,8 @@
 // E4M3 pools.  Warp 8 streams tiles of codes, and three warps (10, 12, 13: one a scheduler) expand
 // them into the ring as f16, where every code is exact, and clean V on the way;
 // K's scale multiplies the scores, V's the output.  The products run in f16: a
-// bf16 query tile is converted in place by its softmax warps.  A step takes 1.8 us
-// (1.5 over 16-bit pools): the conversion shares the issue slots with the softmax.
+// bf16 query tile is converted in place by its softmax warps.  A step takes 1.7 us
+// (1.45 over 16-bit pools): the conversion shares the issue slots with the softmax.
 //
 // Every wait is bounded in wall time; a CTA that gives up raises the error
 // word, gives its copies and products in flight time to land and frees its TMEM.
