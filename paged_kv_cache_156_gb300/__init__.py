@@ -219,6 +219,18 @@ def _cuda(name, t, dtype=None, ndim=None):
     return t.data_ptr()
 
 
+def _usual(*tensors) -> bool:
+    """Plain contiguous tensors of the current device.  The calls below take such arguments without the checks that
+    name what is wrong (which cost a third of a small call's host time); whatever else they meet goes through those."""
+    dev = tensors[0].get_device() if type(tensors[0]) is _Tensor else -1
+    if dev < 0:
+        return False
+    for t in tensors:
+        if type(t) is not _Tensor or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return dev == _current_device()
+
+
 def _pool(name, c, dtypes=(torch.float16, torch.bfloat16)):
     _cuda(name, c, dtypes, 4)
     return c.shape  # num_blocks, block_size, num_kv_heads, head_dim
@@ -501,7 +513,6 @@ def prefill_plan(workspace, seq_lens, query_starts, num_tokens, num_heads, num_k
                                    _stream(workspace)))
 
 
-@_one_device
 def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, scale=None,
                             max_seq_len=None, workspace=None, planned=False, k_scale=None, v_scale=None) -> None:
     """Attention of a ragged batch of new tokens over the paged cache.  q, out: [T, Hq, d]; sequence s owns rows
@@ -510,6 +521,32 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
     see ``alloc_prefill_workspace`` (allocated here when omitted); ``planned``: run over the list ``prefill_plan``
     put there for this batch.  ``max_seq_len`` is read from the device if omitted, which synchronises.  uint8 pools hold
     E4M3 codes and take k_scale / v_scale (float32 [Hkv]) as paged_attention_decode_fp8 does."""
+    if _usual(q, out, key_cache, value_cache, block_tables, seq_lens, query_starts, workspace) and scale is not None and \
+            max_seq_len is not None:
+        dt, qdt, pool, rows, table = key_cache.dtype, q.dtype, key_cache.shape, q.shape, block_tables.shape
+        kv8 = dt is torch.uint8
+        if (kv8 or dt is qdt) and qdt in _DT and out.dtype is qdt and value_cache.dtype is dt and \
+                block_tables.dtype is seq_lens.dtype is query_starts.dtype is torch.int32 and len(pool) == 4 and \
+                len(rows) == 3 and len(table) == 2 and value_cache.shape == pool and out.shape == rows and \
+                seq_lens.shape == table[:1] and query_starts.shape == (table[0] + 1,) and rows[2] == pool[3] and \
+                (k_scale is None and v_scale is None if not kv8 else _usual(q, k_scale, v_scale) and
+                 k_scale.dtype is v_scale.dtype is torch.float32 and k_scale.shape == v_scale.shape == pool[2:3]):
+            args = (out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+                    table[1], seq_lens.data_ptr(), query_starts.data_ptr(), table[0], rows[0], int(max_seq_len), rows[1],
+                    pool[2], pool[3], pool[1], pool[0], float(scale), _DT[qdt])
+            end = (workspace.data_ptr(), workspace.nbytes, PLANNED if planned else 0, _stream(q))
+            if kv8:
+                status = load().pkv_paged_attention_prefill_fp8(*args, k_scale.data_ptr(), v_scale.data_ptr(), *end)
+            else:
+                status = load().pkv_paged_attention_prefill(*args, *end)
+            return _check(status)
+    _prefill(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, scale, max_seq_len, workspace, planned,
+             k_scale, v_scale)
+
+
+@_one_device
+def _prefill(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, scale, max_seq_len, workspace, planned,
+             k_scale, v_scale) -> None:
     dt = key_cache.dtype
     kv8 = dt is torch.uint8
     if not kv8 and (k_scale is not None or v_scale is not None):
@@ -536,8 +573,7 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
         workspace = alloc_prefill_workspace(B, T, Hq, Hkv, d, q.device)
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     wp, flags = _cuda("workspace", workspace), PLANNED if planned else 0
     if kv8:
         ks, vs = _scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv)
@@ -548,12 +584,32 @@ def paged_attention_prefill(out, q, key_cache, value_cache, block_tables, seq_le
                                                   scale, _DT[dt], wp, workspace.nbytes, flags, _stream(q)))
 
 
-@_one_device
 def paged_kv_gather(k_out, v_out, key_cache, value_cache, block_tables, seq_lens, row_starts, k_scale=None,
                     v_scale=None) -> None:
     """Rows row_starts[s] + t of k_out, v_out ([R, Hkv, d]) = position t < seq_lens[s] of sequence s (row_starts
     int32 [B + 1]; other rows are left as they are).  uint8 pools hold E4M3 codes and take k_scale / v_scale
     (float32 [Hkv]): the rows are then code value * scale, rounded to the outputs' fp16 / bf16."""
+    if _usual(key_cache, value_cache, k_out, v_out, block_tables, seq_lens, row_starts):
+        dt, odt, pool, rows, table = key_cache.dtype, k_out.dtype, key_cache.shape, k_out.shape, block_tables.shape
+        kv8 = dt is torch.uint8
+        if (kv8 or dt is odt) and odt in _DT and v_out.dtype is odt and value_cache.dtype is dt and \
+                block_tables.dtype is seq_lens.dtype is row_starts.dtype is torch.int32 and len(pool) == 4 and \
+                len(rows) == 3 and len(table) == 2 and value_cache.shape == pool and v_out.shape == rows and \
+                seq_lens.shape == table[:1] and row_starts.shape == (table[0] + 1,) and rows[1:] == pool[2:] and \
+                (k_scale is None and v_scale is None if not kv8 else _usual(k_out, k_scale, v_scale) and
+                 k_scale.dtype is v_scale.dtype is torch.float32 and k_scale.shape == v_scale.shape == pool[2:3]):
+            args = (k_out.data_ptr(), v_out.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+                    table[1], seq_lens.data_ptr(), row_starts.data_ptr(), table[0], rows[0], *pool, _DT[odt])
+            if kv8:
+                status = load().pkv_paged_kv_gather_fp8(*args, k_scale.data_ptr(), v_scale.data_ptr(), _stream(k_out))
+            else:
+                status = load().pkv_paged_kv_gather(*args, _stream(k_out))
+            return _check(status)
+    _gather(k_out, v_out, key_cache, value_cache, block_tables, seq_lens, row_starts, k_scale, v_scale)
+
+
+@_one_device
+def _gather(k_out, v_out, key_cache, value_cache, block_tables, seq_lens, row_starts, k_scale, v_scale) -> None:
     dt = key_cache.dtype
     kv8 = dt is torch.uint8
     if not kv8 and (k_scale is not None or v_scale is not None):
@@ -581,7 +637,6 @@ def paged_kv_gather(k_out, v_out, key_cache, value_cache, block_tables, seq_lens
         _check(load().pkv_paged_kv_gather(ko, vo, kc, vc, bt, W, sl, rs, B, R, NB, bs, Hkv, d, _DT[dt], _stream(key_cache)))
 
 
-@_one_device
 def speculative_accept(tokens, num_accepted, draft_tokens, target_probs, uniform, draft_probs=None,
                        num_drafts=None) -> None:
     """Accept drafted tokens against the target's probabilities and draw the token that follows.
@@ -590,6 +645,25 @@ def speculative_accept(tokens, num_accepted, draft_tokens, target_probs, uniform
     probabilities, taken as certain) float32 / float16 / bfloat16; uniform float32 [B, K + 1] in [0, 1): entry
     i < K decides draft i, entry K the draw; num_drafts int32 [B] (None: K each).  tokens int64 [B, K + 1]
     receives the accepted drafts, the drawn token, then -1; num_accepted int32 [B] the count of drafts kept."""
+    if _usual(tokens, num_accepted, draft_tokens, target_probs, uniform) and \
+            (draft_probs is None or _usual(tokens, draft_probs)) and (num_drafts is None or _usual(tokens, num_drafts)):
+        dt, drafts, target, rows = target_probs.dtype, draft_tokens.shape, target_probs.shape, tokens.shape
+        if dt in _PROB_DT and tokens.dtype is draft_tokens.dtype is torch.int64 and num_accepted.dtype is torch.int32 and \
+                uniform.dtype is torch.float32 and len(drafts) == 2 and len(target) == 3 and \
+                rows == (drafts[0], drafts[1] + 1) and target[:2] == rows and uniform.shape == rows and \
+                num_accepted.shape == drafts[:1] and \
+                (draft_probs is None or draft_probs.dtype is dt and draft_probs.shape == (*drafts, target[2])) and \
+                (num_drafts is None or num_drafts.dtype is torch.int32 and num_drafts.shape == drafts[:1]):
+            return _check(load().pkv_speculative_accept(
+                tokens.data_ptr(), num_accepted.data_ptr(), draft_tokens.data_ptr(),
+                None if num_drafts is None else num_drafts.data_ptr(), target_probs.data_ptr(),
+                None if draft_probs is None else draft_probs.data_ptr(), uniform.data_ptr(), *drafts, target[2],
+                _PROB_DT[dt], _stream(tokens)))
+    _accept(tokens, num_accepted, draft_tokens, target_probs, uniform, draft_probs, num_drafts)
+
+
+@_one_device
+def _accept(tokens, num_accepted, draft_tokens, target_probs, uniform, draft_probs, num_drafts) -> None:
     ptrs = [_cuda("tokens", tokens, torch.int64, 2), _cuda("num_accepted", num_accepted, torch.int32, 1),
             _cuda("draft_tokens", draft_tokens, torch.int64, 2)]
     target = _cuda("target_probs", target_probs, _PROB_DTS, 3)
