@@ -238,6 +238,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -1272,6 +1277,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                     for (int hh = 0; hh < 2; ++hh) {
                         const int ra = 16 * hh + (lane >> 2);                                 // rows ra and ra + 8 of the warp
                         const float ia = __shfl_sync(0xffffffffu, inv, ra), ib = __shfl_sync(0xffffffffu, inv, ra + 8);
+                        const uint64_t ia2 = pack64(ia, ia), ib2 = pack64(ib, ib);
                         const int aa = __shfl_sync(0xffffffffu, at, ra), ab = __shfl_sync(0xffffffffu, at, ra + 8);
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 64) {
@@ -1284,8 +1290,10 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const uint32_t* y = &o[4 * (g + e)];
-                                    wa[e] = Mma<OT>::pack(__uint_as_float(y[0]) * ia, __uint_as_float(y[1]) * ia);
-                                    wb[e] = Mma<OT>::pack(__uint_as_float(y[2]) * ib, __uint_as_float(y[3]) * ib);
+                                    const float2 fa = unpack64(mul2(pack64(__uint_as_float(y[0]), __uint_as_float(y[1])), ia2));
+                                    const float2 fb = unpack64(mul2(pack64(__uint_as_float(y[2]), __uint_as_float(y[3])), ib2));
+                                    wa[e] = Mma<OT>::pack(fa.x, fa.y);
+                                    wb[e] = Mma<OT>::pack(fb.x, fb.y);
                                 }
                                 quad_transpose(wa);
                                 quad_transpose(wb);
