@@ -1253,6 +1253,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 if (!ok) break;
                 tc::fence_after_sync();
                 const float vs = KV8 ? __ldcg(a.v_scale + it.kvh) : 1.0f;
+                const float inv = l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l;                  // (a NaN sum stays)
                 if (split) {
                     // a row a thread, 16 bytes of 32 neighbouring rows side by side
 #pragma unroll 1
@@ -1272,7 +1273,6 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                     // The 16x256b shape gives a quad two rows' columns; transposed over the quad, four lanes
                     // write 64 contiguous bytes of a row (a row a thread would touch 32 lines a store, 2 us
                     // an item in the load-store unit).
-                    const float inv = l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l;              // (a NaN sum stays)
 #pragma unroll 1
                     for (int hh = 0; hh < 2; ++hh) {
                         const int ra = 16 * hh + (lane >> 2);                                 // rows ra and ra + 8 of the warp
@@ -1306,12 +1306,14 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                         }
                     }
                 }
-                tc::fence_before_sync();
-                const bool bad0 = bad_tag[0] == r, bad1 = bad_tag[1] == r, bad2 = KV8 && bad_tag[2] == r;
-                if (bad0 || bad1 || bad2) {                  // rare: V elements that were cleaned away
+                // rare: V elements that were cleaned away are added to what the products gave, which may hold an
+                // infinity or NaN of its own from a position that every row sees
+                const bool bad0 = __any_sync(0xffffffffu, bad_tag[0] == r), bad1 = __any_sync(0xffffffffu, bad_tag[1] == r),
+                           bad2 = KV8 && __any_sync(0xffffffffu, bad_tag[2] == r);
+                if (bad0 || bad1 || bad2) {
                     __syncwarp();
 #pragma unroll 1
-                    for (int c = 0; has && c < D; ++c) {
+                    for (int c = 0; c < D; ++c) {
                         bool up, down;
                         if (KV8) {
                             up = (bad0 && bad[c] < seen) || (bad1 && bad[D + c] < seen) || (bad2 && bad[2 * D + c] < seen);
@@ -1320,12 +1322,19 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                             up = (bad0 && bad[c] < seen) || (bad1 && bad[2 * D + c] < seen);
                             down = (bad0 && bad[D + c] < seen) || (bad1 && bad[3 * D + c] < seen);
                         }
-                        if (!up && !down) continue;
-                        const float x = (up ? INFINITY : 0.0f) + (down ? -INFINITY : 0.0f);
-                        if (split) reinterpret_cast<float*>(prow + static_cast<int64_t>(c / 4) * a.part_rows)[c & 3] += x;
-                        else out[static_cast<int64_t>(at) * D + c] = from_float<OT>(x);
+                        const bool add = has && (up || down);
+                        if (__any_sync(0xffffffffu, add)) {
+                            const uint32_t o = tc::ld1(to + c);
+                            tc::wait_ld();
+                            const float x = (up ? INFINITY : 0.0f) + (down ? -INFINITY : 0.0f);
+                            if (add) {
+                                if (split) reinterpret_cast<float*>(prow + static_cast<int64_t>(c / 4) * a.part_rows)[c & 3] += x;
+                                else out[static_cast<int64_t>(at) * D + c] = from_float<OT>(__uint_as_float(o) * inv + x);
+                            }
+                        }
                     }
                 }
+                tc::fence_before_sync();
             } else if (has && !split) {                      // rows that see nothing
                 uint4* o = reinterpret_cast<uint4*>(out + static_cast<int64_t>(at) * D);
 #pragma unroll

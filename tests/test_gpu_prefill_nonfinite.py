@@ -1,0 +1,105 @@
+"""paged_attention_prefill where the cache or the scores are not finite.
+
+The expected kinds (finite, an infinity, NaN) come from the definition in IEEE arithmetic over the positions that a
+token sees: out = sum_t w_t V_t / sum_t w_t, w_t = exp(z_t - max z).  The weights of these inputs stay far above the
+smallest 16-bit number unless a test says otherwise.
+"""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_156_gb300 as pkv
+from prefill_cases import build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    pkv.device_error(reset=True)
+    yield
+    assert pkv.device_error(reset=True) == 0
+
+
+def run(b):
+    c = b.to("cuda")
+    out = torch.full_like(c.q, -7.0)
+    pkv.paged_attention_prefill(out, c.q, c.kc, c.vc, c.tables, c.lens, c.starts, c.scale, max_seq_len=c.max_len,
+                                k_scale=c.k_scale, v_scale=c.v_scale)
+    torch.cuda.synchronize()
+    return out.cpu()
+
+
+def slot(b, s, pos):
+    bs = b.kc.shape[1]
+    return int(b.tables[s, pos // bs]), pos % bs
+
+
+def definition(b):
+    """[T, Hq, d] in float64: sums over the seen positions only, with IEEE's infinities and NaN."""
+    T, Hq, d = b.q.shape
+    G = Hq // b.kc.shape[2]
+    out = torch.full((T, Hq, d), -7.0, dtype=torch.float64)
+    for s in range(len(b.lens)):
+        r0, r1, L = int(b.starts[s]), int(b.starts[s + 1]), int(b.lens[s])
+        K, V = b.dense(s, b.kc, b.k_scale), b.dense(s, b.vc, b.v_scale)
+        for r in range(r0, r1):
+            lim = L - (r1 - r0) + (r - r0) + 1
+            for h in range(Hq):
+                if lim <= 0:
+                    out[r, h] = 0.0
+                    continue
+                z = (K[:lim, h // G] * b.q[r, h].double()).sum(1) * b.scale
+                w = torch.exp(z - z.max())
+                out[r, h] = (w[:, None] * V[:lim, h // G]).sum(0) / w.sum()
+    return out
+
+
+def same_kind(got, want):
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf], want[inf])
+
+
+# Old positions every token sees (position 550 in the 128-position step that the last tokens see in part), new
+# tokens' own; split over a long cache, or not.
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [("bf16", 8, 2, 128), ("f16", 3, 1, 64)])
+def test_seen_by_all_and_seen_in_part(dtype, heads, kv_heads, dim, split):
+    """What an element that every token sees gave the sum stays when elements that only the last tokens see are added:
+    opposite infinities and NaN anywhere give NaN, wherever they lie."""
+    total = 6000 if split else 600
+    near = total - 50                                   # seen by every token, in the last tokens' step
+    b = build([40], [total], heads, kv_heads, dim, 16, dtype, seed=3)
+    clean = run(b)
+    pairs = [(math.nan, math.inf), (-math.inf, math.inf), (math.inf, -math.inf), (math.inf, math.inf),
+             (math.nan, -math.inf), (math.nan, math.nan), (None, math.inf), (None, -math.inf), (-math.inf, None)]
+    for i, (old, new) in enumerate(pairs):
+        for j, pos in enumerate((100, near)):
+            col = 2 * i + j + 1
+            if old is not None:
+                blk, at = slot(b, 0, pos)
+                b.vc[blk, at, 0, col] = old
+            if new is not None:
+                blk, at = slot(b, 0, total - 1 - i % 3)
+                b.vc[blk, at, 0, col] = new
+    got, want = run(b), definition(b)
+    same_kind(got, want)
+    keep = torch.isfinite(want)
+    assert torch.equal(got[keep], clean[keep])          # (columns are independent of one another)
+    assert torch.isnan(got[39, 0, 1]).all() and torch.isnan(got[39, 0, 3]) and got[39, 0, 7] == math.inf
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_nan_scores_beside_infinite_values(split):
+    """A NaN key that every token sees makes every output NaN, columns with an infinite value among them."""
+    total = 6000 if split else 600
+    b = build([40], [total], 4, 1, 64, 16, "bf16", seed=4)
+    blk, at = slot(b, 0, 77)
+    b.kc[blk, at, 0, 5] = math.nan
+    blk, at = slot(b, 0, total - 1)
+    b.vc[blk, at, 0, 9] = math.inf
+    assert torch.isnan(run(b)).all()
