@@ -92,8 +92,8 @@ struct PfGeo {
     static constexpr int kItems = 4;                        // items decoded ahead
     static constexpr int kItemReaders = 15;                 // warps that read each
     static constexpr int kNumBars = 3 * kStages + 21 + 2 * kItems + 2 * kCodes;
-    static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, epilogue count, tags
-    static constexpr size_t kBad = (kMisc + 32 + 15) / 16 * 16;   // first positions of non-finite V elements: [2 warps][+inf, -inf][D], or [3 warps][NaN][D]
+    static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, tags [3], epilogues [8]
+    static constexpr size_t kBad = (kMisc + 52 + 15) / 16 * 16;   // first positions of non-finite V elements: [2 warps][+inf, -inf][D], or [3 warps][NaN][D]
     static constexpr size_t kList = kBad + size_t(4) * D * 4;    // [kItems] decoded items
     static constexpr size_t kBytes = kList + kItems * 64;
     static_assert(!KV8 || D == 128, "E4M3 pools: a row of codes is one 128-byte plane");
@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
     uint64_t* code_empty = code_full + G::kCodes;   // [kCodes] it is expanded (converter warps)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kMisc + 4);
-    volatile int* epilogues = abort_flag + 1;       // epilogues finished, counted per softmax warp
-    volatile int* bad_tag = abort_flag + 2;         // [3] the item whose non-finite V elements a warp's table lists (-1: none)
+    volatile int* epilogues = abort_flag + 4;       // [8] items a softmax warp is through with
+    volatile int* bad_tag = abort_flag + 1;         // [3] the item whose non-finite V elements a warp's table lists (-1: none)
     int* bad = reinterpret_cast<int*>(smem + G::kBad);      // (kBad)
 
     const int warp = threadIdx.x >> 5;
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             mbar_init(&code_empty[i], G::kConverters);
         }
         mbar_init(fin, 2);
-        *epilogues = 0;
+        for (int i = 0; i < 8; ++i) epilogues[i] = 0;
         bad_tag[0] = bad_tag[1] = bad_tag[2] = -1;
         // the 128B swizzle and the MMA descriptors assume 1 KB aligned tiles
         const bool misaligned = (smem_u32(smem) & 1023u) != 0;
@@ -560,6 +560,20 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[k]);
         return it.rows >= 0;
+    };
+
+    // Before a cleaning warp writes item r's first entry into its table: every softmax warp is through with the items
+    // before r, whose entries it may still read.  Each by itself: a warp whose tile has no steps in several items runs
+    // ahead of the others by as many.  False: the wait gave up, or another role did.
+    auto table_free = [&](int r) {
+        const unsigned long long t0 = globaltimer_ns();
+        for (;;) {
+            if (!__any_sync(0xffffffffu, lane < 8 && epilogues[lane] < r)) break;
+            if (__any_sync(0xffffffffu, *abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+            __nanosleep(200);
+        }
+        __threadfence_block();
+        return true;
     };
 
     if (warp >= 8) {
@@ -659,8 +673,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                             }
                             if (__any_sync(0xffffffffu, hit != 0)) {                           // rare
                                 if (bad_tag[cw] != r) {
-                                    const unsigned long long t0 = globaltimer_ns();
-                                    while (*epilogues < 8 * r && !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
+                                    ok = table_free(r);
                                     for (int k = lane; k < D; k += 32) mine[k] = 0x7fffffff;
                                     __syncwarp();
                                     if (lane == 0) bad_tag[cw] = r;
@@ -1037,9 +1050,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                         }
                         if (__any_sync(0xffffffffu, hit != 0)) {             // rare
                             if (bad_tag[fw] != r) {          // (warp-uniform: this warp alone writes it)
-                                // the softmax warps read the table in their epilogues: those of earlier items first
-                                const unsigned long long t0 = globaltimer_ns();
-                                while (*epilogues < 8 * r && !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
+                                ok = table_free(r);
                                 for (int k = lane; k < 2 * D; k += 32) mine[k] = 0x7fffffff;
                                 __syncwarp();
                                 if (lane == 0) bad_tag[fw] = r;
@@ -1333,6 +1344,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                             }
                         }
                     }
+                    __threadfence_block();                   // (the table is read)
                 }
                 tc::fence_before_sync();
             } else if (has && !split) {                      // rows that see nothing
@@ -1342,7 +1354,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             }
             if (split && has) a.part_ml[slot * a.part_rows + myrow] = make_float2(m_ref, l);
             __syncwarp();
-            if (lane == 0) atomicAdd(const_cast<int*>(epilogues), 1);
+            if (lane == 0) epilogues[warp] = r + 1;
         }
         if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
     }

@@ -103,3 +103,29 @@ def test_nan_scores_beside_infinite_values(split):
     blk, at = slot(b, 0, total - 1)
     b.vc[blk, at, 0, 9] = math.inf
     assert torch.isnan(run(b)).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16_d64", "e4m3"])
+@pytest.mark.parametrize("news", [1, 200])
+def test_items_in_a_row_that_all_hold_some(news, kind):
+    """Several work items a CTA, one after another, each with an infinite (E4M3: NaN) value that its last tokens see:
+    every row has its own sequence's, in its own columns, and no other."""
+    e4m3 = kind == "e4m3"
+    dim, dtype = (64, "f16") if kind == "f16_d64" else (128, "bf16")
+    B = 300 if news == 1 else 60
+    totals = [news + (37 * s) % 290 for s in range(B)]
+    b = build([news] * B, totals, 8, 8, dim, 16, dtype, seed=9, e4m3=e4m3)
+    clean = run(b)
+    want = clean.clone()
+    bad = math.nan if e4m3 else math.inf
+    for s in range(B):
+        for back in {0, news // 3, news - 1}:
+            blk, at = slot(b, s, totals[s] - 1 - back)
+            col = (5 * s + 7 * back) % dim
+            b.vc[blk, at, :, col] = 0x7f if e4m3 else bad
+            want[news * (s + 1) - 1 - back:news * (s + 1), :, col] = bad
+    for _ in range(3):
+        got = run(b)
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        keep = ~torch.isnan(want)
+        assert torch.equal(got[keep], want[keep])
