@@ -343,8 +343,8 @@ PKV_API pkv_status pkv_paged_attention_verify(void* out, const void* q, const vo
  * t < seq_lens[s] - n_s + i + 1:
  *     z_t = scale * <q[r][h], K_t>,  out[r][h] = sum_t softmax(z)_t * V_t,
  * r = query_starts[s] + i, K and V those of KV head h / (num_heads /
- * num_kv_heads).  A token that sees no position gets zeros.  Accumulation and
- * softmax statistics are fp32; the weights are rounded to `dt` for the product
+ * num_kv_heads).  A token that sees no position gets zeros, one all of whose
+ * scores are -inf NaN.  Accumulation and softmax statistics are fp32; the weights are rounded to `dt` for the product
  * with V, `out` is rounded to nearest even.  What the cache holds at positions
  * that a token does not see (infinities and NaN too) does not reach its
  * output.

@@ -1264,7 +1264,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 if (!ok) break;
                 tc::fence_after_sync();
                 const float vs = KV8 ? __ldcg(a.v_scale + it.kvh) : 1.0f;
-                const float inv = l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l;                  // (a NaN sum stays)
+                // (no weight: zeros for a row that sees nothing, NaN where every score it sees is -inf; a NaN sum stays)
+                const float inv = l > 0.0f ? vs / l : l == 0.0f ? (lim > 0 ? NAN : 0.0f) : l;
                 if (split) {
                     // a row a thread, 16 bytes of 32 neighbouring rows side by side
 #pragma unroll 1
@@ -1352,7 +1353,10 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (split && has) a.part_ml[slot * a.part_rows + myrow] = make_float2(m_ref, l);
+            // (a part whose every score the row sees is -inf: its sum is -1, told from a part it sees nothing of; its weight
+            // in the merge is 2^(-inf - m), 0 beside a part with a finite score and NaN without one)
+            if (split && has)
+                a.part_ml[slot * a.part_rows + myrow] = make_float2(m_ref, l == 0.0f && seen > it.step0 * kStep ? -1.0f : l);
             __syncwarp();
             if (lane == 0) epilogues[warp] = r + 1;
         }

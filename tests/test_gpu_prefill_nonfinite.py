@@ -129,3 +129,45 @@ def test_items_in_a_row_that_all_hold_some(news, kind):
         assert torch.equal(torch.isnan(got), torch.isnan(want))
         keep = ~torch.isnan(want)
         assert torch.equal(got[keep], want[keep])
+
+
+def all_low(b, s, positions):
+    """Keys whose every score is -inf: K = -inf in every column, for the positive queries of these tests."""
+    for pos in positions:
+        blk, at = slot(b, s, pos)
+        b.kc[blk, at] = -math.inf
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_that_are_all_minus_infinity(dim):
+    """A token all of whose scores are -inf has no defined softmax: NaN, as the definition gives it.  Tokens with a
+    finite score weigh the others 0; tokens that see nothing still get zeros."""
+    b = build([6, 5, 300, 9], [6, 40, 700, 4], 4, 2, dim, 16, "bf16", seed=6)
+    b.q.copy_(b.q.abs().clamp(min=0.25))
+    all_low(b, 0, range(3))                             # its first three tokens see nothing else
+    all_low(b, 1, range(40))                            # every token
+    all_low(b, 2, range(0, 700, 3))
+    got, want = run(b), definition(b)
+    same_kind(got, want)
+    assert torch.isnan(got[:3]).all() and torch.isnan(got[6:11]).all()
+    assert torch.isfinite(got[3:6]).all() and torch.isfinite(got[11:311]).all() and (got[311:316] == 0).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_that_are_all_minus_infinity_over_a_long_cache(dim):
+    """The same through the merge of a split tile's parts: every part without a finite score, and all but one."""
+    for finite in (None, 17, 4000, 5995):
+        b = build([3], [6000], 4, 1, dim, 16, "bf16", seed=7)
+        b.q.copy_(b.q.abs().clamp(min=0.25))
+        keep = b.kc.clone()
+        all_low(b, 0, range(6000))
+        if finite is not None:
+            blk, at = slot(b, 0, finite)
+            b.kc[blk, at] = keep[blk, at]
+            v = b.vc[blk, at, 0].double()
+        got = run(b)
+        if finite is None:
+            assert torch.isnan(got).all()
+        else:
+            # one weight of 1, the others 0: the value itself
+            assert (got.double() == v).all()
