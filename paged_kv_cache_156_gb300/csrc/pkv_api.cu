@@ -712,8 +712,9 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     a.num_blocks = num_blocks;
     a.err = error_word(current_device());
-    // (a zero scale becomes one that no finite score survives, so that a masked score, -inf, stays -inf)
-    a.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-30f);
+    // (a zero scale becomes the least positive number, 2^-149: a masked score, -inf, stays -inf, every finite one, below
+    // 2^128, becomes less than 2^-20)
+    a.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-149f);
     a.negate_q = scale < 0.0f;
     a.q_tma = pkv::kPrefillSub % a.group == 0;
     CUtensorMap tmq{}, tmk{}, tmv{};

@@ -1110,7 +1110,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             float sl2 = a.scale_log2;
             if (KV8) {
                 sl2 *= __ldcg(a.k_scale + it.kvh);
-                if (sl2 == 0.0f) sl2 = 1e-38f;               // (a masked score, -inf, stays -inf)
+                if (sl2 == 0.0f) sl2 = 0x1p-149f;            // (a masked score, -inf, stays -inf)
             }
             const uint64_t sl2x2 = pack64(sl2, sl2);
             if constexpr (kConvertQ) {
