@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             // hundred instructions a step between the softmax warps' thousands on the same schedulers, so
             // nearly every instruction line is fetched anew; with a warp for each tile one's waits and
             // bookkeeping run beside the other's products.
-            const uint32_t kIdS = tc::idesc_f16(kSub, kStep, kBf16, false) | (a.negate_q ? 1u << 13 : 0u);   // S = Q K^T, -Q K^T
+            const uint32_t kIdS = tc::idesc_f16(kSub, kStep, kBf16, false) | (a.negate_q ? tc::kNegateA : 0u);
             constexpr uint32_t kIdO = tc::idesc_f16(kSub, D, kBf16, true);        // O += P V
             const int i = warp != G::kMma;
             const uint64_t dq = tc::smem_desc_sw128(smem_u32(smem) + i * G::kTile, 16, 1024);
@@ -797,6 +797,9 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             auto wait = [&](uint64_t* bar, unsigned parity) { return wait_bar(bar, parity, abort_flag); };
             for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps(), ni = it.steps_of(i);
+                // S = Q K^T, or -Q K^T where scale and K's scale together are negative (the softmax takes their magnitude)
+                uint32_t id_s = kIdS;
+                if (KV8 && __ldcg(a.k_scale + it.kvh) < 0.0f) id_s ^= tc::kNegateA;
                 // round j: O += P V of step j, then S of step j + 1 (round -1: the first S alone)
 #pragma unroll 1
                 for (int j = -1; j < n; ++j) {
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
                             const uint64_t off = ((ks >> 2) * G::kPlane + (ks & 3) * 32) >> 4;
-                            tc::mma_ss(ts, dq + off, d + off, kIdS, ks > 0);
+                            tc::mma_ss(ts, dq + off, d + off, id_s, ks > 0);
                         }
                         tc::commit(&s_full[i]);
                         if (j + 2 == ni) tc::commit(&q_empty[i]);
@@ -1109,7 +1112,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             float m_ref = -INFINITY, l = 0.0f;
             float sl2 = a.scale_log2;
             if (KV8) {
-                sl2 *= __ldcg(a.k_scale + it.kvh);
+                sl2 *= fabsf(__ldcg(a.k_scale + it.kvh));
                 if (sl2 == 0.0f) sl2 = 0x1p-149f;            // (a masked score, -inf, stays -inf)
             }
             const uint64_t sl2x2 = pack64(sl2, sl2);

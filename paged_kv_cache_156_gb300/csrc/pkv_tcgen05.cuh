@@ -50,6 +50,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+constexpr uint32_t kNegateA = 1u << 13;             // (in the descriptor: -A B)
+
 // ---------------------------------------------------------------- MMA (one thread)
 // D[tmem] (+)= A[tmem] * B[smem], accumulate when `acc` is non-zero.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {

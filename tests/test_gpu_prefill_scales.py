@@ -37,3 +37,14 @@ def test_large_scores_and_a_small_scale(scale, total):
     b.kc *= 2.0 ** 60
     ref, bound = reference(b)
     check(run(b), ref, bound)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [None, -0.1])
+def test_e4m3_scales_of_either_sign(dtype, scale):
+    """K = code * k_scale[g] for a negative k_scale[g] too, as in the decode call."""
+    b = build([40, 1, 260, 9], [40, 700, 300, 6000], 8, 4, 128, 16, dtype, seed=22, scale=scale, e4m3=True)
+    b.k_scale *= torch.tensor([1.0, -1.0, 1.0, -2.0])
+    b.v_scale *= torch.tensor([1.0, 1.0, -1.0, -1.0])
+    ref, bound = reference(b, torch.float16)
+    check(run(b), ref, bound)
