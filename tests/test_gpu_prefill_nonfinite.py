@@ -171,3 +171,19 @@ def test_scores_that_are_all_minus_infinity_over_a_long_cache(dim):
         else:
             # one weight of 1, the others 0: the value itself
             assert (got.double() == v).all()
+
+
+@pytest.mark.parametrize("total", [600, 6000])
+def test_an_infinite_value_of_a_vanishing_weight(total):
+    """A weight that 16 bits or fp32 round to zero: the column is an infinity or NaN, never a number."""
+    b = build([20], [total], 4, 1, 64, 16, "f16", seed=8)
+    b.q.copy_(b.q.abs().clamp(min=0.25))
+    for pos, key, col in ((50, -8.0, 3), (51, -200.0, 4), (total - 3, -8.0, 5), (total - 1, -200.0, 6)):
+        blk, at = slot(b, 0, pos)
+        b.kc[blk, at] = key
+        b.vc[blk, at, 0, col] = math.inf
+    got = run(b)
+    assert not torch.isfinite(got[:, :, 3:5]).any()
+    assert not torch.isfinite(got[18:, :, 5]).any() and not torch.isfinite(got[19, :, 6]).any()
+    assert torch.isfinite(got[:17, :, 5]).all() and torch.isfinite(got[:19, :, 6]).all()
+    assert torch.isfinite(got[:, :, 7:]).all() and torch.isfinite(got[:, :, :3]).all()

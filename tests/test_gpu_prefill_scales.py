@@ -48,3 +48,14 @@ def test_e4m3_scales_of_either_sign(dtype, scale):
     b.v_scale *= torch.tensor([1.0, 1.0, -1.0, -1.0])
     ref, bound = reference(b, torch.float16)
     check(run(b), ref, bound)
+
+
+def test_e4m3_bf16_queries_up_to_the_end_of_f16():
+    """A bf16 query is converted to f16: exact between 2^-14 and 65504 in magnitude (65280 is bf16's last there)."""
+    b = build([40, 1], [200, 700], 8, 4, 128, 16, "bf16", seed=23, e4m3=True)
+    b.q[:, :, ::2] = 2.0 ** -14
+    b.q[:, :, 1::16] = 65280.0
+    b.q[:, :, 9::16] = -65280.0
+    b.k_scale *= 2.0 ** -18
+    ref, bound = reference(b, torch.float16)
+    check(run(b), ref, bound)
