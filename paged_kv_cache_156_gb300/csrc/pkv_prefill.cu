@@ -1361,7 +1361,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             if (split && has)
                 a.part_ml[slot * a.part_rows + myrow] = make_float2(m_ref, l == 0.0f && seen > it.step0 * kStep ? -1.0f : l);
             __syncwarp();
-            if (lane == 0) epilogues[warp] = r + 1;
+            if (lane == 0) atomicAdd(const_cast<int*>(epilogues) + warp, 1);
         }
         if (!ok && lane == 0) dec::raise_abort(a.err, abort_flag);
     }
