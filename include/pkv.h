@@ -347,10 +347,13 @@ PKV_API pkv_status pkv_paged_attention_verify(void* out, const void* q, const vo
  * scores are -inf NaN.  Accumulation and softmax statistics are fp32; the weights are rounded to `dt` for the product
  * with V, `out` is rounded to nearest even.  What the cache holds at positions
  * that a token does not see (infinities and NaN too) does not reach its
- * output.
+ * output; an infinity or NaN of V at a position it does see makes its column
+ * what the sum gives, except that a weight which 16 bits round to zero may
+ * give NaN in an infinity's place.
  *
- *   out, q        [num_tokens][num_heads][head_dim], dtype `dt`; rows that no
- *                 sequence owns are neither read nor written
+ *   out, q        [num_tokens][num_heads][head_dim], dtype `dt`; rows of out that
+ *                 no sequence owns are not written, such rows of q may be read
+ *                 but reach no output
  *   seq_lens      int32 [num_seqs]: positions cached, the new tokens among
  *                 them, each in [0, max_seq_len] (a larger length is treated as
  *                 max_seq_len and raises the error word's bounds bit)
@@ -364,9 +367,10 @@ PKV_API pkv_status pkv_paged_attention_verify(void* out, const void* q, const vo
  *                 pkv_prefill_plan wrote into `workspace` (once per step, for
  *                 every layer): the same seq_lens and query_starts contents
  *                 and the same num_seqs, num_tokens, max_seq_len, num_heads,
- *                 num_kv_heads and head_dim (not checked on the host; a plan
- *                 that does not fit the arguments gives undefined outputs and
- *                 raises the bounds bit, but never leaves the buffers)
+ *                 num_kv_heads and head_dim (not checked on the host; under
+ *                 another batch's plan the outputs are undefined, entries that
+ *                 do not fit the arguments are skipped and raise the bounds
+ *                 bit, and no access leaves the buffers)
  *   block_tables, max_blocks_per_seq, max_seq_len, block_size, num_blocks and
  *   the pools as for pkv_paged_attention_decode
  * head_dim in {64, 128}; block_size in {8, 16, 32}; num_heads a multiple of
@@ -449,9 +453,12 @@ PKV_API pkv_status pkv_paged_attention_verify_fp8(void* out, const void* q, cons
 
 /*
  * pkv_paged_attention_prefill_fp8: pkv_paged_attention_prefill over uint8 E4M3
- * pools, with K and V as in pkv_paged_attention_decode_fp8 (the products run in
- * f16, where every code is exact; a bf16 query is converted to f16).  head_dim
- * 128 only; the same plan and workspace as the 16-bit call.
+ * pools, with K and V as in pkv_paged_attention_decode_fp8; scales of zero or
+ * below are taken as they are.  The products run in f16, where every code is
+ * exact; a bf16 query is converted to f16: exact from 2^-14 to 65504 in
+ * magnitude, rounded to a multiple of 2^-24 below, infinite (the row NaN)
+ * above, which is not supported.  The weights are rounded to f16.  head_dim 128
+ * only; the same plan and workspace as the 16-bit call.
  */
 PKV_API pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void* key_cache,
                                            const void* value_cache, const int32_t* block_tables,

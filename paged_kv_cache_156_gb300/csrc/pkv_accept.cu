@@ -10,21 +10,27 @@
 //
 // The draw is the inverse of the cumulative sum, and the answer is a whole
 // number, so the sum must not depend on its order.  Each weight is therefore
-// cut to whole units of 2^-44 (fp32 times 2^44 is exact; what is cut off a row
-// of 2^18 tokens is below 2^-26 of it, less than the rounding of the
-// probabilities themselves) and summed in 64-bit integers: with T the total,
-// the token is the first whose inclusive sum exceeds floor(u T).
+// cut to whole units of 2^-44 (fp32 times 2^44 is exact) and summed in 64-bit
+// integers: with T the total, the token is the first whose inclusive sum exceeds
+// floor(u T).  What is cut off a row is below 2^-44 a token, 2^-25 at the largest
+// vocabulary, of a target row that sums to 1.  Of a residual max(p - q, 0) that
+// sums to R it may be a larger share, up to all of it (the target's own row is
+// then drawn from), but a refusal is itself only as likely as R: a token's
+// probability over both stays within 2^-25.
 //
 // One cluster a sequence: its CTAs take a contiguous piece of the row each, a
 // warp a contiguous piece of that, so the row is read once; totals go round
 // through distributed shared memory.  Every lane keeps its sum of each batch of
 // 512 weights in shared memory, so the warp that holds the mark finds the batch
 // from there and reads those 512 weights again.  (Weights held in registers
-// instead spilled at two CTAs an SM: 36 us for 64 sequences of 128000 tokens.)
+// instead spilled at two CTAs an SM: 36 us for 64 sequences of 128000 tokens.
+// The float32 form still spills 44 bytes a thread at its 64 registers.)
 // Bound by latency: at a few sequences by dependent loads (draft token, its
-// probabilities, the row: 5.5 us for one of 32000 tokens), at many by those and
-// the exchange (64 sequences of 128000 float32: 10.1 us, of which the rows, 41 MB,
-// take 5.1; a prefetch of the pieces into L2 ahead of the loop made it 11.6).
+// probabilities, the row: 5.1 us for one of 32000 tokens), at many by those and
+// the exchange (64 sequences of 128000 float32, 41 MB read: 9.8 us with the rows
+// in L2 from the call before, of which they take 5; 12.0 us with the rows in HBM,
+// 50% of the copy rate.  A prefetch of the pieces into L2 ahead of the loop made
+// the first of these 11.6).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -16,8 +16,11 @@
 //     P_i = 2^(S_i - ref)   one thread a row; the reference maximum moves only
 //                      when a score passes it by more than 2^8 (O_i is then
 //                      rescaled in TMEM); P_i, rounded to the input type (the
-//                      MMA's operand type), takes S_i's place in TMEM; the row
-//                      sum stays fp32 and sums the weights before rounding
+//                      MMA's operand type, the price of its rate: bf16 outputs
+//                      are 2.3e-3 from 64 bits where a form in fp32, rounded
+//                      once, is 1.7e-3; f16 2.5e-4 and 1.9e-4), takes S_i's
+//                      place in TMEM; the row sum stays fp32 and sums the
+//                      weights before rounding
 //     O_i += P_i V     tcgen05.mma, A from TMEM, V from shared memory read as an
 //                      MN-major operand, O_i fp32 in TMEM
 // The two tiles are a step's ping and pong: while one tile's softmax runs, the
@@ -29,13 +32,16 @@
 // What bounds it.  A step of two tiles is 2048 tensor cycles at head_dim 128 and
 // takes 2650 to 2850: a tile's S, softmax, P V and next S are a serial chain, under
 // which only the other tile's products run.  One prompt of 8192 tokens, 64 heads
-// over 8: 683 us, 1610 TFLOP/s; of 16384: 1670 TFLOP/s, 87% of the rate measured
-// for a large bf16 matrix product.  Start-up takes 7 us without a plan, 9 with one
+// over 8: 690 us, 1590 TFLOP/s, 83% of the rate measured for a large bf16 matrix
+// product, in the first milliseconds; 754 us, 1460 TFLOP/s, once the power cap
+// holds the clock down, 86% of that product's own rate then.  Start-up takes 7 us without a plan, 9 with one
 // (plan 3 to 4, first S 5, second 1.6: latencies and instruction fetch), and the
 // items' ends spread by a tenth of a call.  Tiles of up to 128 rows compute half as
 // much over the same K and V: where all CTAs run such, a step takes 1.41 us, the HBM
-// rate.  At head_dim 64 the exponentials, as many for half the products, come first:
-// 990 TFLOP/s over 16384 tokens, 16 heads over 4.
+// rate.  At head_dim 64 there are as many exponentials for half the products: 950 to
+// 990 TFLOP/s over 16384 tokens, 16 heads over 4.  No unit is the bound there either
+// (8192 tokens: tensor pipe 40% busy, exponentials' unit 40%, issue slots 52%): the
+// softmax is two warps a scheduler, waiting for TMEM and for each other.
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (they also write the output),
 // 13 loads Q tiles, 8 and 10 stream the K and V blocks (TMA, one
@@ -48,14 +54,15 @@
 // not finite, so on the steps that some row sees only in part, and on a
 // sequence's last, two warps look through the V rows that not every row sees:
 // slots past the end become zeros, non-finite elements too, after their first
-// position per column is noted; the epilogue then gives inf or NaN to exactly
+// position per column is noted; the epilogue then adds inf or NaN to exactly
 // the rows that see them.
 //
 // E4M3 pools.  Warp 8 streams tiles of codes, and three warps (10, 12, 13: one a scheduler) expand
 // them into the ring as f16, where every code is exact, and clean V on the way;
 // K's scale multiplies the scores, V's the output.  The products run in f16: a
 // bf16 query tile is converted in place by its softmax warps.  A step takes 1.7 us
-// (1.45 over 16-bit pools): the conversion shares the issue slots with the softmax.
+// (1.45 over 16-bit pools), which the three warps' expansion sets: 16 groups of eight
+// rows, two a warp at a time, are three trips (issue slots 45%, tensor pipe 48% busy).
 //
 // Every wait is bounded in wall time; a CTA that gives up raises the error
 // word, gives its copies and products in flight time to land and frees its TMEM.
@@ -1376,7 +1383,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 
 // The split tiles' parts merged: 32 rows by 64 columns a CTA, a row a lane, its columns over the warps.
 //     m = max_p m_p,  out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
-// summed in part order.  A kernel of its own, since the merge of a 256-row tile is a megabyte of reads:
+// summed in part order.  Launched for every call whose plan may split, since the host does not know whether it did
+// (without a split tile its CTAs end at once).  A kernel of its own, since the merge of a 256-row tile is a megabyte of reads:
 // by the last CTA to finish it took 70 us of a 177 us call (33 tokens x 64 heads over 65549 positions).
 // Bound by latency: the next call waits for the last of these CTAs.  So the parts' weights are found first, a part a
 // warp, and kept in shared memory; then every load of the partial outputs is independent of the others, 16 in flight

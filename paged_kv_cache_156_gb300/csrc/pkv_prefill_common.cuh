@@ -87,7 +87,8 @@ struct Choice {
 //     the largest item                        otherwise
 //
 // (the first line is the average load plus the expected overhang of a longest-first schedule).  Tiles are not split
-// when there are many for every SM, nor when the longest is well below what every CTA has to do anyway.
+// when there are many for every SM (8 and more: one much longer than the rest then keeps its KV heads' CTAs after the
+// others are done), nor when the longest is well below what every CTA has to do anyway.
 template <int WARPS>
 __device__ __forceinline__ int choose_part(const PrefillArgs& a, Choice& ch, const int* steps, int tiles, int maxs, float sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

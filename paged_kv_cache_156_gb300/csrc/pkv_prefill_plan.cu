@@ -197,7 +197,8 @@ PrefillWorkspace prefill_workspace_layout(int num_seqs, int64_t num_tokens, int 
     auto pad = [](size_t x) { return (x + 255) / 256 * 256; };
     const int64_t rows = num_tokens * (num_heads / num_kv_heads);
     w.part_rows = static_cast<int>((std::min<int64_t>(kPrefillRows, std::max<int64_t>(rows, 1)) + 31) / 32 * 32);
-    // two parts for every CTA, and one tile split as far as it goes
+    // two parts for every CTA over all KV heads, at least 16 a head: what a KV head's split tiles share, and so the most
+    // parts of one tile too
     w.part_cap = std::max((2 * slots + num_kv_heads - 1) / num_kv_heads, 16);
     w.capacity = static_cast<int>(rows / kPrefillRows + std::min<int64_t>(num_seqs, rows) + w.part_cap);
     const size_t parts = static_cast<size_t>(num_kv_heads) * w.part_cap;
