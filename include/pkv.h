@@ -95,6 +95,49 @@ PKV_API pkv_status pkv_paged_kv_append(const void* k, const void* v, void* key_c
                                void* stream);
 
 /*
+ * paged_kv_append_rotary -- pkv_paged_kv_append with the position rotation of
+ * queries and keys on the way.
+ *
+ * P2 §2.3 and P1 §4.2.2, as pkv_paged_kv_append; the pages leave the position
+ * encoding to the model.  A head's first rotary_dim elements are pairs,
+ * (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with `interleaved`, i < rotary_dim
+ * / 2.  With c = cos_sin[p][i] and s = cos_sin[p][rotary_dim / 2 + i], p the
+ * token's position,
+ *     turned(x, y) = (x c - y s, y c + x s);
+ * the head's other elements stay as they are.  For every token t:
+ *     q_out[t] = turned(q[t]);
+ *     cache rows of slot_mapping[t]:  K = turned(k[t]),  V = v[t]
+ * Products and sums are rounded to fp32 one by one, the result once to its own
+ * type (to E4M3 pools as pkv_paged_kv_append_fp8 does, from fp32).
+ *
+ *   q_out, q      [num_tokens][num_heads][head_dim], dtype `dt`; q_out may be q.
+ *                 num_heads 0: no queries (both ignored)
+ *   k, v          [num_tokens][num_kv_heads][head_dim], dtype `dt`
+ *   *_stride      elements from a token's row to the next (rows may be views of
+ *                 a packed projection): multiples of 8, at least a row
+ *   slot_mapping  int64 [num_tokens], distinct; a negative slot writes nothing
+ *                 to the caches (q_out is written all the same), one outside the
+ *                 pool too, which raises the error word's bounds bit
+ *   positions     int32 [num_tokens], each in [0, num_positions); any other
+ *                 leaves the token out (no q_out, no cache row) and raises the
+ *                 bounds bit, except a negative one beside a negative slot:
+ *                 padding
+ *   cos_sin       float32 [num_positions][rotary_dim]: a row's cosines, then its
+ *                 sines
+ *   kv_dt         dt for 16-bit pools, PKV_E4M3 for 8-bit pools (then k_scale and
+ *                 v_scale as in pkv_paged_kv_append_fp8, else ignored)
+ * Any block_size; head_dim a multiple of 16 up to 4096, rotary_dim a multiple of
+ * 16 up to head_dim; up to 4096 heads.  q_out overlaps no other argument but q.
+ */
+PKV_API pkv_status pkv_paged_kv_append_rotary(void* q_out, const void* q, const void* k, const void* v, void* key_cache,
+                                      void* value_cache, const int64_t* slot_mapping, const int32_t* positions,
+                                      const float* cos_sin, int64_t num_tokens, int64_t q_out_stride,
+                                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int num_positions,
+                                      int rotary_dim, int interleaved, int64_t num_blocks, int block_size,
+                                      int num_heads, int num_kv_heads, int head_dim, pkv_dtype dt, pkv_dtype kv_dt,
+                                      const float* k_scale, const float* v_scale, void* stream);
+
+/*
  * Workspace for pkv_paged_attention_decode: bytes needed for its
  * per-(sequence, head group) merge tickets, its work list and the split-K
  * partials (never 0).  partition_tokens: 0 sizes it for the smallest
@@ -470,6 +513,40 @@ PKV_API pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, con
                                            size_t workspace_bytes, int planned, void* stream);
 
 /*
+ * paged_attention_tree -- the attention of drafted trees over the paged cache.
+ *
+ * P1 §4.4.2 and P3 §4.2 (the target scores every drafted token in one pass), for
+ * drafts that branch: sequence s has n_s = query_starts[s+1] - query_starts[s]
+ * nodes, whose K and V are already in its blocks as its last n_s positions, in
+ * the order of its rows of q, each after its ancestors.  With base =
+ * seq_lens[s] - n_s, node i attends over all positions t < base and over
+ * position base + j for every bit j <= i of tree_mask[query_starts[s] + i]
+ * (usually its ancestors' and its own; bits above i, and bits of positions below
+ * 0, count for nothing), otherwise exactly as pkv_paged_attention_prefill, of
+ * which it is the form with tree_mask[..] = all ones.  A node that sees no
+ * position gets zeros.  What the cache holds at positions that a node does not
+ * see, infinities and NaN too, does not reach its output.
+ *
+ *   n_s           up to PKV_TREE_MAX_NODES (a sequence with more raises the error
+ *                 word's bounds bit, its rows of out are undefined)
+ *   tree_mask     uint64 [num_tokens]
+ *   kv_dt         dt for 16-bit pools, PKV_E4M3 for 8-bit pools (head_dim 128;
+ *                 then k_scale and v_scale, and the query's range, as in
+ *                 pkv_paged_attention_prefill_fp8; else ignored)
+ *   workspace     pkv_prefill_workspace_bytes(...) bytes; planned: 0, or
+ *                 PKV_PLANNED over the plan of pkv_prefill_plan
+ *   other arguments as pkv_paged_attention_prefill
+ */
+#define PKV_TREE_MAX_NODES 64
+PKV_API pkv_status pkv_paged_attention_tree(void* out, const void* q, const void* key_cache, const void* value_cache,
+                                    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                    const int32_t* query_starts, const uint64_t* tree_mask, int num_seqs,
+                                    int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads,
+                                    int head_dim, int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
+                                    pkv_dtype kv_dt, const float* k_scale, const float* v_scale, void* workspace,
+                                    size_t workspace_bytes, int planned, void* stream);
+
+/*
  * paged_kv_gather -- a batch's cached K/V read back into dense rows.
  *
  * The inverse of the slot writes (P2 §2.3), through the same block tables
@@ -542,6 +619,81 @@ PKV_API pkv_status pkv_speculative_accept(int64_t* tokens, int32_t* num_accepted
                                   const int32_t* num_drafts, const void* target_probs, const void* draft_probs,
                                   const float* uniform, int num_seqs, int max_drafts, int64_t vocab, pkv_dtype dt,
                                   void* stream);
+
+/*
+ * speculative_accept_tree -- the path through a drafted tree that follows the
+ * target's distribution, and the token that follows it.
+ *
+ * P3 §4.2 (speculative_verify), P1 §4.4.2, for drafts that branch.  Sequence s's
+ * nodes are rows query_starts[s] .. query_starts[s+1] - 1, as in
+ * pkv_paged_attention_tree; node 0, the root, is its last token, and row r of
+ * target_probs the target's probabilities of node r's successor.  From the root
+ * on, at node i of row r:
+ *     y = the first token whose inclusive sum of target_probs[r] exceeds
+ *         uniform[r] times their total
+ *     if a child of i drafted y (the first such), go on there, else stop
+ * so every token is a draw from the target's own distribution.  With a nodes
+ * gone to after the root:
+ *     path[s] = 0, those nodes, then -1;  num_accepted[s] = a
+ *     tokens[s] = those nodes' tokens, the last y, then -1
+ * The walk stops after width - 1 nodes at the latest.  The sums are exact, in the
+ * units of pkv_speculative_accept; a row that sums to nothing gives y = -1 and
+ * stops the walk.  A sequence without nodes gives -1 throughout and a = 0.
+ *
+ *   tokens        int64 [num_seqs][width]
+ *   path          int32 [num_seqs][width]
+ *   num_accepted  int32 [num_seqs]
+ *   draft_tokens  int64 [num_tokens] (a root's is not looked at; a token outside
+ *                 [0, vocab) is never drawn)
+ *   parents       int32 [num_tokens]: the parent's index within its sequence,
+ *                 before the node (a root's is not looked at; any other raises
+ *                 the error word's bounds bit, and the node is nobody's child)
+ *   query_starts  int32 [num_seqs + 1] in [0, num_tokens], not decreasing, at
+ *                 most PKV_TREE_MAX_NODES apart (a sequence whose pair is not
+ *                 raises the bounds bit and counts as one without nodes)
+ *   target_probs  [num_tokens][vocab], dtype `dt` (PKV_F32, PKV_F16 or PKV_BF16)
+ *   uniform       float32 [num_tokens] in [0, 1)
+ * vocab up to PKV_ACCEPT_MAX_VOCAB; width in [1, 1024].
+ */
+PKV_API pkv_status pkv_speculative_accept_tree(int64_t* tokens, int32_t* path, int32_t* num_accepted,
+                                       const int64_t* draft_tokens, const int32_t* parents,
+                                       const int32_t* query_starts, const void* target_probs, const float* uniform,
+                                       int num_seqs, int64_t num_tokens, int width, int64_t vocab, pkv_dtype dt,
+                                       void* stream);
+
+/*
+ * paged_kv_keep_path -- the cache after a tree step: the accepted path's rows
+ * moved to the places a sequence without branches has.
+ *
+ * P2 §5.2 (the candidates' K/V live in the same blocks).  With n_s and base as in
+ * pkv_paged_attention_tree and a = num_accepted[s], for i = 0 .. a and every
+ * layer's K and V pool:
+ *     row of position base + i = row of position base + path[s][i] before the call,
+ * bit for bit (an E4M3 pool's codes).  The sequence then has base + a + 1
+ * positions; the rows after them hold what they held or a copy.
+ *
+ *   key_caches, value_caches  HOST arrays of num_layers device pointers, each a
+ *                 pool [num_blocks][block_size][num_kv_heads][head_dim], all
+ *                 different; a row's bytes a multiple of 16
+ *   seq_lens      int32 [num_seqs]: the lengths with all nodes, as the attention
+ *                 had them
+ *   query_starts  int32 [num_seqs + 1]; only differences are used
+ *   path          int32 [num_seqs][width], 0 = path[s][0] < path[s][1] < ..
+ *                 < path[s][a] < n_s (what follows is not read)
+ *   num_accepted  int32 [num_seqs]
+ *   dt            the pools' element type (PKV_F16, PKV_BF16 or PKV_E4M3)
+ * The blocks of the nodes' positions are the sequence's own.  A sequence that
+ * breaks one of these conditions, or has more than PKV_TREE_MAX_NODES nodes, is
+ * left as it is and raises the error word's bounds bit; so does a row whose
+ * table entry is out of range.  A sequence without nodes has num_accepted 0.
+ * Any block_size; width in [1, 1024].  num_layers == 0 or num_seqs
+ * == 0 is a no-op.
+ */
+PKV_API pkv_status pkv_paged_kv_keep_path(void* const* key_caches, void* const* value_caches, int num_layers,
+                                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                  const int32_t* query_starts, const int32_t* path, const int32_t* num_accepted,
+                                  int num_seqs, int width, int64_t num_blocks, int block_size, int num_kv_heads,
+                                  int head_dim, pkv_dtype dt, void* stream);
 
 /*
  * copy_blocks -- the copy-on-write block copy at a fork.

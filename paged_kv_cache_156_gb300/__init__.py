@@ -30,6 +30,7 @@ PLANNED = 1                 # PKV_PLANNED: run over the plan an earlier call wro
 _PROB_DT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 3}   # PKV_F32: probabilities only
 _HALF_DTS, _POOL_DTS, _PROB_DTS = tuple(_DT), tuple(_POOL_DT), tuple(_PROB_DT)
 ACCEPT_MAX_VOCAB = 524288   # PKV_ACCEPT_MAX_VOCAB
+TREE_MAX_NODES = 64         # PKV_TREE_MAX_NODES
 INPUTS_READY = 2            # PKV_INPUTS_READY: nothing pending writes the pools, tables, lengths or plan
 
 # every symbol include/pkv.h declares
@@ -42,7 +43,8 @@ ABI_SYMBOLS = ("pkv_version", "pkv_last_error", "pkv_paged_kv_append", "pkv_deco
                "pkv_paged_attention_decode_fp8_planned", "pkv_paged_kv_append_decode",
                "pkv_paged_attention_verify_fp8", "pkv_prefill_workspace_bytes", "pkv_prefill_plan",
                "pkv_paged_attention_prefill", "pkv_paged_attention_prefill_fp8", "pkv_paged_kv_gather",
-               "pkv_paged_kv_gather_fp8", "pkv_speculative_accept")
+               "pkv_paged_kv_gather_fp8", "pkv_speculative_accept", "pkv_paged_kv_append_rotary",
+               "pkv_paged_attention_tree", "pkv_speculative_accept_tree", "pkv_paged_kv_keep_path")
 
 _lib = None
 
@@ -118,6 +120,17 @@ def load() -> ctypes.CDLL:
                                             c_i, c_p, c_p, c_p]
     lib.pkv_speculative_accept.restype = c_i
     lib.pkv_speculative_accept.argtypes = [c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_i, c_i, c_i64, c_i, c_p]
+    lib.pkv_paged_kv_append_rotary.restype = c_i
+    lib.pkv_paged_kv_append_rotary.argtypes = [c_p] * 9 + [c_i64] * 5 + [c_i, c_i, c_i, c_i64, c_i, c_i, c_i, c_i, c_i, c_i,
+                                                                         c_p, c_p, c_p]
+    lib.pkv_paged_attention_tree.restype = c_i
+    lib.pkv_paged_attention_tree.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i, c_p, c_p, c_p, c_i, c_i64, c_i, c_i, c_i, c_i, c_i,
+                                             c_i64, c_f, c_i, c_i, c_p, c_p, c_p, c_sz, c_i, c_p]
+    lib.pkv_speculative_accept_tree.restype = c_i
+    lib.pkv_speculative_accept_tree.argtypes = [c_p] * 8 + [c_i, c_i64, c_i, c_i64, c_i, c_p]
+    lib.pkv_paged_kv_keep_path.restype = c_i
+    lib.pkv_paged_kv_keep_path.argtypes = [ctypes.POINTER(c_p), ctypes.POINTER(c_p), c_i, c_p, c_i, c_p, c_p, c_p, c_p, c_i,
+                                           c_i, c_i64, c_i, c_i, c_i, c_i, c_p]
     lib.pkv_copy_blocks.restype = c_i
     lib.pkv_copy_blocks.argtypes = [ctypes.POINTER(c_p), ctypes.POINTER(c_p), c_i, c_p, c_i64, c_i64, c_i, c_i,
                                     c_i, c_i, c_p]
@@ -248,6 +261,77 @@ def paged_kv_append(k, v, key_cache, value_cache, slot_mapping) -> None:
     if tuple(k.shape) != (T, Hkv, d) or tuple(v.shape) != (T, Hkv, d) or slot_mapping.shape[0] != T:
         raise ValueError("k, v must be [T, num_kv_heads, head_dim] and slot_mapping [T]")
     _check(load().pkv_paged_kv_append(*args, T, NB, bs, Hkv, d, _DT[key_cache.dtype], _stream(key_cache)))
+
+
+def _rows_stride(name, t, dtypes, heads, dim):
+    """Rows of [heads, dim] whose elements are dense, a stride of elements apart (views of a packed projection)."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtypes}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [num_tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: a token's row must be dense")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def paged_kv_append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved=False,
+                           k_scale=None, v_scale=None) -> None:
+    """paged_kv_append with the position rotation on the way: q_out = q turned, and K = k turned, V = v in the caches.
+
+    q_out, q [T, Hq, d] (q_out may be q; both None: no queries), k, v [T, Hkv, d]: rows may be a stride apart (views of a
+    packed projection), a multiple of 8 elements.  slot_mapping int64 [T] (< 0: nothing is cached).  positions int32 [T];
+    cos_sin float32 [P, r]: row p holds the cosines, then the sines, of position p's r / 2 angles.  A head's first r
+    elements turn, as pairs (i, i + r / 2), or (2 i, 2 i + 1) when ``interleaved``.  uint8 pools hold E4M3 codes and take
+    k_scale / v_scale (float32 [Hkv]) as paged_kv_append_fp8 does."""
+    args = (q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved, k_scale, v_scale)
+    if _usual(key_cache, value_cache, slot_mapping, positions, cos_sin):
+        dev = key_cache.get_device()
+        for t in (q_out, q, k, v, k_scale, v_scale):
+            if t is not None and (type(t) is not _Tensor or t.get_device() != dev):
+                break
+        else:
+            return _append_rotary(*args)
+    _append_rotary_on_device(*args)
+
+
+def _append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved, k_scale,
+                   v_scale) -> None:
+    dt = key_cache.dtype
+    kc = _cuda("key_cache", key_cache, _POOL_DTS, 4)
+    kv8 = dt is torch.uint8
+    NB, bs, Hkv, d = key_cache.shape
+    if value_cache.shape != key_cache.shape or value_cache.dtype is not dt:
+        raise ValueError("value_cache must match key_cache")
+    if not kv8 and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale / v_scale belong to E4M3 (uint8) pools")
+    ks = _rows_stride("k", k, _HALF_DTS if kv8 else (dt,), Hkv, d)
+    T, own = k.shape[0], (k.dtype,)
+    vs = _rows_stride("v", v, own, Hkv, d)
+    Hq, qo, qi, qos, qis = 0, None, None, 0, 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        if not isinstance(q, _Tensor) or q.dim() != 3:
+            raise ValueError("q must be a tensor [num_tokens, num_heads, head_dim]")
+        Hq = q.shape[1]
+        qis, qos = _rows_stride("q", q, own, Hq, d), _rows_stride("q_out", q_out, own, Hq, d)
+        qo, qi = q_out.data_ptr(), q.data_ptr()
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError("q, q_out, k and v must have the same tokens")
+    vc, sm = _cuda("value_cache", value_cache), _cuda("slot_mapping", slot_mapping, torch.int64, 1)
+    ps, cs = _cuda("positions", positions, torch.int32, 1), _cuda("cos_sin", cos_sin, torch.float32, 2)
+    if v.shape[0] != T or slot_mapping.shape[0] != T or positions.shape[0] != T:
+        raise ValueError("k, v, slot_mapping and positions must have the same tokens")
+    scales = (_scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv)) if kv8 else (None, None)
+    P, r = cos_sin.shape
+    _check(load().pkv_paged_kv_append_rotary(qo, qi, k.data_ptr(), v.data_ptr(), kc, vc, sm, ps, cs, T, qos, qis, ks, vs, P, r,
+                                             1 if interleaved else 0, NB, bs, Hq, Hkv, d, _DT[k.dtype], _POOL_DT[dt],
+                                             *scales, _stream(key_cache)))
+
+
+_append_rotary_on_device = _one_device(_append_rotary)
 
 
 def decode_partition_tokens(num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len) -> int:
@@ -584,6 +668,72 @@ def _prefill(out, q, key_cache, value_cache, block_tables, seq_lens, query_start
                                                   scale, _DT[dt], wp, workspace.nbytes, flags, _stream(q)))
 
 
+def paged_attention_tree(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, tree_mask, scale=None,
+                         max_seq_len=None, workspace=None, planned=False, k_scale=None, v_scale=None) -> None:
+    """Attention of drafted trees over the paged cache.  q, out: [T, Hq, d]; sequence s's nodes (up to 64) are rows
+    query_starts[s] .. query_starts[s + 1] - 1 (int32 [B + 1]), whose K/V are its last n positions in the pools, in that
+    order; node i attends over every position before them and over node j where bit j <= i of its int64 tree_mask entry
+    is set (its ancestors' and its own).  ``workspace``, ``planned``, ``max_seq_len``, E4M3 pools and their scales: as
+    paged_attention_prefill, whose plan it shares."""
+    if _usual(q, out, key_cache, value_cache, block_tables, seq_lens, query_starts, tree_mask, workspace) and \
+            scale is not None and max_seq_len is not None:
+        dt, qdt, pool, rows, table = key_cache.dtype, q.dtype, key_cache.shape, q.shape, block_tables.shape
+        kv8 = dt is torch.uint8
+        if (kv8 or dt is qdt) and qdt in _DT and out.dtype is qdt and value_cache.dtype is dt and \
+                block_tables.dtype is seq_lens.dtype is query_starts.dtype is torch.int32 and len(pool) == 4 and \
+                tree_mask.dtype is torch.int64 and len(rows) == 3 and len(table) == 2 and value_cache.shape == pool and \
+                out.shape == rows and seq_lens.shape == table[:1] and query_starts.shape == (table[0] + 1,) and \
+                rows[2] == pool[3] and tree_mask.shape == rows[:1] and \
+                (k_scale is None and v_scale is None if not kv8 else _usual(q, k_scale, v_scale) and
+                 k_scale.dtype is v_scale.dtype is torch.float32 and k_scale.shape == v_scale.shape == pool[2:3]):
+            return _check(load().pkv_paged_attention_tree(
+                out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(), table[1],
+                seq_lens.data_ptr(), query_starts.data_ptr(), tree_mask.data_ptr(), table[0], rows[0], int(max_seq_len),
+                rows[1], pool[2], pool[3], pool[1], pool[0], float(scale), _DT[qdt], _POOL_DT[dt],
+                k_scale.data_ptr() if kv8 else None, v_scale.data_ptr() if kv8 else None, workspace.data_ptr(),
+                workspace.nbytes, PLANNED if planned else 0, _stream(q)))
+    _tree(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, tree_mask, scale, max_seq_len, workspace,
+          planned, k_scale, v_scale)
+
+
+@_one_device
+def _tree(out, q, key_cache, value_cache, block_tables, seq_lens, query_starts, tree_mask, scale, max_seq_len, workspace,
+          planned, k_scale, v_scale) -> None:
+    dt = key_cache.dtype
+    kv8 = dt is torch.uint8
+    if not kv8 and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale / v_scale belong to E4M3 (uint8) pools")
+    kc = _cuda("key_cache", key_cache, _POOL_DTS, 4)
+    NB, bs, Hkv, d = key_cache.shape
+    if value_cache.shape != key_cache.shape or value_cache.dtype is not dt:
+        raise ValueError("value_cache must match key_cache")
+    qp = _cuda("q", q, _HALF_DTS if kv8 else dt, 3)
+    T, Hq, dq = q.shape
+    if dq != d or out.shape != q.shape:
+        raise ValueError("q and out must be [num_tokens, num_heads, head_dim]")
+    op, vc, bt = _cuda("out", out, q.dtype), _cuda("value_cache", value_cache), _cuda("block_tables", block_tables, torch.int32, 2)
+    sl, qs = _cuda("seq_lens", seq_lens, torch.int32, 1), _cuda("query_starts", query_starts, torch.int32, 1)
+    tm = _cuda("tree_mask", tree_mask, torch.int64, 1)
+    B = seq_lens.shape[0]
+    NT, W = block_tables.shape
+    if NT != B or query_starts.shape[0] != B + 1:
+        raise ValueError("block_tables must have num_seqs rows and query_starts num_seqs + 1 entries")
+    if tree_mask.shape[0] != T:
+        raise ValueError("tree_mask must have num_tokens entries")
+    if workspace is None:
+        if planned:
+            raise ValueError("planned=True needs the workspace that prefill_plan wrote")
+        workspace = alloc_prefill_workspace(B, T, Hq, Hkv, d, q.device)
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    wp = _cuda("workspace", workspace)
+    scales = (_scales("k_scale", k_scale, Hkv), _scales("v_scale", v_scale, Hkv)) if kv8 else (None, None)
+    _check(load().pkv_paged_attention_tree(op, qp, kc, vc, bt, W, sl, qs, tm, B, T, int(max_seq_len), Hq, Hkv, d, bs, NB, scale,
+                                           _DT[q.dtype], _POOL_DT[dt], *scales, wp, workspace.nbytes, PLANNED if planned else 0,
+                                           _stream(q)))
+
+
 def paged_kv_gather(k_out, v_out, key_cache, value_cache, block_tables, seq_lens, row_starts, k_scale=None,
                     v_scale=None) -> None:
     """Rows row_starts[s] + t of k_out, v_out ([R, Hkv, d]) = position t < seq_lens[s] of sequence s (row_starts
@@ -684,6 +834,71 @@ def _accept(tokens, num_accepted, draft_tokens, target_probs, uniform, draft_pro
             raise ValueError("draft_probs must be [B, K, V]")
     _check(load().pkv_speculative_accept(*ptrs, counts, target, draft, _cuda("uniform", uniform, torch.float32, 2), B, K,
                                          V, _PROB_DT[target_probs.dtype], _stream(tokens)))
+
+
+def speculative_accept_tree(tokens, path, num_accepted, draft_tokens, parents, query_starts, target_probs, uniform) -> None:
+    """The path through each sequence's drafted tree that follows the target's distribution, and the token after it.
+
+    Nodes are rows query_starts[s] .. query_starts[s + 1] - 1 (int32 [B + 1]; up to 64 a sequence, the first its root) of
+    draft_tokens int64 [T], parents int32 [T] (an index within the sequence, before the node's own), target_probs [T, V]
+    float32 / float16 / bfloat16 and uniform float32 [T] in [0, 1).  tokens int64 [B, W] receives the accepted drafts, the
+    token drawn after them, then -1; path int32 [B, W] the root 0, the accepted nodes, then -1; num_accepted int32 [B] how
+    many drafts were accepted, up to W - 1."""
+    if _usual(tokens, path, num_accepted, draft_tokens, parents, query_starts, target_probs, uniform):
+        dt, rows, shape = target_probs.dtype, target_probs.shape, tokens.shape
+        if dt in _PROB_DT and tokens.dtype is draft_tokens.dtype is torch.int64 and uniform.dtype is torch.float32 and \
+                path.dtype is num_accepted.dtype is parents.dtype is query_starts.dtype is torch.int32 and len(rows) == 2 and \
+                len(shape) == 2 and path.shape == shape and num_accepted.shape == shape[:1] and \
+                query_starts.shape == (shape[0] + 1,) and draft_tokens.shape == parents.shape == uniform.shape == rows[:1]:
+            return _check(load().pkv_speculative_accept_tree(
+                tokens.data_ptr(), path.data_ptr(), num_accepted.data_ptr(), draft_tokens.data_ptr(), parents.data_ptr(),
+                query_starts.data_ptr(), target_probs.data_ptr(), uniform.data_ptr(), shape[0], rows[0], shape[1], rows[1],
+                _PROB_DT[dt], _stream(tokens)))
+    _accept_tree(tokens, path, num_accepted, draft_tokens, parents, query_starts, target_probs, uniform)
+
+
+@_one_device
+def _accept_tree(tokens, path, num_accepted, draft_tokens, parents, query_starts, target_probs, uniform) -> None:
+    ptrs = [_cuda("tokens", tokens, torch.int64, 2), _cuda("path", path, torch.int32, 2),
+            _cuda("num_accepted", num_accepted, torch.int32, 1), _cuda("draft_tokens", draft_tokens, torch.int64, 1),
+            _cuda("parents", parents, torch.int32, 1), _cuda("query_starts", query_starts, torch.int32, 1),
+            _cuda("target_probs", target_probs, _PROB_DTS, 2), _cuda("uniform", uniform, torch.float32, 1)]
+    (B, W), (T, V) = tokens.shape, target_probs.shape
+    if path.shape != tokens.shape or num_accepted.shape[0] != B or query_starts.shape[0] != B + 1:
+        raise ValueError("tokens and path must be [B, W], num_accepted [B] and query_starts [B + 1]")
+    if draft_tokens.shape[0] != T or parents.shape[0] != T or uniform.shape[0] != T:
+        raise ValueError("draft_tokens, parents and uniform must be [T], target_probs [T, V]")
+    _check(load().pkv_speculative_accept_tree(*ptrs, B, T, W, V, _PROB_DT[target_probs.dtype], _stream(tokens)))
+
+
+@_one_device
+def paged_kv_keep_path(key_caches, value_caches, block_tables, seq_lens, query_starts, path, num_accepted) -> None:
+    """The cache after a tree step: of sequence s's last n = query_starts[s + 1] - query_starts[s] positions, its tree's
+    nodes, those of path[s] (int32 [B, W], 0 = path[s, 0] < .. < path[s, num_accepted[s]]) move to the first
+    num_accepted[s] + 1, in every layer's pools.  seq_lens: the lengths with all nodes, as the attention had them; the
+    sequence then has seq_lens[s] - n + num_accepted[s] + 1 positions."""
+    if isinstance(key_caches, torch.Tensor):
+        key_caches, value_caches = [key_caches], [value_caches]
+    if len(key_caches) != len(value_caches) or not key_caches:
+        raise ValueError("need the same non-zero number of key and value caches")
+    shape, dt = key_caches[0].shape, key_caches[0].dtype
+    for i, (kc, vc) in enumerate(zip(key_caches, value_caches)):
+        _pool(f"key_caches[{i}]", kc, tuple(_POOL_DT))
+        _pool(f"value_caches[{i}]", vc, tuple(_POOL_DT))
+        if kc.shape != shape or vc.shape != shape or kc.dtype != dt or vc.dtype != dt:
+            raise ValueError("all caches must share shape and dtype")
+    args = [_cuda("block_tables", block_tables, torch.int32, 2), _cuda("seq_lens", seq_lens, torch.int32, 1),
+            _cuda("query_starts", query_starts, torch.int32, 1), _cuda("path", path, torch.int32, 2),
+            _cuda("num_accepted", num_accepted, torch.int32, 1)]
+    B, W = path.shape
+    if block_tables.shape[0] != B or seq_lens.shape[0] != B or query_starts.shape[0] != B + 1 or num_accepted.shape[0] != B:
+        raise ValueError("block_tables, seq_lens, path and num_accepted must have num_seqs rows, query_starts one more")
+    n = len(key_caches)
+    karr = (ctypes.c_void_p * n)(*[kc.data_ptr() for kc in key_caches])
+    varr = (ctypes.c_void_p * n)(*[vc.data_ptr() for vc in value_caches])
+    NB, bs, Hkv, d = shape
+    _check(load().pkv_paged_kv_keep_path(karr, varr, n, args[0], block_tables.shape[1], *args[1:], B, W, NB, bs, Hkv, d,
+                                         _POOL_DT[dt], _stream(key_caches[0])))
 
 
 @_one_device

@@ -21,6 +21,7 @@
 __device__ unsigned int g_pkv_error_word;
 
 static_assert(PKV_PLAN_MAX_SEQS == pkv::kPlanMaxSeqs, "plan batch limit: header and kernels agree");
+static_assert(PKV_TREE_MAX_NODES == pkv::kTreeNodes, "tree limit: header and kernels agree");
 
 namespace {
 
@@ -244,6 +245,74 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, void* key_cache, vo
     a.row_vecs = num_kv_heads * head_dim * 2 / 16;
     a.err = error_word(dev);
     cudaError_t e = pkv::launch_append(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+pkv_status pkv_paged_kv_append_rotary(void* q_out, const void* q, const void* k, const void* v, void* key_cache,
+                                      void* value_cache, const int64_t* slot_mapping, const int32_t* positions,
+                                      const float* cos_sin, int64_t num_tokens, int64_t q_out_stride, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, int num_positions, int rotary_dim,
+                                      int interleaved, int64_t num_blocks, int block_size, int num_heads,
+                                      int num_kv_heads, int head_dim, pkv_dtype dt, pkv_dtype kv_dt,
+                                      const float* k_scale, const float* v_scale, void* stream) {
+    CallRange range_("pkv_paged_kv_append_rotary");
+    if (num_tokens < 0 || num_tokens >= (int64_t(1) << 31))
+        return fail(PKV_ERR_INVALID, "num_tokens %lld outside [0, 2^31)", static_cast<long long>(num_tokens));
+    if (!valid_dtype(dt)) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", static_cast<int>(dt));
+    if (kv_dt != dt && kv_dt != PKV_E4M3) return fail(PKV_ERR_UNSUPPORTED, "kv_dt %d: dt or PKV_E4M3", static_cast<int>(kv_dt));
+    if (num_heads < 0 || num_heads > 4096 || num_kv_heads <= 0 || num_kv_heads > 4096)
+        return fail(PKV_ERR_INVALID, "num_heads %d / num_kv_heads %d (up to 4096)", num_heads, num_kv_heads);
+    if (head_dim <= 0 || head_dim % 16 != 0 || head_dim > 4096)
+        return fail(PKV_ERR_INVALID, "head_dim %d (a multiple of 16 up to 4096)", head_dim);
+    if (rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
+        return fail(PKV_ERR_INVALID, "rotary_dim %d (a multiple of 16 up to head_dim %d)", rotary_dim, head_dim);
+    if (num_positions <= 0 || block_size <= 0 || num_blocks <= 0)
+        return fail(PKV_ERR_INVALID, "num_positions %d / block_size %d / num_blocks %lld", num_positions, block_size,
+                    static_cast<long long>(num_blocks));
+    const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim, kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if ((num_heads > 0 && (q_out_stride < q_row || q_stride < q_row || q_out_stride % 8 || q_stride % 8)) ||
+        k_stride < kv_row || v_stride < kv_row || k_stride % 8 || v_stride % 8)
+        return fail(PKV_ERR_INVALID, "row strides must be multiples of 8 elements and hold a row");
+    if (num_heads > 0 && q_out == q && q_out_stride != q_stride)
+        return fail(PKV_ERR_INVALID, "q_out over q needs q's stride");
+    if (num_tokens == 0) return ok();
+    if ((num_heads > 0 && (!q_out || !q)) || !k || !v || !key_cache || !value_cache || !slot_mapping || !positions || !cos_sin)
+        return fail(PKV_ERR_INVALID, "null pointer");
+    const bool kv8 = kv_dt == PKV_E4M3;
+    if (kv8 && (!k_scale || !v_scale)) return fail(PKV_ERR_INVALID, "E4M3 pools need k_scale and v_scale");
+    const unsigned pool_align = kv8 ? 7u : 15u;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cos_sin) ||
+        (reinterpret_cast<uintptr_t>(key_cache) & pool_align) || (reinterpret_cast<uintptr_t>(value_cache) & pool_align) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+        (kv8 && ((reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u))))
+        return fail(PKV_ERR_INVALID, "tensors and 16-bit caches 16-byte aligned, E4M3 caches and slots 8-byte, the rest 4-byte");
+    pkv::AppendRotaryArgs a{};
+    a.q_out = q_out;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.key_cache = key_cache;
+    a.value_cache = value_cache;
+    a.slots = slot_mapping;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.num_tokens = num_tokens;
+    a.num_slots = num_blocks * block_size;
+    a.q_out_stride = q_out_stride;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.num_positions = num_positions;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved != 0;
+    a.err = error_word(current_device());
+    cudaError_t e = pkv::launch_append_rotary(a, dt == PKV_BF16, kv8, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
     return ok();
 }
@@ -681,8 +750,8 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
                         const int32_t* query_starts, int num_seqs, int64_t num_tokens, int max_seq_len, int num_heads,
                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale, pkv_dtype dt,
                         void* workspace, size_t workspace_bytes, int planned, void* stream,
-                        const float* k_scale = nullptr, const float* v_scale = nullptr) {
-    const bool kv8 = k_scale != nullptr;                 // an E4M3 pool (the _fp8 entry point)
+                        const float* k_scale = nullptr, const float* v_scale = nullptr, const uint64_t* tree_mask = nullptr) {
+    const bool kv8 = k_scale != nullptr;                 // an E4M3 pool
     if (kv8 && head_dim != 128) return fail(PKV_ERR_UNSUPPORTED, "E4M3 pools: head_dim 128 only");
     if (kv8 && ((reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u)))
         return fail(PKV_ERR_INVALID, "k_scale / v_scale must be 4-byte aligned");
@@ -724,6 +793,7 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     if ((st = encode_pool(&tmv, value_cache, num_blocks, block_size, num_kv_heads, head_dim, eb)) != PKV_OK) return st;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
+    a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (planned) a.direct = 0;
     a.local = !planned && !a.direct && pkv::prefill_local(num_seqs, num_tokens, num_heads, num_kv_heads, a.slots, lay);
@@ -784,6 +854,25 @@ pkv_status pkv_paged_attention_prefill_fp8(void* out, const void* q, const void*
     return prefill_call(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, query_starts,
                         num_seqs, num_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
                         scale, dt, workspace, workspace_bytes, planned, stream, k_scale, v_scale);
+}
+
+pkv_status pkv_paged_attention_tree(void* out, const void* q, const void* key_cache, const void* value_cache,
+                                    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                    const int32_t* query_starts, const uint64_t* tree_mask, int num_seqs,
+                                    int64_t num_tokens, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int64_t num_blocks, float scale, pkv_dtype dt, pkv_dtype kv_dt,
+                                    const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes,
+                                    int planned, void* stream) {
+    CallRange range_("pkv_paged_attention_tree");
+    if (kv_dt != dt && kv_dt != PKV_E4M3) return fail(PKV_ERR_UNSUPPORTED, "kv_dt %d: dt or PKV_E4M3", static_cast<int>(kv_dt));
+    const bool kv8 = kv_dt == PKV_E4M3;
+    if (kv8 && (!k_scale || !v_scale)) return fail(PKV_ERR_INVALID, "E4M3 pools need k_scale and v_scale");
+    if (num_seqs > 0 && num_tokens > 0 && (!tree_mask || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)))
+        return fail(PKV_ERR_INVALID, "tree_mask null or not 8-byte aligned");
+    return prefill_call(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, query_starts,
+                        num_seqs, num_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                        scale, dt, workspace, workspace_bytes, planned, stream, kv8 ? k_scale : nullptr,
+                        kv8 ? v_scale : nullptr, tree_mask);
 }
 
 }  // extern "C"
@@ -897,6 +986,96 @@ pkv_status pkv_speculative_accept(int64_t* tokens, int32_t* num_accepted, const 
     a.err = error_word(current_device());
     cudaError_t e = pkv::launch_accept(a, dt == PKV_F16 ? 0 : dt == PKV_BF16 ? 1 : 2, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "accept launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+pkv_status pkv_speculative_accept_tree(int64_t* tokens, int32_t* path, int32_t* num_accepted, const int64_t* draft_tokens,
+                                       const int32_t* parents, const int32_t* query_starts, const void* target_probs,
+                                       const float* uniform, int num_seqs, int64_t num_tokens, int width, int64_t vocab,
+                                       pkv_dtype dt, void* stream) {
+    CallRange range_("pkv_speculative_accept_tree");
+    if (!valid_dtype(dt) && dt != PKV_F32) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", static_cast<int>(dt));
+    if (num_seqs < 0 || num_seqs > (1 << 24)) return fail(PKV_ERR_INVALID, "num_seqs %d outside [0, 2^24]", num_seqs);
+    if (num_tokens < 0 || num_tokens >= (int64_t(1) << 31))
+        return fail(PKV_ERR_INVALID, "num_tokens %lld outside [0, 2^31)", static_cast<long long>(num_tokens));
+    if (width < 1 || width > 1024) return fail(PKV_ERR_INVALID, "width %d outside [1, 1024]", width);
+    if (vocab < 1 || vocab > PKV_ACCEPT_MAX_VOCAB)
+        return fail(PKV_ERR_INVALID, "vocab %lld outside [1, %d]", static_cast<long long>(vocab), PKV_ACCEPT_MAX_VOCAB);
+    if (num_seqs == 0) return ok();
+    if (!tokens || !path || !num_accepted || !query_starts ||
+        (num_tokens > 0 && (!draft_tokens || !parents || !target_probs || !uniform)))
+        return fail(PKV_ERR_INVALID, "null pointer");
+    const unsigned el = dt == PKV_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(tokens) & 7u) || (reinterpret_cast<uintptr_t>(draft_tokens) & 7u) ||
+        (reinterpret_cast<uintptr_t>(path) & 3u) || (reinterpret_cast<uintptr_t>(num_accepted) & 3u) ||
+        (reinterpret_cast<uintptr_t>(parents) & 3u) || (reinterpret_cast<uintptr_t>(query_starts) & 3u) ||
+        (reinterpret_cast<uintptr_t>(uniform) & 3u) || (reinterpret_cast<uintptr_t>(target_probs) & el))
+        return fail(PKV_ERR_INVALID, "tokens must be 8-byte aligned, the rest to their elements");
+    pkv::AcceptTreeArgs a{};
+    a.tokens = tokens;
+    a.path = path;
+    a.num_accepted = num_accepted;
+    a.draft_tokens = draft_tokens;
+    a.parents = parents;
+    a.query_starts = query_starts;
+    a.target_probs = target_probs;
+    a.uniform = uniform;
+    a.num_tokens = num_tokens;
+    a.vocab = vocab;
+    a.num_seqs = num_seqs;
+    a.width = width;
+    a.err = error_word(current_device());
+    cudaError_t e = pkv::launch_accept_tree(a, dt == PKV_F16 ? 0 : dt == PKV_BF16 ? 1 : 2, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "accept launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+pkv_status pkv_paged_kv_keep_path(void* const* key_caches, void* const* value_caches, int num_layers,
+                                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                  const int32_t* query_starts, const int32_t* path, const int32_t* num_accepted,
+                                  int num_seqs, int width, int64_t num_blocks, int block_size, int num_kv_heads,
+                                  int head_dim, pkv_dtype dt, void* stream) {
+    CallRange range_("pkv_paged_kv_keep_path");
+    if (num_layers < 0 || num_seqs < 0) return fail(PKV_ERR_INVALID, "num_layers %d / num_seqs %d below 0", num_layers, num_seqs);
+    if (!valid_dtype(dt) && dt != PKV_E4M3) return fail(PKV_ERR_UNSUPPORTED, "dtype %d", static_cast<int>(dt));
+    if (width < 1 || width > 1024) return fail(PKV_ERR_INVALID, "width %d outside [1, 1024]", width);
+    if (block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || max_blocks_per_seq < 0)
+        return fail(PKV_ERR_INVALID, "bad pool shape");
+    const int64_t row_bytes = static_cast<int64_t>(num_kv_heads) * head_dim * (dt == PKV_E4M3 ? 1 : 2);
+    if (row_bytes % 16 != 0 || row_bytes > (int64_t(1) << 30))
+        return fail(PKV_ERR_INVALID, "row bytes %lld not a multiple of 16 up to 2^30", static_cast<long long>(row_bytes));
+    if (num_layers == 0 || num_seqs == 0) return ok();
+    if (!key_caches || !value_caches || !block_tables || !seq_lens || !query_starts || !path || !num_accepted)
+        return fail(PKV_ERR_INVALID, "null pointer");
+    if ((reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(query_starts) & 3u) || (reinterpret_cast<uintptr_t>(path) & 3u) ||
+        (reinterpret_cast<uintptr_t>(num_accepted) & 3u))
+        return fail(PKV_ERR_INVALID, "tables, lengths and paths must be 4-byte aligned");
+    for (int l = 0; l < num_layers; ++l)
+        if (!key_caches[l] || !value_caches[l] || !aligned16(key_caches[l]) || !aligned16(value_caches[l]))
+            return fail(PKV_ERR_INVALID, "layer %d pool pointer null or not 16-byte aligned", l);
+    pkv::KeepPathArgs a{};
+    a.block_tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.query_starts = query_starts;
+    a.path = path;
+    a.num_accepted = num_accepted;
+    a.num_blocks = num_blocks;
+    a.num_seqs = num_seqs;
+    a.width = width;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_size = block_size;
+    a.row_vecs = static_cast<int>(row_bytes / 16);
+    a.err = error_word(current_device());
+    for (int l0 = 0; l0 < num_layers; l0 += pkv::kMaxCopyLayers) {
+        a.num_layers = std::min(num_layers - l0, pkv::kMaxCopyLayers);
+        for (int i = 0; i < a.num_layers; ++i) {
+            a.pools[2 * i] = static_cast<uint4*>(key_caches[l0 + i]);
+            a.pools[2 * i + 1] = static_cast<uint4*>(value_caches[l0 + i]);
+        }
+        cudaError_t e = pkv::launch_keep_path(a, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "keep_path launch: %s", cudaGetErrorString(e));
+    }
     return ok();
 }
 

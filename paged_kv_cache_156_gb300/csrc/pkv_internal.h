@@ -41,6 +41,32 @@ struct AppendFp8Args {
 };
 cudaError_t launch_append_fp8(const AppendFp8Args& a, cudaStream_t s);
 
+// Append with the position rotation (csrc/pkv_append_rotary.cu).
+struct AppendRotaryArgs {
+    void* q_out;             // rows of [num_heads][head_dim], a stride of elements apart
+    const void* q;
+    const void* k;           // rows of [num_kv_heads][head_dim]
+    const void* v;
+    void* key_cache;         // [num_blocks * block_size][num_kv_heads][head_dim] (16-bit elements, or codes)
+    void* value_cache;
+    const int64_t* slots;    // [num_tokens]
+    const int32_t* positions;
+    const float* cos_sin;    // [num_positions][rotary_dim]: cosines, then sines
+    const float* k_scale;    // [num_kv_heads] (E4M3 pools only)
+    const float* v_scale;
+    int64_t num_tokens;
+    int64_t num_slots;
+    int64_t q_out_stride, q_stride, k_stride, v_stride;
+    int num_positions;
+    int num_heads;           // (0: no queries)
+    int num_kv_heads;
+    int head_dim;
+    int rotary_dim;
+    int interleaved;
+    unsigned* err;
+};
+cudaError_t launch_append_rotary(const AppendRotaryArgs& a, bool bf16, bool kv8, cudaStream_t s);
+
 // Block copies between two pools of the same block shape (the same pool for
 // copy-on-write, a device pool and a pinned host pool for swapping).
 struct CopyArgs {
@@ -208,6 +234,7 @@ int decode_ctas_per_sm(int head_dim, bool kv8 = false);
 constexpr int kPrefillRows = 256;
 constexpr int kPrefillSub = 128;                // rows of one of an item's two tiles (the MMA's M)
 constexpr int kPrefillStep = 128;
+constexpr int kTreeNodes = 64;                  // nodes of a drafted tree at most (a row's mask is one 64-bit word)
 constexpr int kPrefillMaxParts = 152;           // parts one tile's positions are split into at most
 constexpr int kPrefillMinPart = 2;              // steps of a part at least
 // No tile is split in a batch of sequences of up to so many steps: what the parts save the planning and the merge cost.
@@ -266,6 +293,7 @@ struct PrefillArgs {
     float scale_log2;                // |scale| * log2(e)
     const float* k_scale;            // [num_kv_heads] (E4M3 pools only, else nullptr)
     const float* v_scale;
+    const unsigned long long* tree_mask;     // [num_tokens]: bit j, the token sees node j of its tree (nullptr: causal)
 };
 
 // A split tile's part: number of parts, this part, first partial slot.
@@ -329,6 +357,42 @@ struct AcceptArgs {
     unsigned* err;
 };
 cudaError_t launch_accept(const AcceptArgs& a, int dtype, cudaStream_t s);   // dtype 0: fp16, 1: bf16, 2: fp32
+
+// ---------------------------------------------------------------- a drafted tree (csrc/pkv_accept_tree.cu, pkv_keep_path.cu)
+struct AcceptTreeArgs {
+    int64_t* tokens;                 // [num_seqs][width]
+    int32_t* path;                   // [num_seqs][width]
+    int32_t* num_accepted;           // [num_seqs]
+    const int64_t* draft_tokens;     // [num_tokens]
+    const int32_t* parents;          // [num_tokens]
+    const int32_t* query_starts;     // [num_seqs + 1]
+    const void* target_probs;        // [num_tokens][vocab]
+    const float* uniform;            // [num_tokens]
+    int64_t num_tokens;
+    int64_t vocab;
+    int num_seqs;
+    int width;
+    unsigned* err;
+};
+cudaError_t launch_accept_tree(const AcceptTreeArgs& a, int dtype, cudaStream_t s);   // dtype 0: fp16, 1: bf16, 2: fp32
+
+struct KeepPathArgs {
+    uint4* pools[2 * kMaxCopyLayers];        // every layer's K pool and V pool: [num_blocks * block_size][row_vecs]
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* query_starts;
+    const int32_t* path;             // [num_seqs][width]
+    const int32_t* num_accepted;     // [num_seqs]
+    int64_t num_blocks;
+    int num_seqs;
+    int num_layers;
+    int width;
+    int max_blocks_per_seq;
+    int block_size;
+    int row_vecs;                    // 16-byte pieces of a row
+    unsigned* err;
+};
+cudaError_t launch_keep_path(const KeepPathArgs& a, cudaStream_t s);
 
 // Record `msg` as the calling thread's pkv_last_error() message and return `st`.
 int set_error_message(int st, const char* msg);

@@ -81,7 +81,7 @@ namespace {
 constexpr int kStep = kPrefillStep;
 constexpr int kSub = kPrefillSub;
 
-template <int D, bool KV8 = false>
+template <int D, bool KV8 = false, bool TREE = false>
 struct PfGeo {
     static constexpr int kThreads = 512;
     static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12, kLoadQ = KV8 ? 14 : 13, kPlan = 15;   // (9 and 11: MMAs; 12 and 14: cleaning; E4M3: 10, 12 and 13 expand)
@@ -89,8 +89,8 @@ struct PfGeo {
     static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
     static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
     // ring of K and V tiles, in turn; over an E4M3 pool a tile less in favour of two tiles of codes
-    static constexpr int kStages = KV8 ? 4 : D == 128 ? 5 : 10;
-    static constexpr int kCodes = KV8 ? 2 : 0;              // staged tiles of codes (128 rows of D bytes)
+    static constexpr int kStages = KV8 ? (TREE ? 3 : 4) : D == 128 ? 5 : 10;
+    static constexpr int kCodes = KV8 ? (TREE ? 3 : 2) : 0;   // staged tiles of codes (128 rows of D bytes)
     static constexpr int kCodeTile = 128 * D;
     static constexpr int kConverters = 3;                   // warps 10, 12 and 13: on two of the schedulers (10, 12, 14) 120 us, on three 117 (8 chunks of 256 to 512)
     static constexpr size_t kRing = 2 * size_t(kTile);      // after the two Q tiles
@@ -101,7 +101,8 @@ struct PfGeo {
     static constexpr int kNumBars = 3 * kStages + 21 + 2 * kItems + 2 * kCodes;
     static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, tags [3], epilogues [8]
     static constexpr size_t kBad = (kMisc + 52 + 15) / 16 * 16;   // first positions of non-finite V elements: [2 warps][+inf, -inf][D], or [3 warps][NaN][D]
-    static constexpr size_t kList = kBad + size_t(4) * D * 4;    // [kItems] decoded items
+    // a tree's: the nodes that hold them, 64 bits, [+inf, -inf][D] (a warp cleans half the columns), or [3 warps][NaN][D]
+    static constexpr size_t kList = kBad + size_t(TREE && KV8 ? 6 : 4) * D * 4;    // [kItems] decoded items
     static constexpr size_t kBytes = kList + kItems * 64;
     static_assert(!KV8 || D == 128, "E4M3 pools: a row of codes is one 128-byte plane");
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
@@ -192,6 +193,7 @@ __device__ __forceinline__ Entry find_entry(const PrefillArgs& a) {
     }
     return n;
 }
+template <bool TREE>
 __device__ __forceinline__ void read_item(const PrefillArgs& a, const Entry& n, Item& it) {
     const int4 x = n.x, y = n.y;
     it.kvh = n.kvh;
@@ -211,14 +213,14 @@ __device__ __forceinline__ void read_item(const PrefillArgs& a, const Entry& n, 
     if (it.s < 0 || it.s >= a.num_seqs || it.tile < 0 || it.step0 < 0 || step1 < it.step0 || it.qs < 0 || it.n <= 0 ||
         it.qs + static_cast<long long>(it.n) > a.num_tokens || it.L < 0 || it.L > a.max_seq_len ||
         static_cast<long long>(it.tile) * kPrefillRows >= static_cast<long long>(it.n) * a.group || it.split < 0 ||
-        (it.split != 0 && (part >= nparts || base + nparts > a.part_cap))) {
+        (it.split != 0 && (part >= nparts || base + nparts > a.part_cap)) || (TREE && it.n > kTreeNodes)) {
         if ((threadIdx.x & 31) == 0) raise_error(a.err, kErrBounds);
         return;
     }
     const int row0 = it.tile * kPrefillRows;
     it.rows = min(kPrefillRows, it.n * a.group - row0);
     const int past = it.L - it.n;
-    it.lim0 = max(0, past + pf::div(row0, a.by_group) + 1);
+    it.lim0 = max(0, TREE ? past : past + pf::div(row0, a.by_group) + 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = min(kSub, it.rows - i * kSub);
@@ -460,12 +462,13 @@ __device__ __forceinline__ Entry local_entry(const LocalPlan& lp, int e, int kvh
 }
 
 // T: the products' type; KV8: E4M3 pools (codes expanded to f16, every one exact there); OT: q's and out's.
-template <typename T, int D, bool KV8, typename OT>
-__global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
+// TREE: the last n positions are a tree's nodes, of which row (token i, head) sees those of token i's mask.
+template <typename T, int D, bool KV8, typename OT, bool TREE>
+__global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
                                                                         const __grid_constant__ CUtensorMap tmk,
                                                                         const __grid_constant__ CUtensorMap tmv,
                                                                         const __grid_constant__ PrefillArgs a) {
-    using G = PfGeo<D, KV8>;
+    using G = PfGeo<D, KV8, TREE>;
     constexpr int ST = G::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr bool kConvertQ = !std::is_same<T, OT>::value;     // bf16 queries over an E4M3 pool: to f16 in place
@@ -494,6 +497,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
     volatile int* epilogues = abort_flag + 4;       // [8] items a softmax warp is through with
     volatile int* bad_tag = abort_flag + 1;         // [3] the item whose non-finite V elements a warp's table lists (-1: none)
     int* bad = reinterpret_cast<int*>(smem + G::kBad);      // (kBad)
+    unsigned long long* bad_nodes = reinterpret_cast<unsigned long long*>(smem + G::kBad);      // (TREE)
+    static_assert(G::kBad % 8 == 0, "the node masks are 64-bit words");
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -640,7 +645,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             // and 2 (q and q ^ 5): the swizzles then put the eight pieces into different banks both times.  A
             // lane's row in a group of eight, and so its swizzle, never changes: addresses advance by 1 KB.
             const int cw = warp == G::kLoadV ? 0 : warp - G::kClean + 1;
-            int* mine = bad + cw * D;
+            [[maybe_unused]] int* mine = bad + cw * D;
             const int l3 = lane & 3, rl = (lane >> 3) ^ ((lane >> 2) & 1 ? 5 : 0);
             Ring<ST> c;
             Ring<G::kCodes> q;
@@ -681,7 +686,10 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                             if (__any_sync(0xffffffffu, hit != 0)) {                           // rare
                                 if (bad_tag[cw] != r) {
                                     ok = table_free(r);
-                                    for (int k = lane; k < D; k += 32) mine[k] = 0x7fffffff;
+                                    for (int k = lane; k < D; k += 32) {
+                                        if constexpr (TREE) bad_nodes[cw * D + k] = 0ull;
+                                        else mine[k] = 0x7fffffff;
+                                    }
                                     __syncwarp();
                                     if (lane == 0) bad_tag[cw] = r;
                                     __syncwarp();
@@ -694,8 +702,10 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 #pragma unroll 1
                                         for (int b = 0; b < 4; ++b) {
                                             if ((x[u][e] >> (8 * b) & 0x7fu) != 0x7fu) continue;
-                                            atomicMin(&mine[64 * (u & 1) + 16 * l3 + 4 * e + b],
-                                                      tok0 + 8 * (g0 + (u >> 1) * G::kConverters) + rl);
+                                            const int col = 64 * (u & 1) + 16 * l3 + 4 * e + b;
+                                            const int pos = tok0 + 8 * (g0 + (u >> 1) * G::kConverters) + rl;
+                                            if constexpr (TREE) atomicOr(&bad_nodes[cw * D + col], 1ull << (pos - it.L + it.n));
+                                            else atomicMin(&mine[col], pos);
                                             x[u][e] &= ~(0xffu << (8 * b));
                                         }
                                 }
@@ -979,7 +989,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 Item it;
                 more = next.live;
                 if (more) {
-                    read_item(a, next, it);
+                    read_item<TREE>(a, next, it);
                     if (!a.local) next = fetch_entry(a, total, r + 1);
                     else if (r < 31) next = round_entry(r + 1);
                     else next.live = false;
@@ -999,8 +1009,12 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
         } else if (warp == G::kClean || warp == G::kClean + 2) {
             // ======================================================== V tiles that some row sees only in part
             const int fw = warp != G::kClean;
-            int* mine = bad + fw * 2 * D;
-            constexpr int kCh = D / 8;
+            [[maybe_unused]] int* mine = bad + fw * 2 * D;
+            // the 16-byte pieces of a row, which two warps share: alternating runs of rows, or (TREE) half the columns
+            // each, so that a column's node masks are one warp's
+            constexpr int kCh = TREE ? D / 16 : D / 8;
+            const int ch0 = TREE ? fw * kCh : 0;
+            constexpr int kApart = TREE ? 1 : 2;             // runs of rows side by side
             constexpr int kBatch = 4;                        // loads in flight a lane
             constexpr uint32_t kCarry = kBf16 ? 0x00800080u : 0x04000400u;   // exponent all ones -> bit 15
             Ring<ST> c;
@@ -1034,10 +1048,13 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                     }
                     const uint32_t vt = smem_u32(ring + slot * G::kTile);
                     const int tok0 = (it.step0 + j) * kStep;
-                    auto addr_of = [&](int i) { return dec::swz(vt + (i % kCh >> 3) * G::kPlane, i / kCh, i % kCh & 7); };
+                    auto addr_of = [&](int i) {
+                        const int ch = ch0 + i % kCh;
+                        return dec::swz(vt + (ch >> 3) * G::kPlane, i / kCh, ch & 7);
+                    };
                     const int end = nv16 * kCh;
 #pragma unroll 1
-                    for (int i0 = lo * kCh + fw * 32 * kBatch; i0 < end; i0 += 64 * kBatch) {       // (warp-uniform)
+                    for (int i0 = lo * kCh + (TREE ? 0 : fw * 32 * kBatch); i0 < end; i0 += 32 * kApart * kBatch) {       // (warp-uniform)
                         uint32_t hit = 0;                    // bit u: piece u holds a non-finite element
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
@@ -1061,7 +1078,11 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                         if (__any_sync(0xffffffffu, hit != 0)) {             // rare
                             if (bad_tag[fw] != r) {          // (warp-uniform: this warp alone writes it)
                                 ok = table_free(r);
-                                for (int k = lane; k < 2 * D; k += 32) mine[k] = 0x7fffffff;
+                                if constexpr (TREE) {
+                                    for (int k = lane; k < D; k += 32) bad_nodes[(k / (D / 2)) * D + fw * (D / 2) + k % (D / 2)] = 0ull;
+                                } else {
+                                    for (int k = lane; k < 2 * D; k += 32) mine[k] = 0x7fffffff;
+                                }
                                 __syncwarp();
                                 if (lane == 0) bad_tag[fw] = r;
                                 __syncwarp();
@@ -1075,9 +1096,16 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr));
                                 const uint32_t mag = h & 0x7fffu, inf = 0x8000u - (kCarry & 0xffffu);
                                 if (mag < inf) continue;
-                                const int col = 8 * (i % kCh) + (e & 7), pos = tok0 + i / kCh;
-                                if (mag > inf || h < 0x8000u) atomicMin(&mine[col], pos);
-                                if (mag > inf || h >= 0x8000u) atomicMin(&mine[D + col], pos);
+                                const int col = 8 * (ch0 + i % kCh) + (e & 7), pos = tok0 + i / kCh;
+                                const bool up = mag > inf || h < 0x8000u, down = mag > inf || h >= 0x8000u;
+                                if constexpr (TREE) {
+                                    const unsigned long long node = 1ull << (pos - it.L + it.n);
+                                    if (up) atomicOr(&bad_nodes[col], node);
+                                    if (down) atomicOr(&bad_nodes[D + col], node);
+                                } else {
+                                    if (up) atomicMin(&mine[col], pos);
+                                    if (down) atomicMin(&mine[D + col], pos);
+                                }
                                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(uint16_t(0)) : "memory");
                             }
                         }
@@ -1116,6 +1144,16 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             // of them beside 4 chunks; at head_dim 64 the code more cost 4%)
             const bool idle = wg * kSub + (warp & 3) * 32 >= it.rows;
             const int seen = min(lim, it.end_of(wg));           // (dummy rows too stop at the tile's end)
+            // TREE: the nodes the row sees (dummy rows: all), none after its own nor of a position below 0
+            const int past = it.L - it.n;
+            unsigned long long nodes = 0ull;
+            if constexpr (TREE) {
+                if (it.rows > 0) {
+                    nodes = ~0ull >> (kTreeNodes - it.n);
+                    if (has) nodes &= __ldcg(a.tree_mask + it.qs + tok) & ~0ull >> (kTreeNodes - 1 - tok);
+                    if (past < 0) nodes = past > -kTreeNodes ? nodes & ~0ull << -past : 0ull;
+                }
+            }
             float m_ref = -INFINITY, l = 0.0f;
             float sl2 = a.scale_log2;
             if (KV8) {
@@ -1165,7 +1203,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 // Two passes over S, a rolled loop of two halves each, S read from TMEM again for the second: half
                 // the code of one pass with S in registers, and the code of the loops is what the schedulers'
                 // instruction caches must hold beside the MMA warps'.
-                const int vis = seen - (it.step0 + j) * kStep;
+                [[maybe_unused]] const int vis = seen - (it.step0 + j) * kStep;
                 float top = -INFINITY;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -1173,7 +1211,23 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                     tc::ld32(x[0], ts + 64 * h);
                     tc::ld32(x[1], ts + 64 * h + 32);
                     tc::wait_ld();
-                    if (__any_sync(0xffffffffu, vis < 64 * h + 64)) {            // masked scores go back as -inf
+                    if constexpr (TREE) {
+                        const int j0 = (it.step0 + j) * kStep + 64 * h - past;    // the node of the first column
+                        if (j0 > -64) {                      // (the same in every thread) masked scores go back as -inf
+                            const unsigned long long word = j0 >= kTreeNodes ? 0ull
+                                                            : j0 >= 0        ? nodes >> j0
+                                                                             : nodes << -j0 | ((1ull << -j0) - 1ull);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t half = static_cast<uint32_t>(word >> (32 * c));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(half >> e & 1u)) x[c][e] = 0xff800000u;
+                                tc::st32(ts + 64 * h + 32 * c, x[c]);
+                            }
+                            tc::wait_st();
+                        }
+                    } else if (__any_sync(0xffffffffu, vis < 64 * h + 64)) {     // masked scores go back as -inf
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -1275,7 +1329,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
                 tc::fence_after_sync();
                 const float vs = KV8 ? __ldcg(a.v_scale + it.kvh) : 1.0f;
                 // (no weight: zeros for a row that sees nothing, NaN where every score it sees is -inf; a NaN sum stays)
-                const float inv = l > 0.0f ? vs / l : l == 0.0f ? (lim > 0 ? NAN : 0.0f) : l;
+                const bool sees = TREE ? past > 0 || nodes != 0ull : lim > 0;
+                const float inv = l > 0.0f ? vs / l : l == 0.0f ? (sees ? NAN : 0.0f) : l;
                 if (split) {
                     // a row a thread, 16 bytes of 32 neighbouring rows side by side
 #pragma unroll 1
@@ -1337,7 +1392,17 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
 #pragma unroll 1
                     for (int c = 0; c < D; ++c) {
                         bool up, down;
-                        if (KV8) {
+                        if constexpr (TREE) {
+                            if constexpr (KV8) {
+                                up = (bad0 && (bad_nodes[c] & nodes)) || (bad1 && (bad_nodes[D + c] & nodes)) ||
+                                     (bad2 && (bad_nodes[2 * D + c] & nodes));
+                                down = up;
+                            } else {
+                                const bool listed = c < D / 2 ? bad0 : bad1;
+                                up = listed && (bad_nodes[c] & nodes);
+                                down = listed && (bad_nodes[D + c] & nodes);
+                            }
+                        } else if (KV8) {
                             up = (bad0 && bad[c] < seen) || (bad1 && bad[D + c] < seen) || (bad2 && bad[2 * D + c] < seen);
                             down = up;
                         } else {
@@ -1365,8 +1430,16 @@ __global__ void __launch_bounds__(PfGeo<D, KV8>::kThreads, 1) prefill_kernel(con
             }
             // (a part whose every score the row sees is -inf: its sum is -1, told from a part it sees nothing of; its weight
             // in the merge is 2^(-inf - m), 0 beside a part with a finite score and NaN without one)
-            if (split && has)
-                a.part_ml[slot * a.part_rows + myrow] = make_float2(m_ref, l == 0.0f && seen > it.step0 * kStep ? -1.0f : l);
+            if (split && has) {
+                bool some = seen > it.step0 * kStep;
+                if constexpr (TREE) {
+                    const int from = it.step0 * kStep - past, to = it.end_of(wg) - past;     // the part's nodes
+                    some = from < 0 && n > 0;
+                    if (from < kTreeNodes && to > 0)
+                        some |= ((nodes & ~0ull >> (kTreeNodes - min(to, kTreeNodes))) >> max(from, 0)) != 0ull;
+                }
+                a.part_ml[slot * a.part_rows + myrow] = make_float2(m_ref, l == 0.0f && some ? -1.0f : l);
+            }
             __syncwarp();
             if (lane == 0) atomicAdd(const_cast<int*>(epilogues) + warp, 1);
         }
@@ -1475,12 +1548,12 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
     }
 }
 
-template <typename T, int D, bool KV8 = false, typename OT = T>
+template <typename T, int D, bool KV8, typename OT, bool TREE>
 cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                      cudaStream_t s) {
-    using G = PfGeo<D, KV8>;
+    using G = PfGeo<D, KV8, TREE>;
     static_assert(G::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
-    auto kern = prefill_kernel<T, D, KV8, OT>;
+    auto kern = prefill_kernel<T, D, KV8, OT, TREE>;
     // once a device: the shared memory, and that the warpgroups' register split fits what a block is launched with
     // (or it would wait for ever)
     static std::atomic<uint64_t> ready{0};
@@ -1514,16 +1587,25 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtenso
     return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<OT, D>, a);
 }
 
+template <bool TREE>
+cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype,
+                   int head_dim, cudaStream_t s) {
+    using bf16 = __nv_bfloat16;
+    if (a.k_scale)
+        return dtype == 0 ? launch_t<__half, 128, true, __half, TREE>(a, tmq, tmk, tmv, s)
+                          : launch_t<__half, 128, true, bf16, TREE>(a, tmq, tmk, tmv, s);
+    if (dtype == 0)
+        return head_dim == 128 ? launch_t<__half, 128, false, __half, TREE>(a, tmq, tmk, tmv, s)
+                               : launch_t<__half, 64, false, __half, TREE>(a, tmq, tmk, tmv, s);
+    return head_dim == 128 ? launch_t<bf16, 128, false, bf16, TREE>(a, tmq, tmk, tmv, s)
+                           : launch_t<bf16, 64, false, bf16, TREE>(a, tmq, tmk, tmv, s);
+}
+
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            int dtype, int head_dim, cudaStream_t s) {
-    if (a.k_scale)
-        return dtype == 0 ? launch_t<__half, 128, true>(a, tmq, tmk, tmv, s)
-                          : launch_t<__half, 128, true, __nv_bfloat16>(a, tmq, tmk, tmv, s);
-    if (dtype == 0)
-        return head_dim == 128 ? launch_t<__half, 128>(a, tmq, tmk, tmv, s) : launch_t<__half, 64>(a, tmq, tmk, tmv, s);
-    return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(a, tmq, tmk, tmv, s) : launch_t<__nv_bfloat16, 64>(a, tmq, tmk, tmv, s);
+    return a.tree_mask ? launch<true>(a, tmq, tmk, tmv, dtype, head_dim, s) : launch<false>(a, tmq, tmk, tmv, dtype, head_dim, s);
 }
 
 }  // namespace pkv
