@@ -12,9 +12,11 @@ library's CUDA kernels; there is no CPU path.  A missing library raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import math
+import operator
 import os
 
 import torch
@@ -129,7 +131,7 @@ def load() -> ctypes.CDLL:
     lib.pkv_speculative_accept_tree.restype = c_i
     lib.pkv_speculative_accept_tree.argtypes = [c_p] * 8 + [c_i, c_i64, c_i, c_i64, c_i, c_p]
     lib.pkv_paged_kv_keep_path.restype = c_i
-    lib.pkv_paged_kv_keep_path.argtypes = [ctypes.POINTER(c_p), ctypes.POINTER(c_p), c_i, c_p, c_i, c_p, c_p, c_p, c_p, c_i,
+    lib.pkv_paged_kv_keep_path.argtypes = [c_p, c_p, c_i, c_p, c_i, c_p, c_p, c_p, c_p, c_i,
                                            c_i, c_i64, c_i, c_i, c_i, c_i, c_p]
     lib.pkv_copy_blocks.restype = c_i
     lib.pkv_copy_blocks.argtypes = [ctypes.POINTER(c_p), ctypes.POINTER(c_p), c_i, c_p, c_i64, c_i64, c_i, c_i,
@@ -285,17 +287,31 @@ def paged_kv_append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping,
     cos_sin float32 [P, r]: row p holds the cosines, then the sines, of position p's r / 2 angles.  A head's first r
     elements turn, as pairs (i, i + r / 2), or (2 i, 2 i + 1) when ``interleaved``.  uint8 pools hold E4M3 codes and take
     k_scale / v_scale (float32 [Hkv]) as paged_kv_append_fp8 does."""
-    args = (q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved, k_scale, v_scale)
-    if _usual(key_cache, value_cache, slot_mapping, positions, cos_sin):
-        dev = key_cache.get_device()
-        for t in (q_out, q, k, v, k_scale, v_scale):
-            if t is not None and (type(t) is not _Tensor or t.get_device() != dev):
-                break
-        else:
-            return _append_rotary(*args)
-    _append_rotary_on_device(*args)
+    if _usual(key_cache, value_cache, slot_mapping, positions, cos_sin) and type(k) is _Tensor:
+        dev, dt, pool, kdt = key_cache.get_device(), key_cache.dtype, key_cache.shape, k.dtype
+        kv8 = dt is torch.uint8
+        T, h, d = k.shape if k.dim() == 3 else (0, 0, 0)
+        if T > 1 and type(v) is type(q) is type(q_out) is _Tensor and len(pool) == 4 and pool[2] == h and \
+                pool[3] == d and k.get_device() == v.get_device() == q.get_device() == q_out.get_device() == dev and \
+                (kv8 or dt is kdt) and v.dtype is q.dtype is q_out.dtype is kdt and kdt in _DT and value_cache.dtype is dt and \
+                value_cache.shape == pool and v.shape == (T, h, d) and slot_mapping.dtype is torch.int64 and \
+                positions.dtype is torch.int32 and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and \
+                slot_mapping.shape == positions.shape == (T,) and \
+                (k_scale is None and v_scale is None if not kv8 else _usual(key_cache, k_scale, v_scale) and
+                 k_scale.dtype is v_scale.dtype is torch.float32 and k_scale.shape == v_scale.shape == (h,)):
+            rows = q.shape
+            ks, vs, qs, os_ = k.stride(), v.stride(), q.stride(), q_out.stride()
+            if len(rows) == 3 and rows[0] == T and rows[2] == d and q_out.shape == rows and \
+                    ks[2] == vs[2] == qs[2] == os_[2] == 1 and ks[1] == vs[1] == qs[1] == os_[1] == d:
+                return _check(load().pkv_paged_kv_append_rotary(
+                    q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                    slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T, os_[0], qs[0], ks[0], vs[0],
+                    *cos_sin.shape, 1 if interleaved else 0, pool[0], pool[1], rows[1], h, d, _DT[kdt], _POOL_DT[dt],
+                    k_scale.data_ptr() if kv8 else None, v_scale.data_ptr() if kv8 else None, _stream(key_cache)))
+    _append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved, k_scale, v_scale)
 
 
+@_one_device
 def _append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved, k_scale,
                    v_scale) -> None:
     dt = key_cache.dtype
@@ -329,9 +345,6 @@ def _append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping, positio
     _check(load().pkv_paged_kv_append_rotary(qo, qi, k.data_ptr(), v.data_ptr(), kc, vc, sm, ps, cs, T, qos, qis, ks, vs, P, r,
                                              1 if interleaved else 0, NB, bs, Hq, Hkv, d, _DT[k.dtype], _POOL_DT[dt],
                                              *scales, _stream(key_cache)))
-
-
-_append_rotary_on_device = _one_device(_append_rotary)
 
 
 def decode_partition_tokens(num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len) -> int:
@@ -871,12 +884,37 @@ def _accept_tree(tokens, path, num_accepted, draft_tokens, parents, query_starts
     _check(load().pkv_speculative_accept_tree(*ptrs, B, T, W, V, _PROB_DT[target_probs.dtype], _stream(tokens)))
 
 
-@_one_device
+_get_dtype, _get_shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
 def paged_kv_keep_path(key_caches, value_caches, block_tables, seq_lens, query_starts, path, num_accepted) -> None:
     """The cache after a tree step: of sequence s's last n = query_starts[s + 1] - query_starts[s] positions, its tree's
     nodes, those of path[s] (int32 [B, W], 0 = path[s, 0] < .. < path[s, num_accepted[s]]) move to the first
     num_accepted[s] + 1, in every layer's pools.  seq_lens: the lengths with all nodes, as the attention had them; the
     sequence then has seq_lens[s] - n + num_accepted[s] + 1 positions."""
+    if _usual(block_tables, seq_lens, query_starts, path, num_accepted) and type(key_caches) is type(value_caches) is list and \
+            len(key_caches) == len(value_caches) and key_caches:
+        # (map and set over the pools: statements of its own for each of 32 layers' took three times as long)
+        pools = key_caches + value_caches
+        first, table, shape = pools[0], block_tables.shape, path.shape
+        if set(map(type, pools)) == {_Tensor} and set(map(_Tensor.get_device, pools)) == {block_tables.get_device()} and \
+                all(map(_Tensor.is_contiguous, pools)) and len(set(map(_get_dtype, pools))) == 1 and \
+                list(map(_get_shape, pools)).count(first.shape) == len(pools) and first.dim() == 4 and first.dtype in _POOL_DT and \
+                block_tables.dtype is seq_lens.dtype is query_starts.dtype is path.dtype is num_accepted.dtype is torch.int32 and \
+                len(table) == len(shape) == 2 and seq_lens.shape == num_accepted.shape == table[:1] == shape[:1] and \
+                query_starts.shape == (shape[0] + 1,):
+            n, (NB, bs, Hkv, d) = len(key_caches), first.shape
+            ptrs = array.array("Q", map(_Tensor.data_ptr, pools))
+            at = ptrs.buffer_info()[0]
+            return _check(load().pkv_paged_kv_keep_path(
+                at, at + 8 * n, n, block_tables.data_ptr(), table[1], seq_lens.data_ptr(), query_starts.data_ptr(),
+                path.data_ptr(), num_accepted.data_ptr(), shape[0], shape[1], NB, bs, Hkv, d, _POOL_DT[first.dtype],
+                _stream(path)))
+    _keep_path(key_caches, value_caches, block_tables, seq_lens, query_starts, path, num_accepted)
+
+
+@_one_device
+def _keep_path(key_caches, value_caches, block_tables, seq_lens, query_starts, path, num_accepted) -> None:
     if isinstance(key_caches, torch.Tensor):
         key_caches, value_caches = [key_caches], [value_caches]
     if len(key_caches) != len(value_caches) or not key_caches:
@@ -897,7 +935,7 @@ def paged_kv_keep_path(key_caches, value_caches, block_tables, seq_lens, query_s
     karr = (ctypes.c_void_p * n)(*[kc.data_ptr() for kc in key_caches])
     varr = (ctypes.c_void_p * n)(*[vc.data_ptr() for vc in value_caches])
     NB, bs, Hkv, d = shape
-    _check(load().pkv_paged_kv_keep_path(karr, varr, n, args[0], block_tables.shape[1], *args[1:], B, W, NB, bs, Hkv, d,
+    _check(load().pkv_paged_kv_keep_path(ctypes.addressof(karr), ctypes.addressof(varr), n, args[0], block_tables.shape[1], *args[1:], B, W, NB, bs, Hkv, d,
                                          _POOL_DT[dt], _stream(key_caches[0])))
 
 
