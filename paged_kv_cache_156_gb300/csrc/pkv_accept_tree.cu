@@ -95,43 +95,66 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
         const int batches = (V + off + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128);
         const int piece = (rank * kWarps + warp) * batches * kBatch * 128 - off;
 
-        float w[kBatch][4];
-        auto load = [&](int batch) {                // this lane's weights of a batch
-            const int i0 = piece + batch * kBatch * 128;         // (warp-uniform)
-            const int i = i0 + 4 * lane;
-            if (i0 >= 0 && i0 + kBatch * 128 <= V) {
-                uint32_t p[kBatch][Four<T>::kWords];
+        constexpr int kWords = Four<T>::kWords;
+        const T* mine_at = row + piece + 4 * lane;
+        // (warp-uniform: a batch wholly in the row; one of the row's ends is read weight by weight)
+        auto inside = [&](int batch) { return piece + batch * kBatch * 128 >= 0 && piece + (batch + 1) * kBatch * 128 <= V; };
+        auto load = [&](int batch, uint32_t (&p)[kBatch][kWords]) {
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) Four<T>::load(p[k], row + i + 128 * k);
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    Four<T>::unpack(p[k], w[k]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(w[k][e]);
-                }
-            } else {                                // a batch at the row's ends
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int at = i + 128 * k + e;
-                        w[k][e] = at >= 0 && at < V ? __saturatef(to_f32(row[at])) : 0.0f;
-                    }
-            }
+            for (int k = 0; k < kBatch; ++k) Four<T>::load(p[k], mine_at + (batch * kBatch + k) * 128);
         };
-
-        unsigned long long mine = 0;
-#pragma unroll 1
-        for (int batch = 0; batch < batches; ++batch) {
+        auto at_ends = [&](int batch, int k, int e) {
+            const int at = piece + (batch * kBatch + k) * 128 + 4 * lane + e;
+            return at >= 0 && at < V ? __saturatef(to_f32(row[at])) : 0.0f;
+        };
+        auto units_of = [&](const uint32_t (&p)[kBatch][kWords]) {            // of a batch's 16 weights
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                float w[4];
+                Four<T>::unpack(p[k], w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add_units(__saturatef(w[e]), hi, lo);
+            }
+            return join(hi, lo);
+        };
+        auto units_at_ends = [&](int batch) {
             uint32_t hi = 0, lo = 0;
             if (piece + batch * kBatch * 128 < V) {
-                load(batch);
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) add_units(w[k][e], hi, lo);
+                    for (int e = 0; e < 4; ++e) add_units(at_ends(batch, k, e), hi, lo);
             }
-            const unsigned long long sum = join(hi, lo);
+            return join(hi, lo);
+        };
+
+        // ---- the row's total, two batches in flight: a sequence whose neighbours are through has its SMs to itself, and
+        // what its eight warps a CTA have in flight sets its pace
+        unsigned long long mine = 0;
+        int batch = 0;
+#pragma unroll 1
+        for (; batch + 2 <= batches && inside(batch) && inside(batch + 1); batch += 2) {
+            uint32_t p[2][kBatch][kWords];
+            load(batch, p[0]);
+            load(batch + 1, p[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const unsigned long long sum = units_of(p[i]);
+                batch_sum[batch + i][t] = sum;
+                mine += sum;
+            }
+        }
+#pragma unroll 1
+        for (; batch < batches; ++batch) {
+            unsigned long long sum;
+            if (inside(batch)) {
+                uint32_t p[kBatch][kWords];
+                load(batch, p);
+                sum = units_of(p);
+            } else {
+                sum = units_at_ends(batch);
+            }
             batch_sum[batch][t] = sum;
             mine += sum;
         }
@@ -157,7 +180,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             for (int v = 0; v < warp; ++v) before += warp_total[v];
             if (mark >= before && mark < before + mine) {
                 // the batch that holds the mark: four batches' sums at a time, side by side
-                int batch = 0;
+                batch = 0;
                 for (int b0 = 0; b0 < batches; b0 += 4) {
                     unsigned long long sum[4];
 #pragma unroll
@@ -174,7 +197,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
                     }
                     if (here) break;
                 }
-                load(batch);
+                float w[kBatch][4];
+                if (inside(batch)) {
+                    uint32_t p[kBatch][kWords];
+                    load(batch, p);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        Four<T>::unpack(p[k], w[k]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(w[k][e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[k][e] = at_ends(batch, k, e);
+                }
                 unsigned long long own[kBatch], inc[kBatch];      // a lane's four weights, and up to and with them
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {

@@ -22,7 +22,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;                       // (heads of more than 2048 elements: twice as many)
 constexpr int kRows = 3;                            // rows of a thread whose loads are in flight together
 
 // (ld.cg, never ld.nc: q_out may be q, and the compiler may move an ld.nc above the wait for the kernel that writes it)
@@ -64,16 +64,39 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
 }
 
 template <bool BF16, bool KV8>
-__global__ void __launch_bounds__(kThreads) append_rotary_kernel(const __grid_constant__ AppendRotaryArgs a) {
+__global__ void __launch_bounds__(2 * kThreads) append_rotary_kernel(const __grid_constant__ AppendRotaryArgs a) {
     grid_dependency_wait();
     launch_dependents();
     const int64_t tok = blockIdx.x;
     const int units = a.head_dim / 16;              // of a row: two 16-byte pieces each
-    const int step = kThreads / units;              // rows the CTA takes side by side
+    const int step = blockDim.x / units;             // rows the CTA takes side by side
     const int u = threadIdx.x % units, r0 = threadIdx.x / units;
     if (r0 >= step) return;
+    const int half = a.rotary_dim / 2;
+    const bool turns = u < a.rotary_dim / 16;
+    const bool apart = turns && !a.interleaved;     // its pieces stand half the rotated elements apart
+    const int e0 = apart ? 8 * u : 16 * u, e1 = apart ? e0 + half : e0 + 8;      // their first elements
+    const int hq = a.num_heads, hk = a.num_kv_heads, d = a.head_dim;
+    const int rows = hq + 2 * hk;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + tok * a.q_stride;
+    const uint16_t* k = static_cast<const uint16_t*>(a.k) + tok * a.k_stride;
+    const uint16_t* v = static_cast<const uint16_t*>(a.v) + tok * a.v_stride;
+    uint16_t* q_out = static_cast<uint16_t*>(a.q_out) + tok * a.q_out_stride;
+    uint4 x[kRows][2];
+    auto load = [&](int base) {                     // (whatever becomes of the token: its rows are there)
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = base + i * step;
+            if (r < rows) {
+                const uint16_t* src = r < hq ? q + r * d : r < hq + hk ? k + (r - hq) * d : v + (r - hq - hk) * d;
+                x[i][0] = load16(src + e0);
+                x[i][1] = load16(src + e1);
+            }
+        }
+    };
     const int64_t slot = __ldcg(a.slots + tok);
     const int pos = __ldcg(a.positions + tok);
+    load(r0);
     if (pos < 0 || pos >= a.num_positions) {        // nothing to turn by: the token is left out
         if (threadIdx.x == 0 && !(pos < 0 && slot < 0)) raise_error(a.err, kErrBounds);
         return;
@@ -83,10 +106,6 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const __grid_co
         if (threadIdx.x == 0) raise_error(a.err, kErrBounds);
         store_kv = false;
     }
-    const int half = a.rotary_dim / 2;
-    const bool turns = u < a.rotary_dim / 16;
-    const bool apart = turns && !a.interleaved;     // its pieces stand half the rotated elements apart
-    const int e0 = apart ? 8 * u : 16 * u, e1 = apart ? e0 + half : e0 + 8;      // their first elements
     float c[8], s[8];
     if (turns) {
         const float4* cp = reinterpret_cast<const float4*>(a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim + 8 * u);
@@ -95,24 +114,8 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const __grid_co
         c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
         s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
     }
-    const int hq = a.num_heads, hk = a.num_kv_heads, d = a.head_dim;
-    const int rows = hq + 2 * hk;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + tok * a.q_stride;
-    const uint16_t* k = static_cast<const uint16_t*>(a.k) + tok * a.k_stride;
-    const uint16_t* v = static_cast<const uint16_t*>(a.v) + tok * a.v_stride;
-    uint16_t* q_out = static_cast<uint16_t*>(a.q_out) + tok * a.q_out_stride;
 #pragma unroll 1
-    for (int base = r0; base < rows; base += kRows * step) {
-        uint4 x[kRows][2];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = base + i * step;
-            if (r < hq || (r < rows && store_kv)) {
-                const uint16_t* src = r < hq ? q + r * d : r < hq + hk ? k + (r - hq) * d : v + (r - hq - hk) * d;
-                x[i][0] = load16(src + e0);
-                x[i][1] = load16(src + e1);
-            }
-        }
+    for (int base = r0;;) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = base + i * step;
@@ -154,6 +157,9 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const __grid_co
                 *reinterpret_cast<uint2*>(dst + e1) = quantize8f(hi, scale);
             }
         }
+        base += kRows * step;
+        if (base >= rows) break;
+        load(base);
     }
 }
 
@@ -161,7 +167,7 @@ template <bool BF16, bool KV8>
 cudaError_t launch(const AppendRotaryArgs& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.num_tokens));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(a.head_dim / 16 > kThreads ? 2 * kThreads : kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -23,8 +23,10 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMoves = 8;                           // rows of a thread in flight together
+constexpr int kThreads = 64;
+constexpr int kMoves = 8;                           // rows of a thread in flight together,
+constexpr int kAtOnce = 2;                          // in so many pools
+constexpr int kCtas = 152 * 12;                     // of the grid
 constexpr int kNodes = PKV_TREE_MAX_NODES;
 
 __global__ void __launch_bounds__(kThreads) keep_path_kernel(const __grid_constant__ KeepPathArgs a) {
@@ -63,18 +65,32 @@ __global__ void __launch_bounds__(kThreads) keep_path_kernel(const __grid_consta
         s_dst[at] = in ? static_cast<int64_t>(db) * a.block_size + dst % a.block_size : -1;
     }
     __syncthreads();
-    const int pools = 2 * a.num_layers;
-    for (int p = blockIdx.y; p < pools; p += gridDim.y) {
-        uint4* pool = a.pools[p];
-        for (int c = t; c < a.row_vecs; c += kThreads) {
-            for (int m0 = 0; m0 < moves; m0 += kMoves) {
-                uint4 x[kMoves];
+    // every (pool, column) of the CTA, kAtOnce at a time
+    const int pools = 2 * a.num_layers, y = gridDim.y;
+    const int wide = (a.row_vecs + kThreads - 1) / kThreads;                  // columns of a thread in a pool
+    const int all = (pools - static_cast<int>(blockIdx.y) + y - 1) / y * wide;
+    for (int k0 = 0; k0 < all; k0 += kAtOnce) {
+        uint4* column[kAtOnce];
 #pragma unroll
-                for (int i = 0; i < kMoves; ++i)
-                    if (m0 + i < moves && s_src[m0 + i] >= 0) x[i] = __ldcg(pool + s_src[m0 + i] * a.row_vecs + c);
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int p = (k0 + k) / wide, c = (k0 + k) % wide * kThreads + t;
+            column[k] = k0 + k < all && c < a.row_vecs ? a.pools[blockIdx.y + p * y] + c : nullptr;
+        }
+        for (int m0 = 0; m0 < moves; m0 += kMoves) {
+            uint4 x[kAtOnce][kMoves];
 #pragma unroll
-                for (int i = 0; i < kMoves; ++i)
-                    if (m0 + i < moves && s_src[m0 + i] >= 0) pool[s_dst[m0 + i] * a.row_vecs + c] = x[i];
+            for (int i = 0; i < kMoves; ++i) {
+                const int64_t src = m0 + i < moves ? s_src[m0 + i] : -1;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    if (src >= 0 && column[k]) x[k][i] = __ldcg(column[k] + src * a.row_vecs);
+            }
+#pragma unroll
+            for (int i = 0; i < kMoves; ++i) {
+                const int64_t dst = m0 + i < moves ? s_dst[m0 + i] : -1;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    if (dst >= 0 && column[k]) column[k][dst * a.row_vecs] = x[k][i];
             }
         }
     }
@@ -85,7 +101,8 @@ __global__ void __launch_bounds__(kThreads) keep_path_kernel(const __grid_consta
 cudaError_t launch_keep_path(const KeepPathArgs& a, cudaStream_t s) {
     if (a.num_seqs <= 0 || a.num_layers <= 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs), static_cast<unsigned>(2 * a.num_layers));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs),
+                       static_cast<unsigned>(std::min(2 * a.num_layers, (kCtas + a.num_seqs - 1) / a.num_seqs)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
