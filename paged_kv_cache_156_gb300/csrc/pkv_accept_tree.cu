@@ -11,9 +11,10 @@
 // first token whose inclusive sum exceeds floor(u T), exact whatever the order.
 //
 // One cluster of 8 CTAs a sequence, as there: a row is cut into a piece a warp;
-// the CTAs' totals go round through distributed shared memory; the warp that
-// holds the mark reads its batch of 512 weights again, finds the token and hands
-// it to every CTA, each of which looks the child up in its own copy of the tree.
+// the CTAs' totals go round through distributed shared memory, and with them, for
+// each child of the node, the units before its token: whether the walk goes on to
+// a child is then known in every CTA.  Only the walk's last token is searched for,
+// by the warp that holds the mark, which reads its batch of 512 weights again.
 // Rows depend on one another: bound by latency, a row after another.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -41,18 +42,39 @@ constexpr int kCluster = 8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;                           // groups of 128 weights whose loads are in flight together
-constexpr int kMaxBatches = (PKV_ACCEPT_MAX_VOCAB + 3 + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128);
+constexpr int kSpan = kCluster * kWarps * kBatch * 128;       // weights of a batch of every warp
+__host__ __device__ constexpr int batches_of(int weights) { return (weights + kSpan - 1) / kSpan; }
+constexpr int kMaxBatches = batches_of(PKV_ACCEPT_MAX_VOCAB + 3);
+static_assert(kMaxBatches <= 32, "a batch a lane");
 constexpr int kNodes = PKV_TREE_MAX_NODES;
-static_assert(kNodes == 64, "a warp looks a child up two nodes a lane");
+static_assert(kNodes == 64, "a warp looks the children up two nodes a lane");
+
+// Four weights of a row into shared memory, asynchronously.
+template <int BYTES>
+__device__ __forceinline__ void copy_vector(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+// The units of a warp's weights (up to 16 a lane: each half's sum stays below 2^31).
+__device__ __forceinline__ unsigned long long warp_units(uint32_t hi, uint32_t lo) {
+    return join(__reduce_add_sync(0xffffffffu, hi), __reduce_add_sync(0xffffffffu, lo));
+}
 
 template <typename T>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTreeArgs a) {
     __shared__ unsigned long long warp_total[kWarps];
-    __shared__ unsigned long long cta_total[kCluster];       // every CTA's total of the row
-    __shared__ unsigned long long batch_sum[kMaxBatches][kThreads];
+    // (two of each, for the rows in turn: a CTA may still read a row's when another writes the next one's)
+    __shared__ unsigned long long s_total[2][kCluster];      // every CTA's total of the row
+    __shared__ unsigned long long s_before[2][kNodes];       // of a child's token: the units before it in its CTA's piece,
+    __shared__ unsigned long long s_units[2][kNodes];        // and its own
+    __shared__ unsigned long long batch_total[kWarps][kMaxBatches];
+    struct alignas(4 * sizeof(T)) Vector {
+        uint32_t w[Four<T>::kWords];
+    };
+    __shared__ Vector kid_batch[kBatch * kThreads];
     __shared__ int s_parent[kNodes];
     __shared__ int s_draft[kNodes];
-    __shared__ int s_drawn;                                   // the row's token, from the CTA that found it
+    __shared__ int s_owner[kNodes];                           // the warp of the cluster whose piece of the parent's row holds it
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
     const int b = blockIdx.x / kCluster;
@@ -65,6 +87,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
     const int first = __ldcg(a.query_starts + b), end = __ldcg(a.query_starts + b + 1);
     const bool valid = first >= 0 && end >= first && end <= a.num_tokens && end - first <= kNodes;
     const int n = valid ? end - first : 0;
+    // the rows are cut at their boundaries of four: a row's first vector may hold elements before it
+    auto row_of = [&](int r) { return static_cast<const T*>(a.target_probs) + static_cast<int64_t>(r) * V; };
+    auto offset_of = [&](int r) { return static_cast<int>((reinterpret_cast<uintptr_t>(row_of(r)) / sizeof(T)) & 3); };
     if (t < kNodes) {
         int parent = -1, token = -1;
         if (t > 0 && t < n) {
@@ -76,8 +101,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
                 parent = -1;
             }
         }
+        int owner = -1;
+        if (parent >= 0 && token >= 0) {
+            const int off = offset_of(first + parent);
+            owner = (token + off) / (batches_of(V + off) * kBatch * 128);
+        }
         s_parent[t] = parent;
         s_draft[t] = token;
+        s_owner[t] = owner;
     }
     if (!valid && rank == 0 && t == 0) raise_error(a.err, kErrBounds);
     __syncthreads();
@@ -88,11 +119,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
     int node = 0, steps = 0;                        // (the same in every thread of the cluster)
     for (; steps < W && n > 0; ++steps) {
         if (rank == 0 && t == 0) path[steps] = node;
-        const T* row = static_cast<const T*>(a.target_probs) + static_cast<int64_t>(first + node) * V;
+        const T* row = row_of(first + node);
         const float u = __ldcg(a.uniform + first + node);
-        // the row is cut at its boundaries of four: its first vector may hold elements before it
-        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 3);
-        const int batches = (V + off + kCluster * kWarps * kBatch * 128 - 1) / (kCluster * kWarps * kBatch * 128);
+        const int off = offset_of(first + node);
+        const int batches = batches_of(V + off);
         const int piece = (rank * kWarps + warp) * batches * kBatch * 128 - off;
 
         constexpr int kWords = Four<T>::kWords;
@@ -116,7 +146,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) add_units(__saturatef(w[e]), hi, lo);
             }
-            return join(hi, lo);
+            return warp_units(hi, lo);
         };
         auto units_at_ends = [&](int batch) {
             uint32_t hi = 0, lo = 0;
@@ -126,11 +156,40 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) add_units(at_ends(batch, k, e), hi, lo);
             }
-            return join(hi, lo);
+            return warp_units(hi, lo);
         };
 
         // ---- the row's total, two batches in flight: a sequence whose neighbours are through has its SMs to itself, and
         // what its eight warps a CTA have in flight sets its pace
+        // what the pass does not load at once is on its way to L2 meanwhile
+        if (lane == 0) {
+            const uintptr_t from = (reinterpret_cast<uintptr_t>(row + piece + 2 * kBatch * 128) + 15) & ~uintptr_t(15);
+            const uintptr_t upto = reinterpret_cast<uintptr_t>(row + min(piece + batches * kBatch * 128, V)) & ~uintptr_t(15);
+            if (batches > 2 && piece + 2 * kBatch * 128 < V && upto > from)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(static_cast<uint32_t>(upto - from)) : "memory");
+        }
+        // The node's children.  Whether the mark falls on the token of one is known as soon as the totals are, if the units
+        // before that token are, which its warp adds up.  So a row whose token a child drafted needs no search.  Lane l looks
+        // after nodes l and 32 + l.
+        int owner[2];
+        unsigned here[2];                           // the children whose token lies in this warp's piece
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            owner[h] = s_parent[32 * h + lane] == node ? s_owner[32 * h + lane] : -1;
+            here[h] = __ballot_sync(0xffffffffu, owner[h] == rank * kWarps + warp);
+        }
+        // the batch of the first of them is fetched beside the pass
+        const int ahead = here[0] ? __ffs(here[0]) - 1 : here[1] ? 31 + __ffs(here[1]) : -1;
+        const uint32_t saved = smem_u32(kid_batch) + threadIdx.x * sizeof(kid_batch[0]);
+        if (ahead >= 0) {
+            const int kb = (s_draft[ahead] - piece) / (kBatch * 128);
+            if (inside(kb)) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    copy_vector<4 * sizeof(T)>(saved + k * kThreads * static_cast<uint32_t>(sizeof(kid_batch[0])), mine_at + (kb * kBatch + k) * 128);
+            }
+            cp_async_commit();
+        }
         unsigned long long mine = 0;
         int batch = 0;
 #pragma unroll 1
@@ -141,7 +200,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const unsigned long long sum = units_of(p[i]);
-                batch_sum[batch + i][t] = sum;
+                if (lane == 0) batch_total[warp][batch + i] = sum;
                 mine += sum;
             }
         }
@@ -155,107 +214,162 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             } else {
                 sum = units_at_ends(batch);
             }
-            batch_sum[batch][t] = sum;
+            if (lane == 0) batch_total[warp][batch] = sum;
             mine += sum;
         }
-        mine = warp_sum(mine);
+        if (ahead >= 0) cp_async_wait_all();
+        __syncwarp();
+#pragma unroll 1
+        for (unsigned long long m = static_cast<unsigned long long>(here[1]) << 32 | here[0]; m; m &= m - 1) {
+            const int c = __ffsll(m) - 1, kb = (s_draft[c] - piece) / (kBatch * 128);
+            const int at = s_draft[c] - piece - kb * kBatch * 128;            // in its batch
+            uint32_t hi = 0, lo = 0;
+            float x = 0.0f;                         // the token's own weight, in its lane
+#pragma unroll 1
+            for (int k = 0; k < kBatch; ++k) {
+                float w[4];
+                if (c == ahead && inside(kb)) {
+                    const Vector v = kid_batch[k * kThreads + t];
+                    Four<T>::unpack(v.w, w);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = at_ends(kb, k, e);
+                }
+                const int i = at - k * 128 - 4 * lane;            // this lane's weights before it: i of these four
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    add_units(e < i ? __saturatef(w[e]) : 0.0f, hi, lo);
+                    x = e == i ? __saturatef(w[e]) : x;
+                }
+            }
+            unsigned long long before = warp_units(hi, lo);
+            hi = lo = 0;
+            add_units(x, hi, lo);
+            const unsigned long long own = warp_units(hi, lo);
+            for (int i = 0; i < kb; ++i) before += batch_total[warp][i];
+            if (lane == 0) {
+                s_before[steps & 1][c] = before;
+                s_units[steps & 1][c] = own;
+            }
+        }
         if (lane == 0) warp_total[warp] = mine;
         __syncthreads();
         if (warp == 0) {
             const unsigned long long sum = warp_sum(lane < kWarps ? warp_total[lane] : 0ull);
-            if (lane < kCluster) *cluster.map_shared_rank(&cta_total[rank], lane) = sum;
+            if (lane < kCluster) *cluster.map_shared_rank(&s_total[steps & 1][rank], lane) = sum;
+        }
+#pragma unroll 1
+        for (unsigned long long m = static_cast<unsigned long long>(here[1]) << 32 | here[0]; m; m &= m - 1) {
+            const int c = __ffsll(m) - 1;
+            unsigned long long before = s_before[steps & 1][c];
+            const unsigned long long own = s_units[steps & 1][c];
+            for (int v = 0; v < warp; ++v) before += warp_total[v];
+            __syncwarp();
+            if (lane < kCluster) {
+                *cluster.map_shared_rank(&s_before[steps & 1][c], lane) = before;
+                *cluster.map_shared_rank(&s_units[steps & 1][c], lane) = own;
+            }
         }
         cluster.sync();
-        unsigned long long total = 0, before = 0;   // of the row; of what stands before this warp's piece
+        unsigned long long total = 0;               // of the row
+        unsigned long long before = 0, kid[2] = {0, 0};      // of what stands before this CTA's piece; before a lane's children's
 #pragma unroll
         for (int c = 0; c < kCluster; ++c) {
-            const unsigned long long x = cta_total[c];
-            before += c < rank ? x : 0ull;
+            const unsigned long long x = s_total[steps & 1][c];
             total += x;
+            before += c < rank ? x : 0ull;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) kid[h] += c < owner[h] / kWarps ? x : 0ull;
         }
-        int drawn = -1;
-        if (total != 0) {
-            const double z = (u > 0.0f ? static_cast<double>(u) : 0.0) * static_cast<double>(total);
-            const unsigned long long mark = min(__double2ull_rz(z), total - 1);
-            for (int v = 0; v < warp; ++v) before += warp_total[v];
-            if (mark >= before && mark < before + mine) {
-                // the batch that holds the mark: four batches' sums at a time, side by side
-                batch = 0;
-                for (int b0 = 0; b0 < batches; b0 += 4) {
-                    unsigned long long sum[4];
+        if (total == 0) {                           // nothing to draw from
+            if (rank == 0 && t == 0) tokens[steps] = -1;
+            break;
+        }
+        const double z = (u > 0.0f ? static_cast<double>(u) : 0.0) * static_cast<double>(total);
+        const unsigned long long mark = min(__double2ull_rz(z), total - 1);
+        unsigned holds[2];                          // the children whose token holds the mark: the first is gone to
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[e] = b0 + e < batches ? batch_sum[b0 + e][t] : 0ull;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[e] = warp_sum(sum[e]);
-                    bool here = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (here) continue;
-                        batch = b0 + e;
-                        here = mark < before + sum[e];
-                        if (!here) before += sum[e];
-                    }
-                    if (here) break;
-                }
-                float w[kBatch][4];
-                if (inside(batch)) {
-                    uint32_t p[kBatch][kWords];
-                    load(batch, p);
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        Four<T>::unpack(p[k], w[k]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(w[k][e]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[k][e] = at_ends(batch, k, e);
-                }
-                unsigned long long own[kBatch], inc[kBatch];      // a lane's four weights, and up to and with them
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    uint32_t hi = 0, lo = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) add_units(w[k][e], hi, lo);
-                    own[k] = inc[k] = join(hi, lo);
-                }
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const unsigned long long y = __shfl_up_sync(0xffffffffu, inc[k], o);
-                        if (lane >= o) inc[k] += y;
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    unsigned long long at = before + inc[k] - own[k];     // before this lane's four
-                    if (mark >= at && mark < at + own[k]) {
-                        int e = 0;
-#pragma unroll
-                        for (int f = 0; f < 3; ++f) {
-                            uint32_t hi = 0, lo = 0;
-                            add_units(w[k][f], hi, lo);
-                            at += join(hi, lo);
-                            e += mark >= at;
-                        }
-                        const int y = piece + (batch * kBatch + k) * 128 + 4 * lane + e;
-                        for (int c = 0; c < kCluster; ++c) *cluster.map_shared_rank(&s_drawn, c) = y;
-                    }
-                    before += __shfl_sync(0xffffffffu, inc[k], 31);
-                }
+        for (int h = 0; h < 2; ++h) {
+            bool on = owner[h] >= 0;
+            if (on) {
+                const unsigned long long from = kid[h] + s_before[steps & 1][32 * h + lane];
+                on = mark >= from && mark < from + s_units[steps & 1][32 * h + lane];
             }
-            cluster.sync();
-            drawn = s_drawn;
+            holds[h] = __ballot_sync(0xffffffffu, on);
         }
-        if (rank == 0 && t == 0) tokens[steps] = drawn;
-        // the first child that drafted it
-        const unsigned low = __ballot_sync(0xffffffffu, drawn >= 0 && s_parent[lane] == node && s_draft[lane] == drawn);
-        const unsigned high = __ballot_sync(0xffffffffu, drawn >= 0 && s_parent[32 + lane] == node && s_draft[32 + lane] == drawn);
-        if ((low | high) == 0 || steps + 1 == W) break;
-        node = low ? __ffs(low) - 1 : 31 + __ffs(high);
+        const int next = holds[0] ? __ffs(holds[0]) - 1 : holds[1] ? 31 + __ffs(holds[1]) : -1;
+        if (next >= 0) {
+            if (rank == 0 && t == 0) tokens[steps] = s_draft[next];
+            if (steps + 1 == W) break;
+            node = next;
+            continue;
+        }
+        // ---- no child's: the warp whose piece holds the mark finds the token
+        for (int v = 0; v < warp; ++v) before += warp_total[v];
+        if (mark >= before && mark < before + mine) {
+            // the batch that holds the mark
+            unsigned long long sums = lane < batches ? batch_total[warp][lane] : 0ull, upto = sums;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            batch = __ffs(__ballot_sync(0xffffffffu, mark < before + upto)) - 1;
+            before += __shfl_sync(0xffffffffu, upto - sums, batch);
+            float w[kBatch][4];
+            if (inside(batch)) {
+                uint32_t p[kBatch][kWords];
+                load(batch, p);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    Four<T>::unpack(p[k], w[k]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[k][e] = __saturatef(w[k][e]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[k][e] = at_ends(batch, k, e);
+            }
+            // its group of 128, then the lane, then the weight
+            unsigned long long own = 0;             // this lane's units of the group
+            float mine4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            int group = -1;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add_units(w[k][e], hi, lo);
+                const unsigned long long all = warp_units(hi, lo);
+                if (group < 0 && mark < before + all) {
+                    group = k;
+                    own = join(hi, lo);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mine4[e] = w[k][e];
+                }
+                before += group < 0 ? all : 0ull;
+            }
+            unsigned long long inc = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            unsigned long long at = before + inc - own;           // before this lane's four
+            if (mark >= at && mark < at + own) {
+                int e = 0;
+#pragma unroll
+                for (int f = 0; f < 3; ++f) {
+                    uint32_t hi = 0, lo = 0;
+                    add_units(mine4[f], hi, lo);
+                    at += join(hi, lo);
+                    e += mark >= at;
+                }
+                tokens[steps] = piece + (batch * kBatch + group) * 128 + 4 * lane + e;
+            }
+        }
+        break;
     }
     // (steps: the place of the last token written; without nodes nothing was)
     if (rank == 0) {
