@@ -293,6 +293,7 @@ struct PrefillArgs {
     float scale_log2;                // |scale| * log2(e)
     const float* k_scale;            // [num_kv_heads] (E4M3 pools only, else nullptr)
     const float* v_scale;
+    int lone;                        // 1: trees whose tiles are taken one by one (E4M3 pools, few rows a sequence)
     const unsigned long long* tree_mask;     // [num_tokens]: bit j, the token sees node j of its tree (nullptr: causal)
 };
 

@@ -81,7 +81,7 @@ namespace {
 constexpr int kStep = kPrefillStep;
 constexpr int kSub = kPrefillSub;
 
-template <int D, bool KV8 = false, bool TREE = false>
+template <int D, bool KV8 = false, bool TREE = false, bool LONE = false>
 struct PfGeo {
     static constexpr int kThreads = 512;
     static constexpr int kLoadK = 8, kLoadV = 10, kMma = 9, kClean = 12, kLoadQ = KV8 ? 14 : 13, kPlan = 15;   // (9 and 11: MMAs; 12 and 14: cleaning; E4M3: 10, 12 and 13 expand)
@@ -89,20 +89,22 @@ struct PfGeo {
     static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
     static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
     // ring of K and V tiles, in turn; over an E4M3 pool a tile less in favour of two tiles of codes
-    static constexpr int kStages = KV8 ? (TREE ? 3 : 4) : D == 128 ? 5 : 10;
+    static constexpr int kStages = KV8 ? (TREE && !LONE ? 3 : 4) : D == 128 ? 5 : 10;
     static constexpr int kCodes = KV8 ? (TREE ? 3 : 2) : 0;   // staged tiles of codes (128 rows of D bytes)
     static constexpr int kCodeTile = 128 * D;
-    static constexpr int kConverters = 3;                   // warps 10, 12 and 13: on two of the schedulers (10, 12, 14) 120 us, on three 117 (8 chunks of 256 to 512)
-    static constexpr size_t kRing = 2 * size_t(kTile);      // after the two Q tiles
+    static constexpr int kTiles = LONE ? 1 : 2;             // an item's tiles of rows, a softmax warpgroup each
+    static constexpr int kConverters = LONE ? 8 : 3;        // warps 4-7 and 10-13, a trip a tile; else warps 10, 12 and 13: on two of the schedulers (10, 12, 14) 120 us, on three 117 (8 chunks of 256 to 512)
+    static constexpr size_t kRing = kTiles * size_t(kTile); // after the Q tiles
     static constexpr size_t kCode = kRing + size_t(kStages) * kTile;
     static constexpr size_t kBars = kCode + size_t(kCodes) * kCodeTile;
     static constexpr int kItems = 4;                        // items decoded ahead
     static constexpr int kItemReaders = 15;                 // warps that read each
     static constexpr int kNumBars = 3 * kStages + 21 + 2 * kItems + 2 * kCodes;
-    static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, tags [3], epilogues [8]
-    static constexpr size_t kBad = (kMisc + 52 + 15) / 16 * 16;   // first positions of non-finite V elements: [2 warps][+inf, -inf][D], or [3 warps][NaN][D]
-    // a tree's: the nodes that hold them, 64 bits, [+inf, -inf][D] (a warp cleans half the columns), or [3 warps][NaN][D]
-    static constexpr size_t kList = kBad + size_t(TREE && KV8 ? 6 : 4) * D * 4;    // [kItems] decoded items
+    static constexpr int kTags = LONE ? 8 : 3;              // warps that list non-finite V elements, at most
+    static constexpr size_t kMisc = kBars + kNumBars * 8;   // TMEM address, abort flag, tags [kTags], epilogues [8]
+    static constexpr size_t kBad = (kMisc + 40 + 4 * kTags + 15) / 16 * 16;   // first positions of non-finite V elements: [2 warps][+inf, -inf][D], or [3 warps][NaN][D]
+    // a tree's: the nodes that hold them, 64 bits, [+inf, -inf][D] (a warp cleans half the columns), or [kTags][NaN][D]
+    static constexpr size_t kList = kBad + size_t(TREE && KV8 ? 2 * kTags : 4) * D * 4;    // [kItems] decoded items
     static constexpr size_t kBytes = kList + kItems * 64;
     static_assert(!KV8 || D == 128, "E4M3 pools: a row of codes is one 128-byte plane");
     static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
@@ -134,7 +136,8 @@ struct alignas(16) Item {
     int nst[2];                      // steps of each tile
     int lim0;                        // positions every row of the item sees
     int end[2];                      // position after the last one each tile sees in the item
-    int pad[2];
+    int half;                        // (LONE) which of the item's tiles this is
+    int pad;
     __device__ __forceinline__ int steps_of(int i) const { return i ? nst[1] : nst[0]; }
     __device__ __forceinline__ int end_of(int i) const { return i ? end[1] : end[0]; }
     __device__ __forceinline__ int steps() const { return max(nst[0], nst[1]); }
@@ -463,12 +466,13 @@ __device__ __forceinline__ Entry local_entry(const LocalPlan& lp, int e, int kvh
 
 // T: the products' type; KV8: E4M3 pools (codes expanded to f16, every one exact there); OT: q's and out's.
 // TREE: the last n positions are a tree's nodes, of which row (token i, head) sees those of token i's mask.
-template <typename T, int D, bool KV8, typename OT, bool TREE>
-__global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
+// LONE (trees of up to 128 rows over E4M3 pools): an item's tiles are taken one after the other.
+template <typename T, int D, bool KV8, typename OT, bool TREE, bool LONE>
+__global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
                                                                         const __grid_constant__ CUtensorMap tmk,
                                                                         const __grid_constant__ CUtensorMap tmv,
                                                                         const __grid_constant__ PrefillArgs a) {
-    using G = PfGeo<D, KV8, TREE>;
+    using G = PfGeo<D, KV8, TREE, LONE>;
     constexpr int ST = G::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr bool kConvertQ = !std::is_same<T, OT>::value;     // bf16 queries over an E4M3 pool: to f16 in place
@@ -494,8 +498,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
     uint64_t* code_empty = code_full + G::kCodes;   // [kCodes] it is expanded (converter warps)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kMisc + 4);
-    volatile int* epilogues = abort_flag + 4;       // [8] items a softmax warp is through with
-    volatile int* bad_tag = abort_flag + 1;         // [3] the item whose non-finite V elements a warp's table lists (-1: none)
+    volatile int* epilogues = abort_flag + 1 + G::kTags;       // [8] items a softmax warp is through with
+    volatile int* bad_tag = abort_flag + 1;         // [kTags] the item whose non-finite V elements a warp's table lists (-1: none)
     int* bad = reinterpret_cast<int*>(smem + G::kBad);      // (kBad)
     unsigned long long* bad_nodes = reinterpret_cast<unsigned long long*>(smem + G::kBad);      // (TREE)
     static_assert(G::kBad % 8 == 0, "the node masks are 64-bit words");
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], KV8 ? G::kConverters : 1);
-            mbar_init(&empty[i], KV8 ? 2 : 4);
+            mbar_init(&empty[i], KV8 ? G::kTiles : 4);
             mbar_init(&clean[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -528,9 +532,9 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
             mbar_init(&code_full[i], 1);
             mbar_init(&code_empty[i], G::kConverters);
         }
-        mbar_init(fin, 2);
+        mbar_init(fin, G::kTiles);
         for (int i = 0; i < 8; ++i) epilogues[i] = 0;
-        bad_tag[0] = bad_tag[1] = bad_tag[2] = -1;
+        for (int i = 0; i < G::kTags; ++i) bad_tag[i] = -1;
         // the 128B swizzle and the MMA descriptors assume 1 KB aligned tiles
         const bool misaligned = (smem_u32(smem) & 1023u) != 0;
         if (misaligned) raise_error(a.err, kErrTimeout);
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
     auto table_free = [&](int r) {
         const unsigned long long t0 = globaltimer_ns();
         for (;;) {
-            if (!__any_sync(0xffffffffu, lane < 8 && epilogues[lane] < r)) break;
+            if (!__any_sync(0xffffffffu, lane < 4 * G::kTiles && epilogues[lane] < r)) break;
             if (__any_sync(0xffffffffu, *abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) return false;
             __nanosleep(200);
         }
@@ -588,7 +592,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
         return true;
     };
 
-    if (warp >= 8) {
+    if (warp >= 4 * G::kTiles) {
         regs_dec<G::kRegsOther>();
         if (KV8 && warp == G::kLoadK) {
             // ======================================================== tiles of E4M3 codes, K and V in turn
@@ -638,13 +642,13 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                 const unsigned long long t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
             }
-        } else if (KV8 && (warp == G::kLoadV || warp == G::kClean || warp == G::kClean + 1)) {
+        } else if (KV8 && (warp == G::kLoadV || warp == G::kClean || warp == G::kClean + 1 || (LONE && (warp < 8 || warp == G::kMma + 2)))) {
             // ======================================================== codes to f16, V cleaned on the way
             // A lane takes 16 codes, 32 bytes of f16 in one column plane.  A load or store instruction covers
             // eight rows by four lanes a row, and every eight lanes two rows whose numbers differ in bits 0
             // and 2 (q and q ^ 5): the swizzles then put the eight pieces into different banks both times.  A
             // lane's row in a group of eight, and so its swizzle, never changes: addresses advance by 1 KB.
-            const int cw = warp == G::kLoadV ? 0 : warp - G::kClean + 1;
+            const int cw = LONE ? (warp < 8 ? warp - 4 : warp - 6) : warp == G::kLoadV ? 0 : warp - G::kClean + 1;
             [[maybe_unused]] int* mine = bad + cw * D;
             const int l3 = lane & 3, rl = (lane >> 3) ^ ((lane >> 2) & 1 ? 5 : 0);
             Ring<ST> c;
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                 const unsigned long long t0 = globaltimer_ns();       // copies in flight land before the CTA ends
                 while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
             }
-        } else if (warp == G::kMma || warp == G::kMma + 2) {
+        } else if (warp == G::kMma || (!LONE && warp == G::kMma + 2)) {
             // ======================================================== one warp a tile issues its MMAs
             // The warp runs the control flow together and one elected lane issues.  These warps run a few
             // hundred instructions a step between the softmax warps' thousands on the same schedulers, so
@@ -817,6 +821,61 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                 // S = Q K^T, or -Q K^T where scale and K's scale together are negative (the softmax takes their magnitude)
                 uint32_t id_s = kIdS;
                 if (KV8 && __ldcg(a.k_scale + it.kvh) < 0.0f) id_s ^= tc::kNegateA;
+                if constexpr (LONE) {
+                    // S of the next step before this step's P: into the other tile's columns, so that it runs under the
+                    // softmax.  (That buffer's last P is read by a product issued before: in order.)
+                    for (int j = -1; j < n; ++j) {
+                        Ring<ST> v = c;                      // this step's V (c: its K; in round -1 the first K)
+                        if (j >= 0) v.next();
+                        Ring<ST> k = v;
+                        if (j >= 0) k.next();
+                        if (j + 1 < n) {
+                            ok = wait(&full[k.slot], k.phase);
+                            if (ok && j < 0) {
+                                ok = wait(&q_full[0], nq);
+                                nq ^= 1u;
+                            }
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            if (leader) {
+                                const uint64_t d = dk + static_cast<uint64_t>(k.slot * (G::kTile >> 4));
+                                const uint32_t to_s = ts + ((j + 1) & 1) * 128;
+#pragma unroll
+                                for (int ks = 0; ks < D / 16; ++ks) {
+                                    const uint64_t off = ((ks >> 2) * G::kPlane + (ks & 3) * 32) >> 4;
+                                    tc::mma_ss(to_s, dq + off, d + off, id_s, ks > 0);
+                                }
+                                tc::commit(&s_full[(j + 1) & 1]);
+                                tc::commit(&empty[k.slot]);
+                                if (j + 2 == n) tc::commit(&q_empty[0]);
+                            }
+                        }
+                        if (j < 0) continue;
+                        const int b = j & 1, left = it.end_of(0) - (it.step0 + j) * kStep;
+                        const uint64_t d = dv + static_cast<uint64_t>(v.slot * (G::kTile >> 4));
+                        ok = wait(&full[v.slot], v.phase);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && wait(&p_full[2 * b + half], np >> b & 1u);
+                            tc::fence_after_sync();
+                            if (ok && leader) {
+#pragma unroll
+                                for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                    if (kk * 16 < left)      // (16 a product, none wholly past the end)
+                                        tc::mma_ts(to, ts + b * 128 + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                            }
+                        }
+                        np ^= 1u << b;
+                        if (!ok) break;
+                        if (leader) {
+                            tc::commit(&o_step[0]);
+                            if (j == n - 1) tc::commit(&o_full[0]);
+                            tc::commit(&empty[v.slot]);
+                        }
+                        c = k;
+                    }
+                    continue;
+                }
                 // round j: O += P V of step j, then S of step j + 1 (round -1: the first S alone)
 #pragma unroll 1
                 for (int j = -1; j < n; ++j) {
@@ -930,8 +989,9 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
             if (leader && a.q_tma) prefetch_tensormap(&tmq);
             for (int r = 0; ok && get_item(r, it, ok); ++r) {
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < G::kTiles; ++i) {
                     if (it.steps_of(i) == 0) continue;
+                    const int sub = LONE ? it.half : i;
                     ok = wait_bar(&q_empty[i], (ph >> i) & 1u, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     ph ^= 1u << i;
@@ -940,7 +1000,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                     if (a.q_tma) {
                         // (rows of the box past the item's are other tokens' queries, or zeros past the last:
                         // their scores go nowhere)
-                        const int tok = it.qs + (2 * it.tile + i) * sub_tokens;
+                        const int tok = it.qs + (2 * it.tile + sub) * sub_tokens;
                         if (leader) {
                             uint64_t* bar = kConvertQ ? &q_raw[i] : &q_full[i];
                             mbar_arrive_expect_tx(bar, G::kTile);
@@ -949,7 +1009,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                                 tma_load_4d(dst + hf * G::kPlane, &tmq, hf * 64, it.kvh * a.group, tok, 0, bar);
                         }
                     } else {
-                        copy_q<T, D>(a, it, i, smem_u32(dst));
+                        copy_q<T, D>(a, it, sub, smem_u32(dst));
                         if (leader) mbar_arrive(kConvertQ ? &q_raw[i] : &q_full[i]);
                     }
                 }
@@ -984,18 +1044,36 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                 next.live = static_cast<int>(blockIdx.x) < total;
             }
             bool ok = !*abort_flag, more = true;
+            [[maybe_unused]] Item whole;
+            [[maybe_unused]] int entries = 0;
+            [[maybe_unused]] bool second = false;            // (LONE: the item's second tile follows)
             for (int r = 0; ok && more; ++r) {
                 const int k = r % G::kItems;
                 Item it;
-                more = next.live;
-                if (more) {
-                    read_item<TREE>(a, next, it);
-                    if (!a.local) next = fetch_entry(a, total, r + 1);
-                    else if (r < 31) next = round_entry(r + 1);
-                    else next.live = false;
+                if (LONE && second) {
+                    it = whole;
+                    it.half = 1;
+                    it.nst[0] = it.nst[1];
+                    it.end[0] = it.end[1];
+                    second = false;
                 } else {
-                    it.rows = -1;
+                    more = next.live;
+                    if (more) {
+                        read_item<TREE>(a, next, it);
+                        const int entry = LONE ? ++entries : r + 1;
+                        if (!a.local) next = fetch_entry(a, total, entry);
+                        else if (entry < 32) next = round_entry(entry);
+                        else next.live = false;
+                        if constexpr (LONE) {
+                            it.half = 0;
+                            whole = it;
+                            second = it.rows > kSub;
+                        }
+                    } else {
+                        it.rows = -1;
+                    }
                 }
+                if constexpr (LONE) it.nst[1] = it.end[1] = 0;
                 ok = wait_bar(&item_empty[k], ((r / G::kItems) & 1) ^ 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -1126,14 +1204,16 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
         const int wg = warp >> 2;
         const int t = threadIdx.x & 127;
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t ts = tl + G::kColS + wg * 128, to = tl + G::kColO + wg * D, tp = tl + G::kColP + wg * G::kStrideP;
+        uint32_t ts = tl + G::kColS + wg * 128, tp = tl + G::kColP + wg * G::kStrideP;
+        const uint32_t to = tl + G::kColO + wg * D;
         OT* out = static_cast<OT*>(a.out);
-        unsigned ns = 0, no = 0, nraw = 0, nstep = 0;
+        unsigned ns = 0, no = 0, nraw = 0, nstep = 0;       // (LONE: ns holds a parity bit for each S buffer)
         Item it;
         bool ok = !*abort_flag;
 #pragma unroll 1
         for (int r = 0; ok && get_item(r, it, ok); ++r) {
-            const int myrow = wg * kSub + t;                 // row of the item
+            const int sub = LONE ? it.half : wg;             // the tile
+            const int myrow = sub * kSub + t;                // row of the item
             const bool has = myrow < it.rows;
             const int rr = it.tile * kPrefillRows + myrow, tok = pf::div(rr, a.by_group);
             const int at = has ? (it.qs + tok) * a.num_heads + it.kvh * a.group + (rr - tok * a.group) : -1;   // row of out
@@ -1142,7 +1222,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
             const int n = it.steps_of(wg);
             // the warp has no row of the item: single tokens beside prompts leave most warps without (177 -> 175 us for 60
             // of them beside 4 chunks; at head_dim 64 the code more cost 4%)
-            const bool idle = wg * kSub + (warp & 3) * 32 >= it.rows;
+            const bool idle = sub * kSub + (warp & 3) * 32 >= it.rows;
             const int seen = min(lim, it.end_of(wg));           // (dummy rows too stop at the tile's end)
             // TREE: the nodes the row sees (dummy rows: all), none after its own nor of a position below 0
             const int past = it.L - it.n;
@@ -1188,15 +1268,23 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                 }
             }
             for (int j = 0; j < n; ++j) {
-                ok = wait_bar(&s_full[wg], ns & 1, abort_flag);
+                const int sb = LONE ? j & 1 : wg;            // S's buffer
+                if constexpr (LONE) {
+                    ts = tp = tl + G::kColS + sb * 128;
+                    ok = wait_bar(&s_full[sb], ns >> sb & 1u, abort_flag);
+                    ns ^= 1u << sb;
+                } else {
+                    ok = wait_bar(&s_full[wg], ns & 1, abort_flag);
+                    ++ns;
+                }
                 ok = __all_sync(0xffffffffu, ok);
-                ++ns;
                 if (!ok) break;
                 tc::fence_after_sync();
                 if constexpr (!G::kOwnP) {
                     if (idle) {                              // (what P holds there reaches rows of no token alone)
-                        mbar_arrive(&p_full[2 * wg]);
-                        mbar_arrive(&p_full[2 * wg + 1]);
+                        mbar_arrive(&p_full[2 * sb]);
+                        mbar_arrive(&p_full[2 * sb + 1]);
+                        if (LONE && j > 0) ++nstep;
                         continue;
                     }
                 }
@@ -1253,8 +1341,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                     if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - top);
                     m_ref = top;
                 }
-                if constexpr (G::kOwnP) {
-                    // the last step's O product reads P's columns and writes O
+                if constexpr (G::kOwnP || LONE) {
+                    // the last step's O product reads P's columns (kOwnP) and writes O
                     if (j > 0) {
                         ok = wait_bar(&o_step[wg], nstep & 1, abort_flag);
                         ok = __all_sync(0xffffffffu, ok);
@@ -1308,7 +1396,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                     if (!G::kOwnP || h == 1) {
                         tc::wait_st();
                         tc::fence_before_sync();
-                        mbar_arrive(&p_full[2 * wg + (G::kOwnP ? 0 : h)]);
+                        mbar_arrive(&p_full[2 * sb + (G::kOwnP ? 0 : h)]);
                     }
                 }
                 const float2 sm = unpack64(add2(sum0, sum1));
@@ -1321,7 +1409,7 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
             const int64_t slot = static_cast<int64_t>(it.kvh) * a.part_cap + (it.split >> 16) + ((it.split >> 8) & 255);
             float4* prow = a.part_o + slot * (D / 4) * a.part_rows + myrow;      // [column / 4][row]
             if (n > 0) {
-                if (G::kOwnP) ++nstep;                       // (the last step's, of which this is the completion)
+                if (G::kOwnP || LONE) ++nstep;               // (the last step's, of which this is the completion)
                 ok = wait_bar(&o_full[wg], no & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 ++no;
@@ -1387,16 +1475,18 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kern
                 // infinity or NaN of its own from a position that every row sees
                 const bool bad0 = __any_sync(0xffffffffu, bad_tag[0] == r), bad1 = __any_sync(0xffffffffu, bad_tag[1] == r),
                            bad2 = KV8 && __any_sync(0xffffffffu, bad_tag[2] == r);
-                if (bad0 || bad1 || bad2) {
+                [[maybe_unused]] unsigned bads = 0;          // the warps that list some (TREE over E4M3 pools)
+                if constexpr (TREE && KV8) bads = __ballot_sync(0xffffffffu, lane < G::kTags && bad_tag[min(lane, G::kTags - 1)] == r);
+                if (bads || bad0 || bad1 || bad2) {
                     __syncwarp();
 #pragma unroll 1
                     for (int c = 0; c < D; ++c) {
                         bool up, down;
                         if constexpr (TREE) {
                             if constexpr (KV8) {
-                                up = (bad0 && (bad_nodes[c] & nodes)) || (bad1 && (bad_nodes[D + c] & nodes)) ||
-                                     (bad2 && (bad_nodes[2 * D + c] & nodes));
-                                down = up;
+                                unsigned long long listed = 0ull;
+                                for (unsigned m = bads; m; m &= m - 1) listed |= bad_nodes[(__ffs(m) - 1) * D + c];
+                                up = down = (listed & nodes) != 0ull;
                             } else {
                                 const bool listed = c < D / 2 ? bad0 : bad1;
                                 up = listed && (bad_nodes[c] & nodes);
@@ -1548,12 +1638,12 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
     }
 }
 
-template <typename T, int D, bool KV8, typename OT, bool TREE>
+template <typename T, int D, bool KV8, typename OT, bool TREE, bool LONE = false>
 cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                      cudaStream_t s) {
-    using G = PfGeo<D, KV8, TREE>;
+    using G = PfGeo<D, KV8, TREE, LONE>;
     static_assert(G::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
-    auto kern = prefill_kernel<T, D, KV8, OT, TREE>;
+    auto kern = prefill_kernel<T, D, KV8, OT, TREE, LONE>;
     // once a device: the shared memory, and that the warpgroups' register split fits what a block is launched with
     // (or it would wait for ever)
     static std::atomic<uint64_t> ready{0};
@@ -1591,6 +1681,9 @@ template <bool TREE>
 cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype,
                    int head_dim, cudaStream_t s) {
     using bf16 = __nv_bfloat16;
+    if (TREE && a.k_scale && a.lone)
+        return dtype == 0 ? launch_t<__half, 128, true, __half, true, true>(a, tmq, tmk, tmv, s)
+                          : launch_t<__half, 128, true, bf16, true, true>(a, tmq, tmk, tmv, s);
     if (a.k_scale)
         return dtype == 0 ? launch_t<__half, 128, true, __half, TREE>(a, tmq, tmk, tmv, s)
                           : launch_t<__half, 128, true, bf16, TREE>(a, tmq, tmk, tmv, s);
