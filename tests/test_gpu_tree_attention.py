@@ -240,6 +240,54 @@ def test_e4m3_codes_a_node_does_not_see():
                     assert same(got[r], clean[r]), (s, i)
 
 
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("totals", [[100, 33, 200], [9000, 140, 4000], [64, 1, 70]])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_e4m3_one_tree_larger_than_the_rest(dtype, totals, planned):
+    """Few rows a sequence on average, but one of two tiles: over E4M3 pools its tiles follow one another; split tiles,
+    trees shorter than the rest's, sequences without nodes."""
+    news = [64, 1, 33, 0, 2, 1, 1, 1, 3, 1, 1, 1, 1]
+    totals = totals + [0 if n == 0 else n + 130 * i for i, n in enumerate(news[3:])]
+    b = build(news, totals, 8, 2, 128, 16, dtype, seed=60, pad_rows=2, e4m3=True)
+    mask, _ = masks(news, 61, pad_rows=2)
+    ref, bound = reference(b, mask, torch.float16)
+    c, kw = b.to("cuda"), {}
+    if planned:
+        ws = pkv.alloc_prefill_workspace(len(news), c.q.shape[0], 8, 2, 128)
+        pkv.prefill_plan(ws, c.lens, c.starts, c.q.shape[0], 8, 2, 128, c.max_len)
+        kw = dict(workspace=ws, planned=True)
+    out = run(c, mask, **kw)
+    torch.cuda.synchronize()
+    check(out, ref, bound)
+
+
+def test_e4m3_bad_codes_over_many_items():
+    """Many small trees, NaN codes in some of them: no other tree's output changes, nor a node's that does not see them."""
+    news = [(5 * i) % 16 + 1 for i in range(260)]
+    totals = [n + (37 * i) % 300 for i, n in enumerate(news)]
+    b = build(news, totals, 16, 8, 128, 16, "bf16", seed=62, e4m3=True)
+    mask, _ = masks(news, 63)
+    ref, bound = reference(b, mask, torch.float16)
+    clean = run(b.to("cuda"), mask)
+    check(clean, ref, bound)
+    r, bad = random.Random(64), {}
+    for s in range(0, 260, 3):
+        j = r.randrange(news[s])
+        pos = totals[s] - news[s] + j
+        h, c = r.randrange(8), r.randrange(128)
+        b.vc[int(b.tables[s, pos // 16]), pos % 16, h, c] = r.choice([0x7f, 0xff])
+        bad[s] = (j, h, c)
+    got, clean = run(b.to("cuda"), mask).float().cpu(), clean.float().cpu()
+    for s in range(260):
+        for i in range(news[s]):
+            row = int(b.starts[s]) + i
+            if s in bad and int(mask[row]) >> bad[s][0] & 1:
+                _, h, c = bad[s]
+                assert torch.isnan(got[row, 2 * h:2 * h + 2, c]).all()
+                got[row, 2 * h:2 * h + 2, c] = clean[row, 2 * h:2 * h + 2, c]
+            assert torch.equal(got[row], clean[row]), (s, i)
+
+
 def test_all_visible_scores_minus_infinity():
     """A node all of whose visible scores are -inf is NaN, in split tiles too; one that sees a finite score beside them is
     not."""
