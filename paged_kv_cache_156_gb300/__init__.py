@@ -291,7 +291,7 @@ def paged_kv_append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping,
         dev, dt, pool, kdt = key_cache.get_device(), key_cache.dtype, key_cache.shape, k.dtype
         kv8 = dt is torch.uint8
         T, h, d = k.shape if k.dim() == 3 else (0, 0, 0)
-        if T > 1 and type(v) is type(q) is type(q_out) is _Tensor and len(pool) == 4 and pool[2] == h and \
+        if T > 0 and type(v) is type(q) is type(q_out) is _Tensor and len(pool) == 4 and pool[2] == h and \
                 pool[3] == d and k.get_device() == v.get_device() == q.get_device() == q_out.get_device() == dev and \
                 (kv8 or dt is kdt) and v.dtype is q.dtype is q_out.dtype is kdt and kdt in _DT and value_cache.dtype is dt and \
                 value_cache.shape == pool and v.shape == (T, h, d) and slot_mapping.dtype is torch.int64 and \
@@ -305,8 +305,8 @@ def paged_kv_append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping,
                     ks[2] == vs[2] == qs[2] == os_[2] == 1 and ks[1] == vs[1] == qs[1] == os_[1] == d:
                 return _check(load().pkv_paged_kv_append_rotary(
                     q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-                    slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T, os_[0], qs[0], ks[0], vs[0],
-                    *cos_sin.shape, 1 if interleaved else 0, pool[0], pool[1], rows[1], h, d, _DT[kdt], _POOL_DT[dt],
+                    slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T,
+                    *((os_[0], qs[0], ks[0], vs[0]) if T > 1 else (rows[1] * d, rows[1] * d, h * d, h * d)), *cos_sin.shape, 1 if interleaved else 0, pool[0], pool[1], rows[1], h, d, _DT[kdt], _POOL_DT[dt],
                     k_scale.data_ptr() if kv8 else None, v_scale.data_ptr() if kv8 else None, _stream(key_cache)))
     _append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved, k_scale, v_scale)
 

@@ -319,6 +319,38 @@ def test_scales(scale, e4m3):
     check(out, ref, bound, f"scale {scale}")
 
 
+@pytest.mark.parametrize("nodes", [20, 64])
+def test_e4m3_zero_scales(nodes):
+    """A KV head whose K scale is zero weighs every visible position alike; a zero V scale gives zeros."""
+    news, totals = [nodes] * 3, [nodes, 700, 300]
+    b = build(news, totals, 16, 4, 128, 16, "f16", seed=11, e4m3=True)
+    b.k_scale[1] = 0.0
+    b.v_scale[2] = 0.0
+    mask, _ = masks(news, 12)
+    ref, bound = reference(b, mask, torch.float16)
+    out = run(b.to("cuda"), mask)
+    torch.cuda.synchronize()
+    check(out, ref, bound)
+    assert not out[:, 8:12].any()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_of_larger_tensors(e4m3):
+    """q and out are rows of larger tensors; a group that no TMA box fits (24 rows a token)."""
+    news, totals = [5, 1, 9], [400, 30, 9]
+    b = build(news, totals, 24, 1, 128, 32, "bf16", seed=17, e4m3=e4m3)
+    mask, _ = masks(news, 18)
+    ref, bound = reference(b, mask, torch.float16 if e4m3 else None)
+    c = b.to("cuda")
+    wide_q, wide_out = (torch.full((40, 24, 128), math.nan, dtype=c.q.dtype, device="cuda") for _ in range(2))
+    wide_q[7:22] = c.q
+    pkv.paged_attention_tree(wide_out[7:22], wide_q[7:22], c.kc, c.vc, c.tables, c.lens, c.starts, mask.cuda(), c.scale,
+                             max_seq_len=c.max_len, k_scale=c.k_scale, v_scale=c.v_scale)
+    torch.cuda.synchronize()
+    check(wide_out[7:22], ref, bound)
+    assert torch.isnan(wide_out[:7]).all() and torch.isnan(wide_out[22:]).all()
+
+
 def test_plans_are_shared_with_the_prefill_call():
     """prefill_plan's plan serves a step's layers; another mask over the same plan is another answer."""
     news, totals = [1, 60, 3, 0, 33], [3000, 900, 3, 40, 77]
