@@ -164,9 +164,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             return warp_units(hi, lo);
         };
 
-        // ---- the row's total, two batches in flight: a sequence whose neighbours are through has its SMs to itself, and
-        // what its eight warps a CTA have in flight sets its pace
-        // what the pass does not load at once is on its way to L2 meanwhile
+        // what the pass below does not load at once is on its way to L2 meanwhile
         if (lane == 0) {
             const uintptr_t from = (reinterpret_cast<uintptr_t>(row + piece + 2 * kBatch * 128) + 15) & ~uintptr_t(15);
             const uintptr_t upto = reinterpret_cast<uintptr_t>(row + min(piece + batches * kBatch * 128, V)) & ~uintptr_t(15);
@@ -195,6 +193,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             }
             cp_async_commit();
         }
+        // ---- the row's total, two batches in flight: a sequence whose neighbours are through has its SMs to itself, and
+        // what its eight warps a CTA have in flight sets its pace
         unsigned long long mine = 0;
         int batch = 0;
 #pragma unroll 1

@@ -103,7 +103,8 @@ struct PfGeo {
     static constexpr int kHalves = D * 2 / 128;             // 128-byte column planes of a tile
     static constexpr int kPlane = 128 * 128;                // bytes of a plane: 128 rows
     static constexpr int kTile = kHalves * kPlane;          // a K, V or Q tile
-    // ring of K and V tiles, in turn; over an E4M3 pool a tile less in favour of two tiles of codes
+    // ring of K and V tiles, in turn; over an E4M3 pool a tile less in favour of two tiles of codes (a tree's words of nodes
+    // leave no room for those: three of each)
     static constexpr int kStages = KV8 ? (TREE && !LONE ? 3 : 4) : D == 128 ? 5 : 10;
     static constexpr int kCodes = KV8 ? (TREE ? 3 : 2) : 0;   // staged tiles of codes (128 rows of D bytes)
     static constexpr int kCodeTile = 128 * D;

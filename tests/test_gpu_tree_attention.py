@@ -412,6 +412,29 @@ def test_captured_and_replayed_on_new_inputs():
         assert same(outs[0], outs[1])
 
 
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, give what they give one after the other: both pool types, few rows
+    and many."""
+    shapes = [([30, 1, 64], [900, 3000, 64], 8, 2, False), ([26] * 6, [26 + 700 * i for i in range(6)], 8, 2, True),
+              ([64, 50], [6000, 1200], 16, 2, True)]
+    bs = [build(news, totals, hq, hk, 128, 16, "bf16", seed=13 + i, e4m3=e).to("cuda")
+          for i, (news, totals, hq, hk, e) in enumerate(shapes)]
+    ms = [masks(news, 70)[0].cuda() for news, *_ in shapes]
+    want = [run(b, m) for b, m in zip(bs, ms)]
+    streams = [torch.cuda.Stream() for _ in bs]
+    spaces = [pkv.alloc_prefill_workspace(len(b.lens), b.q.shape[0], b.q.shape[1], 2, 128) for b in bs]
+    outs = [[torch.full_like(b.q, math.nan) for _ in range(8)] for b in bs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for b, m, s, ws, out in zip(bs, ms, streams, spaces, outs):
+            with torch.cuda.stream(s):
+                pkv.paged_attention_tree(out[i], b.q, b.kc, b.vc, b.tables, b.lens, b.starts, m, b.scale, max_seq_len=b.max_len,
+                                         workspace=ws, k_scale=b.k_scale, v_scale=b.v_scale)
+    torch.cuda.synchronize()
+    for w, out in zip(want, outs):
+        assert all(same(o, w) for o in out)
+
+
 def test_on_another_stream_and_without_a_workspace():
     news = [50, 1]
     b = build(news, [300, 2000], 4, 2, 64, 8, "f16", seed=50)
