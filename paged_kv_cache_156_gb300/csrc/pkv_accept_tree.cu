@@ -16,15 +16,16 @@
 // a child is then known in every CTA.  Only the walk's last token is searched for,
 // by the warp that holds the mark, which reads its batch of 512 weights again.
 // Rows depend on one another: bound by latency, a row after another.  64 trees of
-// 16 over 128000 float32 tokens: 27.6 us, of which the longest path's five or six
-// rows take 4.5 us each and the first, with every sequence at work, 4 us more (30.3
-// with a search after every row; two batches in flight a thread instead of one took
-// 5 us off that, an asynchronous ring of eleven vectors put 11 on).  One tree over
-// 32000 float16 tokens: 6.5 us.
+// 16 over 128000 float32 tokens: 26.7 us, of which the longest path's five or six
+// rows take 4 us each (1.8 us of loads, the rest the totals, their exchange and the
+// decision).  One batch in flight a thread instead of four took 35 us, a search after
+// every row 30; an asynchronous ring of eleven vectors, waited for one by one, 46; a
+// child's row prefetched in hope 28 to 30.  One tree over 32000 float16 tokens: 6.4 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/pkv.h"
@@ -57,7 +58,8 @@ static_assert(kNodes == 64, "a warp looks the children up two nodes a lane");
 // Four weights of a row into shared memory, asynchronously.
 template <int BYTES>
 __device__ __forceinline__ void copy_vector(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+    if constexpr (BYTES == 16) cp_async_16(dst, src);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 // The units of a warp's weights (up to 16 a lane: each half's sum stays below 2^31).
@@ -76,7 +78,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
     struct alignas(4 * sizeof(T)) Vector {
         uint32_t w[Four<T>::kWords];
     };
-    __shared__ Vector kid_batch[kBatch * kThreads];
+    // a thread's own places: the vectors of two batches, and of a child's
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    Vector* later = reinterpret_cast<Vector*>(dynamic);
+    Vector* kid_batch = later + 2 * kBatch * kThreads;
     __shared__ int s_parent[kNodes];
     __shared__ int s_draft[kNodes];
     __shared__ int s_owner[kNodes];                           // the warp of the cluster whose piece of the parent's row holds it
@@ -164,12 +169,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             return warp_units(hi, lo);
         };
 
-        // what the pass below does not load at once is on its way to L2 meanwhile
-        if (lane == 0) {
-            const uintptr_t from = (reinterpret_cast<uintptr_t>(row + piece + 2 * kBatch * 128) + 15) & ~uintptr_t(15);
-            const uintptr_t upto = reinterpret_cast<uintptr_t>(row + min(piece + batches * kBatch * 128, V)) & ~uintptr_t(15);
-            if (batches > 2 && piece + 2 * kBatch * 128 < V && upto > from)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(static_cast<uint32_t>(upto - from)) : "memory");
+        // the third and fourth batch come by way of shared memory, so that four are in flight (128000 float32 tokens: all)
+        const bool more = batches >= 4 && inside(2) && inside(3);
+        if (more) {
+#pragma unroll
+            for (int k = 0; k < 2 * kBatch; ++k)
+                copy_vector<4 * sizeof(T)>(smem_u32(later + k * kThreads + t), mine_at + (2 * kBatch + k) * 128);
+            cp_async_commit();
         }
         // The node's children.  Whether the mark falls on the token of one is known as soon as the totals are, if the units
         // before that token are, which its warp adds up.  So a row whose token a child drafted needs no search.  Lane l looks
@@ -193,8 +199,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             }
             cp_async_commit();
         }
-        // ---- the row's total, two batches in flight: a sequence whose neighbours are through has its SMs to itself, and
-        // what its eight warps a CTA have in flight sets its pace
+        // ---- the row's total, two batches in flight and two on their way: a sequence whose neighbours are through has its
+        // SMs to itself, and what its eight warps a CTA have in flight sets its pace
         unsigned long long mine = 0;
         int batch = 0;
 #pragma unroll 1
@@ -207,6 +213,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
                 const unsigned long long sum = units_of(p[i]);
                 if (lane == 0) batch_total[warp][batch + i] = sum;
                 mine += sum;
+            }
+            if (batch == 0 && more) {
+                cp_async_wait_all();
+                batch = 2;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const Vector v = later[(i * kBatch + k) * kThreads + t];
+                        float w[4];
+                        Four<T>::unpack(v.w, w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) add_units(__saturatef(w[e]), hi, lo);
+                    }
+                    const unsigned long long sum = warp_units(hi, lo);
+                    if (lane == 0) batch_total[warp][batch + i] = sum;
+                    mine += sum;
+                }
             }
         }
 #pragma unroll 1
@@ -389,6 +414,17 @@ cudaError_t launch(const AcceptTreeArgs& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * kCluster);
     cfg.blockDim = dim3(kThreads);
+    constexpr int kShared = 3 * kBatch * kThreads * 4 * sizeof(T);
+    cfg.dynamicSmemBytes = kShared;
+    static std::atomic<uint64_t> ready{0};          // devices on which the kernel may take that much
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+        e = cudaFuncSetAttribute(accept_tree_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
