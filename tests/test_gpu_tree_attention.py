@@ -240,6 +240,36 @@ def test_e4m3_codes_a_node_does_not_see():
                     assert same(got[r], clean[r]), (s, i)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("nodes,heads,kv_heads,block", [(16, 16, 2, 8), (32, 4, 1, 32), (5, 9, 3, 16), (25, 10, 2, 8), (64, 4, 2, 32),
+                                                         (1, 64, 8, 16), (2, 128, 2, 8), (3, 40, 1, 32)])
+def test_e4m3_trees_of_one_size(nodes, heads, kv_heads, block, dtype):
+    """Up to 128 rows a KV head and sequence: one tile each, over one to many steps, with nodes on either side of a step's
+    and a block's end, caches shorter than the tree, and positions that are not there."""
+    totals = [nodes, 0, nodes // 2, 127, 128, 129, 128 + nodes, 256, 257, 256 + nodes // 2, 383, 640, 1000, 2500, 4096, 4097]
+    news = [nodes] * len(totals)
+    b = build(news, totals, heads, kv_heads, 128, block, dtype, seed=nodes, pad_rows=len(totals), e4m3=True)
+    mask, _ = masks(news, nodes, pad_rows=len(totals))
+    ref, bound = reference(b, mask, torch.float16)
+    out = run(b.to("cuda"), mask)
+    torch.cuda.synchronize()
+    print(f"{check(out, ref, bound):.3f} of the bound")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_more_sequences_than_a_plan_chunk(e4m3):
+    """More than 1024 sequences (the plan kernel reloads them in chunks), some without nodes."""
+    r = random.Random(1)
+    news = [r.randint(0, 5) for _ in range(1500)]
+    totals = [n + r.randint(0, 300) for n in news]
+    b = build(news, totals, 4, 2, 128, 16, "bf16", seed=60, e4m3=e4m3)
+    mask, _ = masks(news, 61)
+    ref, bound = reference(b, mask, torch.float16 if e4m3 else None)
+    out = run(b.to("cuda"), mask)
+    torch.cuda.synchronize()
+    check(out, ref, bound)
+
+
 @pytest.mark.parametrize("planned", [False, True])
 @pytest.mark.parametrize("totals", [[100, 33, 200], [9000, 140, 4000], [64, 1, 70]])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
