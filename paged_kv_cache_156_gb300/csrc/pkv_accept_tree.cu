@@ -10,11 +10,12 @@
 // The draw is the one of pkv_accept.cu: weights in whole units of 2^-44, the
 // first token whose inclusive sum exceeds floor(u T), exact whatever the order.
 //
-// One cluster of 8 CTAs a sequence, as there: a row is cut into a piece a warp;
-// the CTAs' totals go round through distributed shared memory, and with them, for
-// each child of the node, the units before its token: whether the walk goes on to
-// a child is then known in every CTA.  Only the walk's last token is searched for,
-// by the warp that holds the mark, which reads its batch of 512 weights again.
+// One cluster of 8 CTAs a sequence, as there (one CTA over small vocabularies): a
+// row is cut into a piece a warp; the CTAs' totals go round through distributed
+// shared memory, and with them, for each child of the node, the units before its
+// token: whether the walk goes on to a child is then known in every CTA.  Only the
+// walk's last token is searched for, by the warp that holds the mark, which reads
+// its batch of 512 weights again.
 // Rows depend on one another: bound by latency, a row after another.  64 trees of
 // 16 over 128000 float32 tokens: 26.7 us, of which the longest path's five or six
 // rows take 4 us each (1.8 us of loads, the rest the totals, their exchange and the
@@ -44,14 +45,16 @@ using draw::join;
 using draw::to_f32;
 using draw::warp_sum;
 
-constexpr int kCluster = 8;
+// Rows up to so long are one CTA's, longer ones a cluster's (32 trees of 16, bfloat16, one CTA / eight: 12.3 / 14.3 us at 8000
+// tokens, 15.4 / 15.6 at 16000, 20.8 / 15.8 at 32000; 14.9 / 20.8 at 1000).
+constexpr int kSmallVocab = 8192;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;                           // groups of 128 weights whose loads are in flight together
-constexpr int kSpan = kCluster * kWarps * kBatch * 128;       // weights of a batch of every warp
-__host__ __device__ constexpr int batches_of(int weights) { return (weights + kSpan - 1) / kSpan; }
-constexpr int kMaxBatches = batches_of(PKV_ACCEPT_MAX_VOCAB + 3);
-static_assert(kMaxBatches <= 32, "a batch a lane");
+// Batches of every warp that so many weights fill, over a cluster of CTAs.
+__host__ __device__ constexpr int batches_of(int weights, int cluster) {
+    return (weights + cluster * kWarps * kBatch * 128 - 1) / (cluster * kWarps * kBatch * 128);
+}
 constexpr int kNodes = PKV_TREE_MAX_NODES;
 static_assert(kNodes == 64, "a warp looks the children up two nodes a lane");
 
@@ -67,8 +70,10 @@ __device__ __forceinline__ unsigned long long warp_units(uint32_t hi, uint32_t l
     return join(__reduce_add_sync(0xffffffffu, hi), __reduce_add_sync(0xffffffffu, lo));
 }
 
-template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTreeArgs a) {
+template <typename T, int kCluster>
+__global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTreeArgs a) {
+    constexpr int kMaxBatches = batches_of((kCluster == 1 ? kSmallVocab : PKV_ACCEPT_MAX_VOCAB) + 3, kCluster);
+    static_assert(kMaxBatches <= 32, "a batch a lane");
     __shared__ unsigned long long warp_total[kWarps];
     // (two of each, for the rows in turn: a CTA may still read a row's when another writes the next one's)
     __shared__ unsigned long long s_total[2][kCluster];      // every CTA's total of the row
@@ -85,10 +90,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
     __shared__ int s_parent[kNodes];
     __shared__ int s_draft[kNodes];
     __shared__ int s_owner[kNodes];                           // the warp of the cluster whose piece of the parent's row holds it
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank());
-    const int b = blockIdx.x / kCluster;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = kCluster == 1 ? 0 : static_cast<int>(cluster.block_rank());
+    auto sync = [&] {
+        if constexpr (kCluster == 1) __syncthreads();
+        else cluster.sync();
+    };
+    auto put = [&](unsigned long long* at, unsigned long long x) {            // lane r: into CTA r's shared memory
+        if constexpr (kCluster == 1) {
+            if (lane == 0) *at = x;
+        } else {
+            if (lane < kCluster) *cluster.map_shared_rank(at, lane) = x;
+        }
+    };
+    const int b = blockIdx.x / kCluster;
     auto started = cluster.barrier_arrive();        // (waited for before the first write into another CTA)
     grid_dependency_wait();
     launch_dependents();
@@ -114,7 +130,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
         int owner = -1;
         if (parent >= 0 && token >= 0) {
             const int off = offset_of(first + parent);
-            owner = (token + off) / (batches_of(V + off) * kBatch * 128);
+            owner = (token + off) / (batches_of(V + off, kCluster) * kBatch * 128);
         }
         s_parent[t] = parent;
         s_draft[t] = token;
@@ -132,7 +148,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
         const T* row = row_of(first + node);
         const float u = __ldcg(a.uniform + first + node);
         const int off = offset_of(first + node);
-        const int batches = batches_of(V + off);
+        const int batches = batches_of(V + off, kCluster);
         const int piece = (rank * kWarps + warp) * batches * kBatch * 128 - off;
 
         constexpr int kWords = Four<T>::kWords;
@@ -286,7 +302,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
         __syncthreads();
         if (warp == 0) {
             const unsigned long long sum = warp_sum(lane < kWarps ? warp_total[lane] : 0ull);
-            if (lane < kCluster) *cluster.map_shared_rank(&s_total[steps & 1][rank], lane) = sum;
+            put(&s_total[steps & 1][rank], sum);
         }
 #pragma unroll 1
         for (unsigned long long m = static_cast<unsigned long long>(here[1]) << 32 | here[0]; m; m &= m - 1) {
@@ -295,12 +311,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
             const unsigned long long own = s_units[steps & 1][c];
             for (int v = 0; v < warp; ++v) before += warp_total[v];
             __syncwarp();
-            if (lane < kCluster) {
-                *cluster.map_shared_rank(&s_before[steps & 1][c], lane) = before;
-                *cluster.map_shared_rank(&s_units[steps & 1][c], lane) = own;
-            }
+            put(&s_before[steps & 1][c], before);
+            put(&s_units[steps & 1][c], own);
         }
-        cluster.sync();
+        sync();
         unsigned long long total = 0;               // of the row
         unsigned long long before = 0, kid[2] = {0, 0};      // of what stands before this CTA's piece; before a lane's children's
 #pragma unroll
@@ -406,41 +420,49 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4) 
         for (int i = (n > 0 ? steps + 1 : 0) + t; i < W; i += kThreads) tokens[i] = path[i] = -1;
         if (t == 0) a.num_accepted[b] = steps;
     }
-    cluster.sync();                                 // no CTA leaves while another may still write its shared memory
+    sync();                                         // no CTA leaves while another may still write its shared memory
 }
 
-template <typename T>
+template <typename T, int kCluster>
 cudaError_t launch(const AcceptTreeArgs& a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * kCluster);
-    cfg.blockDim = dim3(kThreads);
     constexpr int kShared = 3 * kBatch * kThreads * 4 * sizeof(T);
-    cfg.dynamicSmemBytes = kShared;
     static std::atomic<uint64_t> ready{0};          // devices on which the kernel may take that much
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-        e = cudaFuncSetAttribute(accept_tree_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+        e = cudaFuncSetAttribute(accept_tree_kernel<T, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * kCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kShared;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, accept_tree_kernel<T>, a);
+    cfg.numAttrs = kCluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, accept_tree_kernel<T, kCluster>, a);
+}
+
+template <typename T>
+cudaError_t launch_by_vocab(const AcceptTreeArgs& a, cudaStream_t s) {
+    return a.vocab <= kSmallVocab ? launch<T, 1>(a, s) : launch<T, 8>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_accept_tree(const AcceptTreeArgs& a, int dtype, cudaStream_t s) {
     if (a.num_seqs <= 0) return cudaSuccess;
-    if (dtype == 0) return launch<__half>(a, s);
-    if (dtype == 1) return launch<__nv_bfloat16>(a, s);
-    return launch<float>(a, s);
+    if (dtype == 0) return launch_by_vocab<__half>(a, s);
+    if (dtype == 1) return launch_by_vocab<__nv_bfloat16>(a, s);
+    return launch_by_vocab<float>(a, s);
 }
 
 }  // namespace pkv

@@ -115,6 +115,16 @@ def test_rows_off_every_boundary():
             Case([6, 11, 2], V, 6, dtype, V).check()
 
 
+@pytest.mark.parametrize("V", [8185, 8191, 8192, 8193, 8196])
+def test_around_the_vocabulary_of_one_cta(V):
+    for dtype in DT:
+        c = Case([9, 1, 30, 16], V, 6, dtype, V, gap=1)
+        c.check()
+        c.u[::2] = 1.0 - 2.0 ** -24                           # the row's last tokens, and its first
+        c.u[1::2] = 0.0
+        c.check()
+
+
 def test_the_largest_vocabulary():
     c = Case([4, 6], pkv.ACCEPT_MAX_VOCAB, 5, "bf16", 3)
     c.check()
