@@ -69,8 +69,8 @@
 // plan stay those of the causal call.  On the one or two steps that hold nodes a
 // thread masks its row by its word, and V's non-finite elements are noted as a word of
 // nodes a column, since what two rows see is no longer one a part of the other.  64
-// trees of 16 over 512 to 4096 positions, 32 heads over 8: 102 us, 5.4 TB/s (steps at
-// the HBM rate, 1.5 us; start-up 9 us); 128 ragged trees of 1 to 64, 64 heads over 8:
+// trees of 16 over 512 to 4096 positions, 32 heads over 8: 98.5 us, 5.6 TB/s (steps at
+// the HBM rate, 1.5 us; start-up 9 us; blocks read once leave L2 first, 102 without); 128 ragged trees of 1 to 64, 64 heads over 8:
 // 156 us, where a step of two tiles takes 1.72 us from HBM and an item 3.4 us beside.
 // Over E4M3 pools, trees of up to 128 rows (LONE): a lone tile would leave half the
 // softmax warps idle, so four of them expand codes too (eight in all, one trip a tile)
@@ -334,6 +334,13 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4]) {
             else w[i ^ s] = got;
         }
     }
+}
+
+__device__ __forceinline__ uint64_t l2_policy(bool first) {
+    uint64_t f, n;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(f));
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(n));
+    return first ? f : n;
 }
 
 // Element offset / D of row r of the item's tile in q / out.
@@ -623,6 +630,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefil
             }
             for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps(), stop = it.stop();
+                // (a KV head that is one item reads its blocks once: they leave L2 first)
+                [[maybe_unused]] const uint64_t once = TREE ? l2_policy(it.n * a.group <= (LONE ? kSub : kPrefillRows)) : 0ull;
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
                 auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
                     const int pos = (it.step0 + j) * kStep + lane * bs;
@@ -647,7 +656,10 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefil
                         uint8_t* dst = smem + G::kCode + slot * G::kCodeTile;
                         for (int b = 0; b < nb; ++b) {
                             const int pb = __shfl_sync(0xffffffffu, id, b);
-                            if (leader) tma_load_4d(dst + b * bs * D, kv ? &tmv : &tmk, 0, it.kvh, 0, pb, &code_full[slot]);
+                            if (leader) {
+                                if constexpr (TREE) tma_load_4d_hint(dst + b * bs * D, kv ? &tmv : &tmk, 0, it.kvh, 0, pb, &code_full[slot], once);
+                                else tma_load_4d(dst + b * bs * D, kv ? &tmv : &tmk, 0, it.kvh, 0, pb, &code_full[slot]);
+                            }
                         }
                         c.next();
                     }
@@ -774,6 +786,8 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefil
             if (leader) prefetch_tensormap(tm);
             for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps(), stop = it.stop();
+                // (a KV head that is one item reads its blocks once: they leave L2 first)
+                [[maybe_unused]] const uint64_t once = TREE ? l2_policy(it.n * a.group <= (LONE ? kSub : kPrefillRows)) : 0ull;
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
                 auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
                     const int pos = (it.step0 + j) * kStep + lane * bs;
@@ -799,8 +813,10 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefil
                         const int pb = __shfl_sync(0xffffffffu, id, b);
                         if (leader) {
 #pragma unroll
-                            for (int hf = 0; hf < G::kHalves; ++hf)
-                                tma_load_4d(dst + hf * G::kPlane + b * bs * 128, tm, hf * 64, it.kvh, 0, pb, &full[slot]);
+                            for (int hf = 0; hf < G::kHalves; ++hf) {
+                                if constexpr (TREE) tma_load_4d_hint(dst + hf * G::kPlane + b * bs * 128, tm, hf * 64, it.kvh, 0, pb, &full[slot], once);
+                                else tma_load_4d(dst + hf * G::kPlane + b * bs * 128, tm, hf * 64, it.kvh, 0, pb, &full[slot]);
+                            }
                         }
                     }
                     c.next();
