@@ -677,7 +677,7 @@ PKV_API pkv_status pkv_speculative_accept_tree(int64_t* tokens, int32_t* path, i
  *                 different; a row's bytes a multiple of 16
  *   seq_lens      int32 [num_seqs]: the lengths with all nodes, as the attention
  *                 had them
- *   query_starts  int32 [num_seqs + 1]; only differences are used
+ *   query_starts  int32 [num_seqs + 1], none below 0; only differences are used
  *   path          int32 [num_seqs][width], 0 = path[s][0] < path[s][1] < ..
  *                 < path[s][a] < n_s (what follows is not read)
  *   num_accepted  int32 [num_seqs]

@@ -104,7 +104,7 @@ cudaError_t launch_keep_path(const KeepPathArgs& a, cudaStream_t s) {
     if (a.num_seqs <= 0 || a.num_layers <= 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs),
-                       static_cast<unsigned>(std::min(2 * a.num_layers, (kCtas + a.num_seqs - 1) / a.num_seqs)));
+                       static_cast<unsigned>(std::min(2 * a.num_layers, (kCtas - 1) / a.num_seqs + 1)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -70,8 +70,9 @@
 // thread masks its row by its word, and V's non-finite elements are noted as a word of
 // nodes a column, since what two rows see is no longer one a part of the other.  64
 // trees of 16 over 512 to 4096 positions, 32 heads over 8: 98.5 us, 5.6 TB/s (steps at
-// the HBM rate, 1.5 us; start-up 9 us; blocks read once leave L2 first, 102 without); 128 ragged trees of 1 to 64, 64 heads over 8:
-// 156 us, where a step of two tiles takes 1.72 us from HBM and an item 3.4 us beside.
+// the HBM rate, 1.5 us; start-up 9 us; blocks read once leave L2 first, 102 without);
+// 128 ragged trees of 1 to 64, 64 heads over 8: 156 us, where a step of two tiles takes
+// 1.72 us from HBM and an item 3.4 us beside.
 // Over E4M3 pools, trees of up to 128 rows (LONE): a lone tile would leave half the
 // softmax warps idle, so four of them expand codes too (eight in all, one trip a tile)
 // and S of the next step runs under the softmax, in the other tile's columns: 64 trees
