@@ -907,101 +907,101 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefil
                         }
                         c = k;
                     }
-                    continue;
-                }
-                // round j: O += P V of step j, then S of step j + 1 (round -1: the first S alone)
+                } else {
+                    // round j: O += P V of step j, then S of step j + 1 (round -1: the first S alone)
 #pragma unroll 1
-                for (int j = -1; j < n; ++j) {
-                    const Ring<ST> v = c;                    // V of this step, then K of the next
-                    if (j >= 0) {
-                        c.next();
-                        ok = wait(&full[v.slot], v.phase);
-                        int lo, nv, nv16;
-                        it.partial(j, lo, nv, nv16);
-                        if (!KV8 && ok && lo < nv16) {       // V that some row sees only in part
-                            ok = wait(&clean[v.slot], v.phase);
-                        }
-                    }
-                    const bool more_k = j + 1 < n;
-                    if (ok && more_k) ok = wait(&full[c.slot], c.phase);
-                    if (!ok) break;
-                    auto issue_s = [&]() {                   // (leader) S of step j + 1
-                        const uint64_t d = dk + static_cast<uint64_t>(c.slot * (G::kTile >> 4));
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint64_t off = ((ks >> 2) * G::kPlane + (ks & 3) * 32) >> 4;
-                            tc::mma_ss(ts, dq + off, d + off, id_s, ks > 0);
-                        }
-                        tc::commit(&s_full[i]);
-                        if (j + 2 == ni) tc::commit(&q_empty[i]);
-                    };
-                    if constexpr (G::kOwnP) {
-                        // S of the next step as soon as this one's is in registers: it runs under the softmax
-                        if (j + 1 < ni) {
-                            ok = j < 0 ? wait(&q_full[i], nq) : wait(&s_read[i], nr);
-                            if (!ok) break;
-                            if (j < 0) nq ^= 1u;
-                            else nr ^= 1u;
-                            tc::fence_after_sync();
-                            if (leader) issue_s();
-                        }
-                        // (the item's last S is read too before the next item's first replaces it: by the softmax
-                        // threads that wrote the P this waits for)
-                        if (j >= 0 && j == ni - 1) nr ^= 1u;
-                        if (leader && more_k) tc::commit(&empty[c.slot]);
-                    } else {
-                        // the tiles take turns, a round's O product and S product at a time: left to themselves
-                        // they fall into step, both on the tensor cores, then both in their softmax
-                        ok = wait(&turn[i], nturn);
-                        nturn ^= 1u;
-                        if (!ok) break;
-                    }
-                    if (j >= 0 && j < ni) {
-                        const int left = it.end_of(i) - (it.step0 + j) * kStep;   // (16 a product, none wholly past the end)
-                        const uint64_t d = dv + static_cast<uint64_t>(v.slot * (G::kTile >> 4));
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            if (!G::kOwnP || half == 0) {    // (kOwnP: both halves come at once)
-                                ok = ok && wait(&p_full[2 * i + half], np);
-                                tc::fence_after_sync();
+                    for (int j = -1; j < n; ++j) {
+                        const Ring<ST> v = c;                    // V of this step, then K of the next
+                        if (j >= 0) {
+                            c.next();
+                            ok = wait(&full[v.slot], v.phase);
+                            int lo, nv, nv16;
+                            it.partial(j, lo, nv, nv16);
+                            if (!KV8 && ok && lo < nv16) {       // V that some row sees only in part
+                                ok = wait(&clean[v.slot], v.phase);
                             }
-                            if (ok && leader) {
-                                if (left >= kStep - 15) {
+                        }
+                        const bool more_k = j + 1 < n;
+                        if (ok && more_k) ok = wait(&full[c.slot], c.phase);
+                        if (!ok) break;
+                        auto issue_s = [&]() {                   // (leader) S of step j + 1
+                            const uint64_t d = dk + static_cast<uint64_t>(c.slot * (G::kTile >> 4));
 #pragma unroll
-                                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                        tc::mma_ts(to, tp + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
-                                } else {
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint64_t off = ((ks >> 2) * G::kPlane + (ks & 3) * 32) >> 4;
+                                tc::mma_ss(ts, dq + off, d + off, id_s, ks > 0);
+                            }
+                            tc::commit(&s_full[i]);
+                            if (j + 2 == ni) tc::commit(&q_empty[i]);
+                        };
+                        if constexpr (G::kOwnP) {
+                            // S of the next step as soon as this one's is in registers: it runs under the softmax
+                            if (j + 1 < ni) {
+                                ok = j < 0 ? wait(&q_full[i], nq) : wait(&s_read[i], nr);
+                                if (!ok) break;
+                                if (j < 0) nq ^= 1u;
+                                else nr ^= 1u;
+                                tc::fence_after_sync();
+                                if (leader) issue_s();
+                            }
+                            // (the item's last S is read too before the next item's first replaces it: by the softmax
+                            // threads that wrote the P this waits for)
+                            if (j >= 0 && j == ni - 1) nr ^= 1u;
+                            if (leader && more_k) tc::commit(&empty[c.slot]);
+                        } else {
+                            // the tiles take turns, a round's O product and S product at a time: left to themselves
+                            // they fall into step, both on the tensor cores, then both in their softmax
+                            ok = wait(&turn[i], nturn);
+                            nturn ^= 1u;
+                            if (!ok) break;
+                        }
+                        if (j >= 0 && j < ni) {
+                            const int left = it.end_of(i) - (it.step0 + j) * kStep;   // (16 a product, none wholly past the end)
+                            const uint64_t d = dv + static_cast<uint64_t>(v.slot * (G::kTile >> 4));
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                if (!G::kOwnP || half == 0) {    // (kOwnP: both halves come at once)
+                                    ok = ok && wait(&p_full[2 * i + half], np);
+                                    tc::fence_after_sync();
+                                }
+                                if (ok && leader) {
+                                    if (left >= kStep - 15) {
+#pragma unroll
+                                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                            tc::mma_ts(to, tp + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                                    } else {
 #pragma unroll 1
-                                    for (int kk = 4 * half; kk < 4 * half + 4 && kk * 16 < left; ++kk)
-                                        tc::mma_ts(to, tp + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                                        for (int kk = 4 * half; kk < 4 * half + 4 && kk * 16 < left; ++kk)
+                                            tc::mma_ts(to, tp + kk * 8, d + kk * 128, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                                    }
                                 }
                             }
-                        }
-                        np ^= 1u;
-                        if (!ok) break;
-                        if (G::kOwnP && leader) tc::commit(&o_step[i]);
-                    }
-                    if constexpr (G::kOwnP) {
-                        if (leader && j >= 0) {
-                            if (j == ni - 1) tc::commit(&o_full[i]);
-                            tc::commit(&empty[v.slot]);
-                        }
-                    } else {
-                        if (j < 0 && ni > 0) {
-                            ok = wait(&q_full[i], nq);
-                            nq ^= 1u;
+                            np ^= 1u;
                             if (!ok) break;
-                            tc::fence_after_sync();
+                            if (G::kOwnP && leader) tc::commit(&o_step[i]);
                         }
-                        if (leader) {
-                            if (j + 1 < ni) issue_s();
-                            mbar_arrive(&turn[1 - i]);
-                            if (j >= 0 && j == ni - 1) tc::commit(&o_full[i]);
-                            if (j >= 0) tc::commit(&empty[v.slot]);
-                            if (more_k) tc::commit(&empty[c.slot]);
+                        if constexpr (G::kOwnP) {
+                            if (leader && j >= 0) {
+                                if (j == ni - 1) tc::commit(&o_full[i]);
+                                tc::commit(&empty[v.slot]);
+                            }
+                        } else {
+                            if (j < 0 && ni > 0) {
+                                ok = wait(&q_full[i], nq);
+                                nq ^= 1u;
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                            }
+                            if (leader) {
+                                if (j + 1 < ni) issue_s();
+                                mbar_arrive(&turn[1 - i]);
+                                if (j >= 0 && j == ni - 1) tc::commit(&o_full[i]);
+                                if (j >= 0) tc::commit(&empty[v.slot]);
+                                if (more_k) tc::commit(&empty[c.slot]);
+                            }
                         }
+                        if (more_k) c.next();
                     }
-                    if (more_k) c.next();
                 }
             }
             if (!ok && leader) dec::raise_abort(a.err, abort_flag);
