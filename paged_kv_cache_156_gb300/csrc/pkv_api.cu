@@ -282,7 +282,7 @@ pkv_status pkv_paged_kv_append_rotary(void* q_out, const void* q, const void* k,
     const bool kv8 = kv_dt == PKV_E4M3;
     if (kv8 && (!k_scale || !v_scale)) return fail(PKV_ERR_INVALID, "E4M3 pools need k_scale and v_scale");
     const unsigned pool_align = kv8 ? 7u : 15u;
-    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cos_sin) ||
+    if ((num_heads > 0 && (!aligned16(q_out) || !aligned16(q))) || !aligned16(k) || !aligned16(v) || !aligned16(cos_sin) ||
         (reinterpret_cast<uintptr_t>(key_cache) & pool_align) || (reinterpret_cast<uintptr_t>(value_cache) & pool_align) ||
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
         (kv8 && ((reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u))))
