@@ -794,7 +794,7 @@ pkv_status prefill_call(void* out, const void* q, const void* key_cache, const v
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
-    a.lone = tree_mask && kv8 && pkv::tree_lone(num_seqs, num_tokens, a.group);
+    a.lone_nodes = pkv::tree_lone_nodes(num_tokens, a.group);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (planned) a.direct = 0;
     a.local = !planned && !a.direct && pkv::prefill_local(num_seqs, num_tokens, num_heads, num_kv_heads, a.slots, lay);

@@ -492,10 +492,8 @@ __device__ __forceinline__ Entry local_entry(const LocalPlan& lp, int e, int kvh
 // TREE: the last n positions are a tree's nodes, of which row (token i, head) sees those of token i's mask.
 // LONE (trees of up to 128 rows over E4M3 pools): an item's tiles are taken one after the other.
 template <typename T, int D, bool KV8, typename OT, bool TREE, bool LONE>
-__global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
-                                                                        const __grid_constant__ CUtensorMap tmk,
-                                                                        const __grid_constant__ CUtensorMap tmv,
-                                                                        const __grid_constant__ PrefillArgs a) {
+__device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                            const PrefillArgs& a) {
     using G = PfGeo<D, KV8, TREE, LONE>;
     constexpr int ST = G::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -1577,6 +1575,34 @@ __global__ void __launch_bounds__(PfGeo<D, KV8, TREE, LONE>::kThreads, 1) prefil
     }
 }
 
+// Whether no tree of the call has more than a tile of rows of a KV head, so that their tiles are taken one by one: the same
+// in every CTA.  The query starts alone decide: padding rows behind the last tree and sequences without nodes count for
+// nothing, and a replayed graph goes by its own trees.  Looking, and both forms in one kernel, cost the two-tile form 2.4%
+// (64 trees of 33: 154 to 157.5 us) and the one-tile form, which comes first in the code, nothing (109 us with trees of
+// 26); the other way round 1% and 2% (one small call 7.6 to 8.7 us), a kernel of each, the one ending at once, 2% and 3%.
+__device__ __forceinline__ bool lone_trees(const PrefillArgs& a) {
+    if (a.lone_nodes >= kTreeNodes) return true;
+    grid_dependency_wait();
+    bool more = false;
+    for (int s = threadIdx.x; s < a.num_seqs; s += blockDim.x)
+        more |= static_cast<long long>(__ldcg(a.query_starts + s + 1)) - __ldcg(a.query_starts + s) > a.lone_nodes;
+    return !__syncthreads_or(more);
+}
+
+template <typename T, int D, bool KV8, typename OT, bool TREE>
+__global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
+                                                                        const __grid_constant__ CUtensorMap tmk,
+                                                                        const __grid_constant__ CUtensorMap tmv,
+                                                                        const __grid_constant__ PrefillArgs a) {
+    if constexpr (TREE && KV8) {
+        if (lone_trees(a)) {
+            prefill_cta<T, D, KV8, OT, TREE, true>(tmq, tmk, tmv, a);
+            return;
+        }
+    }
+    prefill_cta<T, D, KV8, OT, TREE, false>(tmq, tmk, tmv, a);
+}
+
 // The split tiles' parts merged: 32 rows by 64 columns a CTA, a row a lane, its columns over the warps.
 //     m = max_p m_p,  out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
 // summed in part order.  Launched for every call whose plan may split, since the host does not know whether it did
@@ -1671,12 +1697,15 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
     }
 }
 
-template <typename T, int D, bool KV8, typename OT, bool TREE, bool LONE = false>
+template <typename T, int D, bool KV8, typename OT, bool TREE>
 cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                      cudaStream_t s) {
-    using G = PfGeo<D, KV8, TREE, LONE>;
-    static_assert(G::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
-    auto kern = prefill_kernel<T, D, KV8, OT, TREE, LONE>;
+    using G = PfGeo<D, KV8, TREE>;
+    using GL = PfGeo<D, KV8, TREE, TREE && KV8>;            // (its other form's)
+    constexpr size_t kShared = std::max(G::kBytes, GL::kBytes);
+    static_assert(G::kRing % 1024 == 0 && GL::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
+    static_assert(G::kRegsSoftmax == GL::kRegsSoftmax && G::kRegsOther == GL::kRegsOther, "one register split");
+    auto kern = prefill_kernel<T, D, KV8, OT, TREE>;
     // once a device: the shared memory, and that the warpgroups' register split fits what a block is launched with
     // (or it would wait for ever)
     static std::atomic<uint64_t> ready{0};
@@ -1687,7 +1716,7 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtenso
         cudaFuncAttributes fa{};
         if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
         if (fa.numRegs * G::kThreads < 256 * G::kRegsSoftmax + 256 * G::kRegsOther) return cudaErrorLaunchOutOfResources;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kBytes));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kShared));
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
@@ -1695,7 +1724,7 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtenso
     cfg.gridDim = dim3(static_cast<unsigned>(
         std::min<int64_t>(a.slots, static_cast<int64_t>(a.direct ? a.capacity - a.part_cap : a.capacity) * a.num_kv_heads)));
     cfg.blockDim = dim3(G::kThreads);
-    cfg.dynamicSmemBytes = G::kBytes;
+    cfg.dynamicSmemBytes = kShared;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1714,9 +1743,6 @@ template <bool TREE>
 cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype,
                    int head_dim, cudaStream_t s) {
     using bf16 = __nv_bfloat16;
-    if (TREE && a.k_scale && a.lone)
-        return dtype == 0 ? launch_t<__half, 128, true, __half, true, true>(a, tmq, tmk, tmv, s)
-                          : launch_t<__half, 128, true, bf16, true, true>(a, tmq, tmk, tmv, s);
     if (a.k_scale)
         return dtype == 0 ? launch_t<__half, 128, true, __half, TREE>(a, tmq, tmk, tmv, s)
                           : launch_t<__half, 128, true, bf16, TREE>(a, tmq, tmk, tmv, s);
