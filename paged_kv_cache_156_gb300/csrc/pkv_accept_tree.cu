@@ -185,16 +185,13 @@ __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTr
             return warp_units(hi, lo);
         };
 
-        // The warp's whole batches are those from `head` on (a row off its boundary starts inside the first warp's first
-        // batch).  The third and fourth of them come by way of shared memory, so that four are in flight (128000 float32
-        // tokens: all).  Where one of these is there, so are the two before it: the pass below then always takes both copies up.
-        const int head = piece < 0;
-        const int late = head + 3 > batches || !inside(head + 2) ? 0 : head + 4 > batches || !inside(head + 3) ? 1 : 2;
-        if (late) {
+        // The third and fourth batch come by way of shared memory, so that four are in flight (128000 float32 tokens: all),
+        // where the first four are whole: the pass below then always takes them up.
+        const bool more = batches >= 4 && inside(0) && inside(3);
+        if (more) {
 #pragma unroll
             for (int k = 0; k < 2 * kBatch; ++k)
-                if (k < late * kBatch)
-                    copy_vector<4 * sizeof(T)>(smem_u32(later + k * kThreads + t), mine_at + ((head + 2) * kBatch + k) * 128);
+                copy_vector<4 * sizeof(T)>(smem_u32(later + k * kThreads + t), mine_at + (2 * kBatch + k) * 128);
             cp_async_commit();
         }
         // The node's children.  Whether the mark falls on the token of one is known as soon as the totals are, if the units
@@ -222,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTr
         // ---- the row's total, two batches in flight and two on their way: a sequence whose neighbours are through has its
         // SMs to itself, and what its eight warps a CTA have in flight sets its pace
         unsigned long long mine = 0;
+        const int head = piece < 0;                 // (a row off its boundary starts inside a batch, which comes last)
         int batch = head;
 #pragma unroll 1
         for (; batch + 2 <= batches && inside(batch) && inside(batch + 1); batch += 2) {
@@ -234,10 +232,11 @@ __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTr
                 if (lane == 0) batch_total[warp][batch + i] = sum;
                 mine += sum;
             }
-            if (batch == head && late) {
+            if (batch == 0 && more) {
                 cp_async_wait_all();
+                batch = 2;
 #pragma unroll 1
-                for (int i = 0; i < late; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     uint32_t hi = 0, lo = 0;
 #pragma unroll
                     for (int k = 0; k < kBatch; ++k) {
@@ -248,28 +247,23 @@ __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTr
                         for (int e = 0; e < 4; ++e) add_units(__saturatef(w[e]), hi, lo);
                     }
                     const unsigned long long sum = warp_units(hi, lo);
-                    if (lane == 0) batch_total[warp][batch + 2 + i] = sum;
+                    if (lane == 0) batch_total[warp][batch + i] = sum;
                     mine += sum;
                 }
-                batch += late;
             }
         }
 #pragma unroll 1
-        for (; batch < batches; ++batch) {
+        for (; batch < batches + head; ++batch) {
+            const int i = batch < batches ? batch : 0;
             unsigned long long sum;
-            if (inside(batch)) {
+            if (inside(i)) {
                 uint32_t p[kBatch][kWords];
-                load(batch, p);
+                load(i, p);
                 sum = units_of(p);
             } else {
-                sum = units_at_ends(batch);
+                sum = units_at_ends(i);
             }
-            if (lane == 0) batch_total[warp][batch] = sum;
-            mine += sum;
-        }
-        if (head) {                                 // the batch the row starts in
-            const unsigned long long sum = units_at_ends(0);
-            if (lane == 0) batch_total[warp][0] = sum;
+            if (lane == 0) batch_total[warp][i] = sum;
             mine += sum;
         }
         if (ahead >= 0) cp_async_wait_all();
