@@ -319,8 +319,7 @@ bool prefill_local(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_h
 // (from kTreeNodes on: none can, and the kernel does not look): 109 us against 124 over 64 sequences of 512 to 4096
 // positions with trees of 26 or of 20 to 32 nodes, 32 heads over 8.  A larger tree's sequence would be streamed twice: 211
 // against 154 with trees of 33, 211 against 155 with trees of 10 and 54 in turn, 343 against 275 over 128 trees of 1 to 24,
-// 64 heads over 8, and 139 against 129 for two trees of 40 among 62 of 26 (117 against 124 for a single one).  (Each form
-// in a kernel of its own; lone_trees says what choosing on the device costs.)
+// 64 heads over 8, and 139 against 129 for two trees of 40 among 62 of 26 (117 against 124 for a single one).
 inline int tree_lone_nodes(int64_t num_tokens, int group) {
     const int64_t most = num_tokens < kTreeNodes ? num_tokens : kTreeNodes;
     return most * group <= kPrefillSub ? kTreeNodes : kPrefillSub / group;

@@ -1582,9 +1582,7 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
 
 // Whether no tree of the call has more than a tile of rows of a KV head, so that their tiles are taken one by one: the same
 // in every CTA.  The query starts alone decide: padding rows behind the last tree and sequences without nodes count for
-// nothing, and a replayed graph goes by its own trees.  Looking, and both forms in one kernel, cost the two-tile form 2.4%
-// (64 trees of 33: 154 to 157.5 us) and the one-tile form, which comes first in the code, nothing (109 us with trees of
-// 26); the other way round 1% and 2% (one small call 7.6 to 8.7 us), a kernel of each, the one ending at once, 2% and 3%.
+// nothing, and a replayed graph goes by its own trees.  Looking takes 1 us.
 __device__ __forceinline__ bool lone_trees(const PrefillArgs& a) {
     if (a.lone_nodes >= kTreeNodes) return true;
     grid_dependency_wait();
@@ -1594,18 +1592,22 @@ __device__ __forceinline__ bool lone_trees(const PrefillArgs& a) {
     return !__syncthreads_or(more);
 }
 
-template <typename T, int D, bool KV8, typename OT, bool TREE>
+// Trees over E4M3 pools: both forms, the one the host expects (LONE_FIRST) first.  The second in the code runs 2 to 5%
+// slower: 64 trees of 26, 32 heads over 8, 101.1 us as the first and 103.3 as the second, of 33 144.3 and 146.7, 128 trees of 1
+// to 64, 64 heads over 8, 194.1 and 202.6.  (In kernels of their own 101.0, 143.0 and 192.7; one after the other, the one
+// that does not apply ending at once, 3 us more a call.)
+template <typename T, int D, bool KV8, typename OT, bool TREE, bool LONE_FIRST>
 __global__ void __launch_bounds__(PfGeo<D, KV8, TREE>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmq,
                                                                         const __grid_constant__ CUtensorMap tmk,
                                                                         const __grid_constant__ CUtensorMap tmv,
                                                                         const __grid_constant__ PrefillArgs a) {
     if constexpr (TREE && KV8) {
-        if (lone_trees(a)) {
-            prefill_cta<T, D, KV8, OT, TREE, true>(tmq, tmk, tmv, a);
+        if (lone_trees(a) == LONE_FIRST) {
+            prefill_cta<T, D, KV8, OT, TREE, LONE_FIRST>(tmq, tmk, tmv, a);
             return;
         }
     }
-    prefill_cta<T, D, KV8, OT, TREE, false>(tmq, tmk, tmv, a);
+    prefill_cta<T, D, KV8, OT, TREE, TREE && KV8 && !LONE_FIRST>(tmq, tmk, tmv, a);
 }
 
 // The split tiles' parts merged: 32 rows by 64 columns a CTA, a row a lane, its columns over the warps.
@@ -1702,7 +1704,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Pref
     }
 }
 
-template <typename T, int D, bool KV8, typename OT, bool TREE>
+template <typename T, int D, bool KV8, typename OT, bool TREE, bool LONE_FIRST = false>
 cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                      cudaStream_t s) {
     using G = PfGeo<D, KV8, TREE>;
@@ -1710,7 +1712,7 @@ cudaError_t launch_t(const PrefillArgs& a, const CUtensorMap& tmq, const CUtenso
     constexpr size_t kShared = std::max(G::kBytes, GL::kBytes);
     static_assert(G::kRing % 1024 == 0 && GL::kRing % 1024 == 0 && G::kTile % 1024 == 0, "tiles start on a swizzle atom");
     static_assert(G::kRegsSoftmax == GL::kRegsSoftmax && G::kRegsOther == GL::kRegsOther, "one register split");
-    auto kern = prefill_kernel<T, D, KV8, OT, TREE>;
+    auto kern = prefill_kernel<T, D, KV8, OT, TREE, LONE_FIRST>;
     // once a device: the shared memory, and that the warpgroups' register split fits what a block is launched with
     // (or it would wait for ever)
     static std::atomic<uint64_t> ready{0};
@@ -1748,6 +1750,12 @@ template <bool TREE>
 cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv, int dtype,
                    int head_dim, cudaStream_t s) {
     using bf16 = __nv_bfloat16;
+    if constexpr (TREE) {
+        // (trees that fill a tile on average or less are expected to be one each)
+        if (a.k_scale && a.num_tokens * a.group <= int64_t(kPrefillSub) * a.num_seqs)
+            return dtype == 0 ? launch_t<__half, 128, true, __half, true, true>(a, tmq, tmk, tmv, s)
+                              : launch_t<__half, 128, true, bf16, true, true>(a, tmq, tmk, tmv, s);
+    }
     if (a.k_scale)
         return dtype == 0 ? launch_t<__half, 128, true, __half, TREE>(a, tmq, tmk, tmv, s)
                           : launch_t<__half, 128, true, bf16, TREE>(a, tmq, tmk, tmv, s);
