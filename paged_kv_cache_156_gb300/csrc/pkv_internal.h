@@ -293,7 +293,7 @@ struct PrefillArgs {
     float scale_log2;                // |scale| * log2(e)
     const float* k_scale;            // [num_kv_heads] (E4M3 pools only, else nullptr)
     const float* v_scale;
-    int lone_nodes;                  // trees of up to so many nodes are taken a tile at a time (E4M3 pools; tree_lone_nodes)
+    int lone_nodes;                  // the one-tile form takes trees of up to so many nodes (E4M3 pools; tree_lone_nodes)
     const unsigned long long* tree_mask;     // [num_tokens]: bit j, the token sees node j of its tree (nullptr: causal)
 };
 
@@ -315,11 +315,11 @@ bool prefill_direct(int num_seqs, int64_t num_tokens, int max_seq_len, int num_h
 // A batch small enough for every CTA to plan it by itself, in its own shared memory, instead of a plan kernel.
 bool prefill_local(int num_seqs, int64_t num_tokens, int num_heads, int num_kv_heads, int slots,
                    const PrefillWorkspace& w);
-// Trees over an E4M3 pool are taken a tile of 128 rows at a time where none has more, that is none more than so many nodes
-// (from kTreeNodes on: none can, and the kernel does not look): 109 us against 124 over 64 sequences of 512 to 4096
-// positions with trees of 26 or of 20 to 32 nodes, 32 heads over 8.  A larger tree's sequence would be streamed twice: 211
-// against 154 with trees of 33, 211 against 155 with trees of 10 and 54 in turn, 343 against 275 over 128 trees of 1 to 24,
-// 64 heads over 8, and 139 against 129 for two trees of 40 among 62 of 26 (117 against 124 for a single one).
+// Trees over an E4M3 pool take the form for tiles of 128 rows of a KV head where none has more, that is none more than so
+// many nodes (from kTreeNodes on: none can, and the kernel does not look): 109 us against the two-tile form's 124 over 64
+// sequences of 512 to 4096 positions with trees of 26 or of 20 to 32 nodes, 32 heads over 8.  A larger tree tile by tile
+// would stream its sequence twice: that took 211 us against 154 with trees of 33, 211 against 155 with trees of 10 and 54 in
+// turn, 343 against 275 over 128 trees of 1 to 24, 64 heads over 8, and 139 against 129 for two trees of 40 among 62 of 26.
 inline int tree_lone_nodes(int64_t num_tokens, int group) {
     const int64_t most = num_tokens < kTreeNodes ? num_tokens : kTreeNodes;
     return most * group <= kPrefillSub ? kTreeNodes : kPrefillSub / group;

@@ -109,7 +109,7 @@ struct PfGeo {
     static constexpr int kStages = KV8 ? (TREE && !LONE ? 3 : 4) : D == 128 ? 5 : 10;
     static constexpr int kCodes = KV8 ? (TREE ? 3 : 2) : 0;   // staged tiles of codes (128 rows of D bytes)
     static constexpr int kCodeTile = 128 * D;
-    static constexpr int kTiles = LONE ? 1 : 2;             // an item's tiles of rows, a softmax warpgroup each
+    static constexpr int kTiles = LONE ? 1 : 2;             // an item's tiles of rows at most, a softmax warpgroup each
     static constexpr int kConverters = LONE ? 8 : 3;        // warps 4-7 and 10-13, a trip a tile; else warps 10, 12 and 13: on two of the schedulers (10, 12, 14) 120 us, on three 117 (8 chunks of 256 to 512)
     static constexpr size_t kRing = kTiles * size_t(kTile); // after the Q tiles
     static constexpr size_t kCode = kRing + size_t(kStages) * kTile;
@@ -153,8 +153,7 @@ struct alignas(16) Item {
     int nst[2];                      // steps of each tile
     int lim0;                        // positions every row of the item sees
     int end[2];                      // position after the last one each tile sees in the item
-    int half;                        // (LONE) which of the item's tiles this is
-    int pad;
+    int pad[2];
     __device__ __forceinline__ int steps_of(int i) const { return i ? nst[1] : nst[0]; }
     __device__ __forceinline__ int end_of(int i) const { return i ? end[1] : end[0]; }
     __device__ __forceinline__ int steps() const { return max(nst[0], nst[1]); }
@@ -213,7 +212,7 @@ __device__ __forceinline__ Entry find_entry(const PrefillArgs& a) {
     }
     return n;
 }
-template <bool TREE>
+template <bool TREE, bool LONE>
 __device__ __forceinline__ void read_item(const PrefillArgs& a, const Entry& n, Item& it) {
     const int4 x = n.x, y = n.y;
     it.kvh = n.kvh;
@@ -233,7 +232,8 @@ __device__ __forceinline__ void read_item(const PrefillArgs& a, const Entry& n, 
     if (it.s < 0 || it.s >= a.num_seqs || it.tile < 0 || it.step0 < 0 || step1 < it.step0 || it.qs < 0 || it.n <= 0 ||
         it.qs + static_cast<long long>(it.n) > a.num_tokens || it.L < 0 || it.L > a.max_seq_len ||
         static_cast<long long>(it.tile) * kPrefillRows >= static_cast<long long>(it.n) * a.group || it.split < 0 ||
-        (it.split != 0 && (part >= nparts || base + nparts > a.part_cap)) || (TREE && it.n > kTreeNodes)) {
+        (it.split != 0 && (part >= nparts || base + nparts > a.part_cap)) || (TREE && it.n > kTreeNodes) ||
+        (LONE && it.n * a.group > kSub)) {
         if ((threadIdx.x & 31) == 0) raise_error(a.err, kErrBounds);
         return;
     }
@@ -495,7 +495,7 @@ __device__ __forceinline__ Entry local_entry(const LocalPlan& lp, int e, int kvh
 
 // T: the products' type; KV8: E4M3 pools (codes expanded to f16, every one exact there); OT: q's and out's.
 // TREE: the last n positions are a tree's nodes, of which row (token i, head) sees those of token i's mask.
-// LONE (trees of up to 128 rows over E4M3 pools): an item's tiles are taken one after the other.
+// LONE (E4M3 pools): no tree has more than 128 rows of a KV head, every item is a single tile.
 template <typename T, int D, bool KV8, typename OT, bool TREE, bool LONE>
 __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                                             const PrefillArgs& a) {
@@ -635,7 +635,7 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
             for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps(), stop = it.stop();
                 // (a KV head that is one item: no other item of the sequence reads its blocks, they leave L2 first)
-                [[maybe_unused]] const uint64_t once = TREE ? l2_policy(it.n * a.group <= (LONE ? kSub : kPrefillRows)) : 0ull;
+                [[maybe_unused]] const uint64_t once = TREE ? l2_policy(LONE || it.n * a.group <= kPrefillRows) : 0ull;
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
                 auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
                     const int pos = (it.step0 + j) * kStep + lane * bs;
@@ -791,7 +791,7 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
             for (int r = 0; ok && get_item(r, it, ok); ++r) {
                 const int n = it.steps(), stop = it.stop();
                 // (a KV head that is one item: no other item of the sequence reads its blocks, they leave L2 first)
-                [[maybe_unused]] const uint64_t once = TREE ? l2_policy(it.n * a.group <= (LONE ? kSub : kPrefillRows)) : 0ull;
+                [[maybe_unused]] const uint64_t once = TREE ? l2_policy(LONE || it.n * a.group <= kPrefillRows) : 0ull;
                 const int32_t* trow = a.block_tables + static_cast<int64_t>(it.s) * a.max_blocks_per_seq;
                 auto id_of = [&](int j) {                    // block id `lane` of step j (-1: no block)
                     const int pos = (it.step0 + j) * kStep + lane * bs;
@@ -1027,7 +1027,6 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
 #pragma unroll 1
                 for (int i = 0; i < G::kTiles; ++i) {
                     if (it.steps_of(i) == 0) continue;
-                    const int sub = LONE ? it.half : i;
                     ok = wait_bar(&q_empty[i], (ph >> i) & 1u, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     ph ^= 1u << i;
@@ -1036,7 +1035,7 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
                     if (a.q_tma) {
                         // (rows of the box past the item's are other tokens' queries, or zeros past the last:
                         // their scores go nowhere)
-                        const int tok = it.qs + (2 * it.tile + sub) * sub_tokens;
+                        const int tok = it.qs + (2 * it.tile + i) * sub_tokens;
                         if (leader) {
                             uint64_t* bar = kConvertQ ? &q_raw[i] : &q_full[i];
                             mbar_arrive_expect_tx(bar, G::kTile);
@@ -1045,7 +1044,7 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
                                 tma_load_4d(dst + hf * G::kPlane, &tmq, hf * 64, it.kvh * a.group, tok, 0, bar);
                         }
                     } else {
-                        copy_q<T, D>(a, it, sub, smem_u32(dst));
+                        copy_q<T, D>(a, it, i, smem_u32(dst));
                         if (leader) mbar_arrive(kConvertQ ? &q_raw[i] : &q_full[i]);
                     }
                 }
@@ -1080,36 +1079,18 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
                 next.live = static_cast<int>(blockIdx.x) < total;
             }
             bool ok = !*abort_flag, more = true;
-            [[maybe_unused]] Item whole;
-            [[maybe_unused]] int entries = 0;
-            [[maybe_unused]] bool second = false;            // (LONE: the item's second tile follows)
             for (int r = 0; ok && more; ++r) {
                 const int k = r % G::kItems;
                 Item it;
-                if (LONE && second) {
-                    it = whole;
-                    it.half = 1;
-                    it.nst[0] = it.nst[1];
-                    it.end[0] = it.end[1];
-                    second = false;
+                more = next.live;
+                if (more) {
+                    read_item<TREE, LONE>(a, next, it);
+                    if (!a.local) next = fetch_entry(a, total, r + 1);
+                    else if (r < 31) next = round_entry(r + 1);
+                    else next.live = false;
                 } else {
-                    more = next.live;
-                    if (more) {
-                        read_item<TREE>(a, next, it);
-                        const int entry = LONE ? ++entries : r + 1;
-                        if (!a.local) next = fetch_entry(a, total, entry);
-                        else if (entry < 32) next = round_entry(entry);
-                        else next.live = false;
-                        if constexpr (LONE) {
-                            it.half = 0;
-                            whole = it;
-                            second = it.rows > kSub;
-                        }
-                    } else {
-                        it.rows = -1;
-                    }
+                    it.rows = -1;
                 }
-                if constexpr (LONE) it.nst[1] = it.end[1] = 0;
                 ok = wait_bar(&item_empty[k], ((r / G::kItems) & 1) ^ 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -1248,8 +1229,7 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
         bool ok = !*abort_flag;
 #pragma unroll 1
         for (int r = 0; ok && get_item(r, it, ok); ++r) {
-            const int sub = LONE ? it.half : wg;             // the tile
-            const int myrow = sub * kSub + t;                // row of the item
+            const int myrow = wg * kSub + t;                 // row of the item
             const bool has = myrow < it.rows;
             const int rr = it.tile * kPrefillRows + myrow, tok = pf::div(rr, a.by_group);
             const int at = has ? (it.qs + tok) * a.num_heads + it.kvh * a.group + (rr - tok * a.group) : -1;   // row of out
@@ -1258,7 +1238,7 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
             const int n = it.steps_of(wg);
             // the warp has no row of the item: single tokens beside prompts leave most warps without (177 -> 175 us for 60
             // of them beside 4 chunks; at head_dim 64 the code more cost 4%)
-            const bool idle = sub * kSub + (warp & 3) * 32 >= it.rows;
+            const bool idle = wg * kSub + (warp & 3) * 32 >= it.rows;
             const int seen = min(lim, it.end_of(wg));           // (dummy rows too stop at the tile's end)
             // TREE: the nodes the row sees (dummy rows: all), none after its own nor of a position below 0
             const int past = it.L - it.n;
@@ -1580,8 +1560,8 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
     }
 }
 
-// Whether no tree of the call has more than a tile of rows of a KV head, so that their tiles are taken one by one: the same
-// in every CTA.  The query starts alone decide: padding rows behind the last tree and sequences without nodes count for
+// Whether no tree of the call has more than a tile of rows of a KV head, so that every item is a single one: the same in
+// every CTA.  The query starts alone decide: padding rows behind the last tree and sequences without nodes count for
 // nothing, and a replayed graph goes by its own trees.  Looking takes 1 us.
 __device__ __forceinline__ bool lone_trees(const PrefillArgs& a) {
     if (a.lone_nodes >= kTreeNodes) return true;
