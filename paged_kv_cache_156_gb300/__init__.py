@@ -306,7 +306,8 @@ def paged_kv_append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping,
                 return _check(load().pkv_paged_kv_append_rotary(
                     q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                     slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T,
-                    *((os_[0], qs[0], ks[0], vs[0]) if T > 1 else (rows[1] * d, rows[1] * d, h * d, h * d)), *cos_sin.shape, 1 if interleaved else 0, pool[0], pool[1], rows[1], h, d, _DT[kdt], _POOL_DT[dt],
+                    *((os_[0], qs[0], ks[0], vs[0]) if T > 1 else (rows[1] * d, rows[1] * d, h * d, h * d)), *cos_sin.shape,
+                    1 if interleaved else 0, pool[0], pool[1], rows[1], h, d, _DT[kdt], _POOL_DT[dt],
                     k_scale.data_ptr() if kv8 else None, v_scale.data_ptr() if kv8 else None, _stream(key_cache)))
     _append_rotary(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, cos_sin, interleaved, k_scale, v_scale)
 
@@ -935,8 +936,8 @@ def _keep_path(key_caches, value_caches, block_tables, seq_lens, query_starts, p
     karr = (ctypes.c_void_p * n)(*[kc.data_ptr() for kc in key_caches])
     varr = (ctypes.c_void_p * n)(*[vc.data_ptr() for vc in value_caches])
     NB, bs, Hkv, d = shape
-    _check(load().pkv_paged_kv_keep_path(ctypes.addressof(karr), ctypes.addressof(varr), n, args[0], block_tables.shape[1], *args[1:], B, W, NB, bs, Hkv, d,
-                                         _POOL_DT[dt], _stream(key_caches[0])))
+    _check(load().pkv_paged_kv_keep_path(ctypes.addressof(karr), ctypes.addressof(varr), n, args[0], block_tables.shape[1],
+                                         *args[1:], B, W, NB, bs, Hkv, d, _POOL_DT[dt], _stream(key_caches[0])))
 
 
 @_one_device
