@@ -72,13 +72,16 @@
 // trees of 16 over 512 to 4096 positions, 32 heads over 8: 98.5 us, 5.6 TB/s (steps at
 // the HBM rate, 1.5 us; start-up 9 us; blocks read once leave L2 first, 102 without);
 // 128 ragged trees of 1 to 64, 64 heads over 8: 156 us, where a step of two tiles takes
-// 1.72 us from HBM and an item 3.4 us beside.
-// Over E4M3 pools, trees of up to 128 rows (LONE): a lone tile would leave half the
-// softmax warps idle, so four of them expand codes too (eight in all, one trip a tile)
-// and S of the next step runs under the softmax, in the other tile's columns: 64 trees
-// of 26, 115 to 102 us.  What bounds that form is the softmax of one warpgroup, a warp
-// a scheduler (1.35 us a step; 94 us in all without the expansion, 96 without the
-// exponentials).  Two warpgroups on even and odd steps, 640 threads, took 111 to 125.
+// 1.72 us from HBM and an item 3.4 us beside.  At head_dim 64 the first batch takes
+// 74 us, 54% of the HBM rate: 0.9 us a step, the chain of a lone tile's S, softmax, P V.
+// Over E4M3 pools: 64 trees of 60, 149 us, two tiles, whose steps the expansion sets
+// (1.7 us).  Where no tree of the batch has more than 128 rows (LONE), the second tile's
+// softmax warps would be idle, so they expand codes too (eight warps in all, one trip a
+// tile) and S of the next step runs under the softmax, in the other tile's columns: 64
+// trees of 26, 115 to 101 us, 1.35 us a step.  No pipe is full there and no one part is
+// the bound: without the expansion 94 us, without the exponentials 96, without the first
+// pass over S 91, without its wait for the last P V where nothing is rescaled 102.  Two
+// warpgroups on even and odd steps, 640 threads, took 111 to 125.
 //
 // Every wait is bounded in wall time; a CTA that gives up raises the error
 // word, gives its copies and products in flight time to land and frees its TMEM.
@@ -1358,7 +1361,8 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap& tmq, const CUtens
                     m_ref = top;
                 }
                 if constexpr (G::kOwnP || LONE) {
-                    // the last step's O product reads P's columns (kOwnP) and writes O
+                    // the last step's O product reads P's columns (kOwnP) and writes O (LONE: only a warp that rescales
+                    // O has to wait, but with the wait in such warps alone 64 trees of 26 took 102.3 us instead of 101.1)
                     if (j > 0) {
                         ok = wait_bar(&o_step[wg], nstep & 1, abort_flag);
                         ok = __all_sync(0xffffffffu, ok);
