@@ -60,6 +60,11 @@ constexpr int kBatch = 4;                           // groups of 128 weights who
 __host__ __device__ constexpr int batches_of(int weights, int cluster) {
     return (weights + cluster * kWarps * kBatch * 128 - 1) / (cluster * kWarps * kBatch * 128);
 }
+// Batches of a warp at most, and of them those that come by way of shared memory (one CTA's rows have no fourth batch).
+__host__ __device__ constexpr int max_batches(int cluster) {
+    return batches_of((cluster == 1 ? kSmallVocab : PKV_ACCEPT_MAX_VOCAB) + 3, cluster);
+}
+__host__ __device__ constexpr int late_batches(int cluster) { return max_batches(cluster) >= 4 ? 2 : 0; }
 constexpr int kNodes = PKV_TREE_MAX_NODES;
 static_assert(kNodes == 64, "a warp looks the children up two nodes a lane");
 
@@ -77,7 +82,7 @@ __device__ __forceinline__ unsigned long long warp_units(uint32_t hi, uint32_t l
 
 template <typename T, int kCluster>
 __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTreeArgs a) {
-    constexpr int kMaxBatches = batches_of((kCluster == 1 ? kSmallVocab : PKV_ACCEPT_MAX_VOCAB) + 3, kCluster);
+    constexpr int kMaxBatches = max_batches(kCluster);
     static_assert(kMaxBatches <= 32, "a batch a lane");
     __shared__ unsigned long long warp_total[kWarps];
     // (two of each, for the rows in turn: a CTA may still read a row's when another writes the next one's)
@@ -91,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTr
     // a thread's own places: the vectors of two batches, and of a child's
     extern __shared__ __align__(16) uint8_t dynamic[];
     Vector* later = reinterpret_cast<Vector*>(dynamic);
-    Vector* kid_batch = later + 2 * kBatch * kThreads;
+    Vector* kid_batch = later + late_batches(kCluster) * kBatch * kThreads;
     __shared__ int s_parent[kNodes];
     __shared__ int s_draft[kNodes];
     __shared__ int s_owner[kNodes];                           // the warp of the cluster whose piece of the parent's row holds it
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTr
 
         // The third and fourth batch come by way of shared memory, so that four are in flight (128000 float32 tokens: all),
         // where the first four are whole: the pass below then always takes them up.
-        const bool more = batches >= 4 && inside(0) && inside(3);
+        const bool more = late_batches(kCluster) && batches >= 4 && inside(0) && inside(3);
         if (more) {
 #pragma unroll
             for (int k = 0; k < 2 * kBatch; ++k)
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 4) accept_tree_kernel(const AcceptTr
 
 template <typename T, int kCluster>
 cudaError_t launch(const AcceptTreeArgs& a, cudaStream_t s) {
-    constexpr int kShared = 3 * kBatch * kThreads * 4 * sizeof(T);
+    constexpr int kShared = (late_batches(kCluster) + 1) * kBatch * kThreads * 4 * sizeof(T);
     static std::atomic<uint64_t> ready{0};          // devices on which the kernel may take that much
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
